@@ -11,6 +11,7 @@ import re
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "moe.h")
+BLOCK_HEADER = os.path.join(os.path.dirname(_HERE), "include", "moe_block.h")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = range(5)
 
@@ -65,6 +66,13 @@ SIGNATURES = {
     "moe_swiglu_backward": (I, [P, P, P, P, I, I, I, P, P, P, P, P, P, P]),
     "grouped_gemm_fp8_wgrad": (I, [P, P, P, P, P, I, I, I, I, P, P]),
     "grouped_gemm_fp8_up_train": (I, [P, P, I, P, P, I, I, I, I, P, P, P, P, P, P, P]),
+    "moe_rmsnorm_quant": (I, [P, P, P, I, I, ctypes.c_float, P, P, P, P, P, P]),
+    "moe_rmsnorm_quant_pow2": (I, [P, P, P, I, I, ctypes.c_float, P, P, P, P, P, P]),
+    "moe_rmsnorm_backward_workspace_bytes": (SZ, [I, I]),
+    "moe_rmsnorm_backward": (I, [P, P, P, P, P, I, I, P, P, P, SZ, P]),
+    "moe_grad_norm_workspace_bytes": (SZ, [I]),
+    "moe_grad_norm": (I, [P, P, P, I, ctypes.c_float, P, P, P, SZ, P]),
+    "moe_grad_scale": (I, [P, P, P, P, I, P, P]),
     "moe_status_string": (ctypes.c_char_p, [I]),
     "moe_last_error": (ctypes.c_char_p, []),
 }
@@ -94,9 +102,9 @@ def check(fn_name, status):
         raise MoEError(fn_name, status, msg)
 
 
-def header_symbols():
-    """Function names declared in include/moe.h."""
-    with open(HEADER) as f:
+def header_symbols(path=HEADER):
+    """Function names declared in a header of include/ (moe.h by default)."""
+    with open(path) as f:
         text = f.read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     return sorted(set(re.findall(r"\b(?:moe_status|size_t|int|const char\*)\s+(\w+)\s*\(", text)))

@@ -4,78 +4,15 @@
 #include <hip/hip_runtime.h>
 
 #include <cmath>
-#include <cstdarg>
 #include <cstdint>
-#include <cstdio>
 
+#include "check.h"
 #include "kernels.h"
 #include "moe.h"
 
-namespace {
-
+namespace moe {
 thread_local char g_err[512];
-
-moe_status fail(moe_status s, const char* fmt, ...) {
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(g_err, sizeof g_err, fmt, ap);
-  va_end(ap);
-  return s;
 }
-
-void clear_error() { g_err[0] = '\0'; }
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-bool aligned16(const void* p) { return aligned(p, 16); }
-
-moe_status hip_status(hipError_t e, const char* what) {
-  if (e == hipSuccess) return MOE_OK;
-  return fail(MOE_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-}
-
-#define REQUIRE(cond, ...)                                 \
-  do {                                                     \
-    if (!(cond)) return fail(MOE_ERR_INVALID_ARG, __VA_ARGS__); \
-  } while (0)
-
-// Byte and BF16 matrices are accessed with 16-byte vector loads/stores; FP32
-// and int32 arrays element by element.
-#define REQUIRE_PTR_A(p, a)                                                   \
-  do {                                                                        \
-    if ((p) == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s is NULL", #p);   \
-    if (!aligned((p), (a)))                                                   \
-      return fail(MOE_ERR_INVALID_ARG, "%s is not %d-byte aligned", #p, (int)(a)); \
-  } while (0)
-#define REQUIRE_PTR(p) REQUIRE_PTR_A(p, 16)
-#define REQUIRE_PTR4(p) REQUIRE_PTR_A(p, 4)
-
-#define REQUIRE_ALIGNED4_OR_NULL(p)                                           \
-  do {                                                                        \
-    if ((p) != nullptr && !aligned((p), 4))                                   \
-      return fail(MOE_ERR_INVALID_ARG, "%s is not 4-byte aligned", #p);       \
-  } while (0)
-
-moe_status check_route_params(const moe_route_params& p) {
-  REQUIRE(p.n_experts >= 1 && p.n_experts <= 256, "n_experts=%d must be in [1, 256]", p.n_experts);
-  REQUIRE(p.n_groups >= 1 && p.n_groups <= 64, "n_groups=%d must be in [1, 64]", p.n_groups);
-  REQUIRE(p.n_experts % p.n_groups == 0, "n_experts=%d is not a multiple of n_groups=%d",
-          p.n_experts, p.n_groups);
-  REQUIRE(p.topk_groups >= 1 && p.topk_groups <= p.n_groups, "topk_groups=%d must be in [1, %d]",
-          p.topk_groups, p.n_groups);
-  REQUIRE(p.topk >= 1, "topk=%d must be >= 1", p.topk);
-  REQUIRE(p.topk % p.topk_groups == 0, "topk=%d is not a multiple of topk_groups=%d", p.topk,
-          p.topk_groups);
-  const int per = p.n_experts / p.n_groups;
-  REQUIRE(p.topk / p.topk_groups <= per, "topk/topk_groups=%d exceeds the %d experts of a group",
-          p.topk / p.topk_groups, per);
-  REQUIRE(p.topk <= p.topk_groups * per, "topk=%d exceeds the %d experts of the kept groups",
-          p.topk, p.topk_groups * per);
-  REQUIRE(std::isfinite(p.route_scale), "route_scale is not finite");
-  if (p.topk > 16) return fail(MOE_ERR_UNSUPPORTED, "topk=%d > 16 is not implemented", p.topk);
-  return MOE_OK;
-}
-
-}  // namespace
 
 extern "C" {
 
@@ -90,7 +27,7 @@ const char* moe_status_string(moe_status s) {
   return "MOE_ERR_UNKNOWN";
 }
 
-const char* moe_last_error(void) { return g_err; }
+const char* moe_last_error(void) { return moe::g_err; }
 
 moe_status moe_route(const uint16_t* x, const uint16_t* wg, const float* bias, int T, int d,
                      moe_route_params p, int32_t* idx, float* w, void* stream) {

@@ -1,0 +1,183 @@
+// C ABI of include/moe_block.h: host-side validation, then launches on the
+// caller's stream, as api.cpp does for moe.h.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <utility>
+#include <vector>
+
+#include "check.h"
+#include "kernels.h"
+#include "moe_block.h"
+
+namespace {
+
+moe_status check_norm_shape(int T, int d) {
+  REQUIRE(T >= 0, "T=%d is negative", T);
+  REQUIRE(d >= 128 && d % 128 == 0, "d=%d must be a positive multiple of 128", d);
+  if (d > moe::kNormMaxD) return fail(MOE_ERR_UNSUPPORTED, "d=%d > %d is not implemented", d, moe::kNormMaxD);
+  return MOE_OK;
+}
+
+#define REQUIRE_ALIGNED_OR_NULL(p)                                                                          \
+  do {                                                                                                      \
+    if ((p) != nullptr && !aligned16(p)) return fail(MOE_ERR_INVALID_ARG, "%s is not 16-byte aligned", #p); \
+  } while (0)
+
+moe_status rmsnorm_impl(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int T, int d, float eps,
+                        uint16_t* sum, uint16_t* y, uint8_t* q, float* scale, float* rstd, bool pow2, void* stream) {
+  moe_status s = check_norm_shape(T, d);
+  if (s != MOE_OK) return s;
+  REQUIRE(std::isfinite(eps) && eps > 0.0f, "eps=%g must be positive and finite", (double)eps);
+  REQUIRE((q == nullptr) == (scale == nullptr), "q and scale must be given together");
+  if (T == 0) return MOE_OK;
+  REQUIRE(sum != nullptr || y != nullptr || q != nullptr || rstd != nullptr, "no output is given");
+  REQUIRE_PTR(x);
+  REQUIRE_ALIGNED_OR_NULL(residual);
+  REQUIRE_PTR(weight);
+  REQUIRE_ALIGNED_OR_NULL(sum);
+  REQUIRE_ALIGNED_OR_NULL(y);
+  REQUIRE_ALIGNED_OR_NULL(q);
+  REQUIRE_ALIGNED4_OR_NULL(scale);
+  REQUIRE_ALIGNED4_OR_NULL(rstd);
+  REQUIRE(y == nullptr || (y != sum && y != x && y != residual), "y must not be another operand's memory");
+  return hip_status(moe::launch_rmsnorm_quant(x, residual, weight, T, d, eps, sum, y, q, scale, rstd, pow2,
+                                              static_cast<hipStream_t>(stream)),
+                    pow2 ? "moe_rmsnorm_quant_pow2 launch" : "moe_rmsnorm_quant launch");
+}
+
+size_t rmsnorm_backward_bytes(int T, int d) {
+  if (T <= 0 || d < 128 || d % 128 != 0 || d > moe::kNormMaxD) return 0;
+  return (size_t)moe::rmsnorm_backward_groups(T, d) * d * sizeof(float);
+}
+
+moe_status check_grads(const void* const* grads, const int64_t* sizes, const int* types, int n_tensors) {
+  REQUIRE(n_tensors >= 0, "n_tensors=%d is negative", n_tensors);
+  if (n_tensors == 0) return MOE_OK;
+  REQUIRE(grads != nullptr, "grads is NULL");
+  REQUIRE(sizes != nullptr, "sizes is NULL");
+  REQUIRE(types != nullptr, "types is NULL");
+  for (int i = 0; i < n_tensors; ++i) {
+    REQUIRE(sizes[i] >= 0 && sizes[i] <= (INT64_C(1) << 40), "sizes[%d]=%lld must be in [0, 2^40]", i,
+            (long long)sizes[i]);
+    REQUIRE(types[i] == MOE_GRAD_FP32 || types[i] == MOE_GRAD_BF16, "types[%d]=%d is not a moe_grad_type", i,
+            types[i]);
+    if (sizes[i] == 0) continue;
+    REQUIRE(grads[i] != nullptr, "grads[%d] is NULL", i);
+    REQUIRE(aligned(grads[i], types[i] == MOE_GRAD_FP32 ? 4 : 2), "grads[%d] is not aligned to its elements", i);
+  }
+  return MOE_OK;
+}
+
+// No two outputs share memory (a tensor listed twice would be scaled twice).
+moe_status check_disjoint(void* const* outs, const int64_t* sizes, const int* types, int n_tensors) {
+  try {
+    std::vector<std::pair<uintptr_t, uintptr_t>> at;
+    at.reserve(n_tensors);
+    for (int i = 0; i < n_tensors; ++i) {
+      if (sizes[i] == 0) continue;
+      const uintptr_t o = reinterpret_cast<uintptr_t>(outs[i]);
+      at.emplace_back(o, o + (uint64_t)sizes[i] * (types[i] == MOE_GRAD_FP32 ? 4 : 2));
+    }
+    std::sort(at.begin(), at.end());
+    for (size_t i = 1; i < at.size(); ++i) REQUIRE(at[i - 1].second <= at[i].first, "two outputs overlap");
+  } catch (...) {
+    return fail(MOE_ERR_INVALID_ARG, "n_tensors=%d: out of host memory", n_tensors);
+  }
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_rmsnorm_quant(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int T, int d,
+                             float eps, uint16_t* sum, uint16_t* y, uint8_t* q, float* scale, float* rstd,
+                             void* stream) {
+  clear_error();
+  return rmsnorm_impl(x, residual, weight, T, d, eps, sum, y, q, scale, rstd, false, stream);
+}
+
+moe_status moe_rmsnorm_quant_pow2(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int T, int d,
+                                  float eps, uint16_t* sum, uint16_t* y, uint8_t* q, float* scale, float* rstd,
+                                  void* stream) {
+  clear_error();
+  return rmsnorm_impl(x, residual, weight, T, d, eps, sum, y, q, scale, rstd, true, stream);
+}
+
+size_t moe_rmsnorm_backward_workspace_bytes(int T, int d) { return rmsnorm_backward_bytes(T, d); }
+
+moe_status moe_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const uint16_t* weight, const float* rstd,
+                                const uint16_t* dres, int T, int d, uint16_t* dh, float* dweight, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  clear_error();
+  moe_status s = check_norm_shape(T, d);
+  if (s != MOE_OK) return s;
+  REQUIRE_PTR4(dweight);
+  if (T > 0) {
+    REQUIRE_PTR(dy);
+    REQUIRE_PTR(h);
+    REQUIRE_PTR(weight);
+    REQUIRE_PTR4(rstd);
+    REQUIRE_ALIGNED_OR_NULL(dres);
+    REQUIRE_PTR(dh);
+    REQUIRE(dh != dy && dh != h, "dh must not be dy's or h's memory");
+    const size_t need = rmsnorm_backward_bytes(T, d);
+    if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need)
+      return fail(MOE_ERR_WORKSPACE, "workspace %p of %zu bytes: %zu bytes, 16-byte aligned, needed", workspace,
+                  workspace_bytes, need);
+  }
+  return hip_status(moe::launch_rmsnorm_backward(dy, h, weight, rstd, dres, T, d, dh, dweight,
+                                                 static_cast<float*>(workspace), static_cast<hipStream_t>(stream)),
+                    "moe_rmsnorm_backward launch");
+}
+
+size_t moe_grad_norm_workspace_bytes(int n_tensors) {
+  return n_tensors <= 0 ? 0 : moe::grad_norm_workspace_bytes(n_tensors);
+}
+
+moe_status moe_grad_norm(const void* const* grads, const int64_t* sizes, const int* types, int n_tensors,
+                         float max_norm, float* norm, float* coef, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  clear_error();
+  moe_status s = check_grads(grads, sizes, types, n_tensors);
+  if (s != MOE_OK) return s;
+  REQUIRE(max_norm > 0.0f, "max_norm=%g must be positive", (double)max_norm);
+  REQUIRE_PTR4(norm);
+  REQUIRE_PTR4(coef);
+  const size_t need = moe_grad_norm_workspace_bytes(n_tensors);
+  if (need > 0 && (workspace == nullptr || !aligned(workspace, 8) || workspace_bytes < need))
+    return fail(MOE_ERR_WORKSPACE, "workspace %p of %zu bytes: %zu bytes, 8-byte aligned, needed", workspace,
+                workspace_bytes, need);
+  return hip_status(moe::launch_grad_norm(grads, sizes, types, n_tensors, max_norm, norm, coef,
+                                          static_cast<double*>(workspace), static_cast<hipStream_t>(stream)),
+                    "moe_grad_norm launch");
+}
+
+moe_status moe_grad_scale(const void* const* grads, void* const* outs, const int64_t* sizes, const int* types,
+                          int n_tensors, const float* coef, void* stream) {
+  clear_error();
+  moe_status s = check_grads(grads, sizes, types, n_tensors);
+  if (s != MOE_OK) return s;
+  REQUIRE_PTR4(coef);
+  if (n_tensors == 0) return MOE_OK;
+  REQUIRE(outs != nullptr, "outs is NULL");
+  for (int i = 0; i < n_tensors; ++i) {
+    if (sizes[i] == 0) continue;
+    REQUIRE(outs[i] != nullptr, "outs[%d] is NULL", i);
+    const uint64_t width = types[i] == MOE_GRAD_FP32 ? 4 : 2;
+    REQUIRE(aligned(outs[i], width), "outs[%d] is not aligned to its elements", i);
+    const uintptr_t g = reinterpret_cast<uintptr_t>(grads[i]), o = reinterpret_cast<uintptr_t>(outs[i]);
+    const uint64_t bytes = (uint64_t)sizes[i] * width;
+    REQUIRE(g == o || g + bytes <= o || o + bytes <= g, "outs[%d] overlaps grads[%d] in part", i, i);
+  }
+  s = check_disjoint(outs, sizes, types, n_tensors);
+  if (s != MOE_OK) return s;
+  return hip_status(moe::launch_grad_scale(grads, outs, sizes, types, n_tensors, coef,
+                                           static_cast<hipStream_t>(stream)),
+                    "moe_grad_scale launch");
+}
+
+}  // extern "C"

@@ -1,0 +1,266 @@
+// Global gradient norm over a list of tensors, and the scaling that clips them.
+//
+//   N = sqrt(sum over tensors and elements of g^2)   FP64, rounded once to FP32
+//   c = 1 if N <= max_norm, else max_norm / N        FP64, rounded once to FP32
+//   out = g c                                        FP32 product, rounded to g's type
+//
+// An FP32 square has 48 bits and so is exact in FP64; the sum runs there too:
+// squares neither overflow nor vanish, and 10^10 of them lose nothing that the
+// FP32 result would show.  The FP64 units take 32 elements per clock and CU
+// (a conversion and a multiply-add each), ten times what memory delivers.
+//
+// Tensor addresses and sizes travel in the kernel arguments, kGradBatch tensors
+// per launch, so a call needs no table in device memory and can be captured.
+// The tensors of a launch are cut into chunks of kGradChunk elements dealt to
+// the workgroups in turn; a workgroup's partial sum depends only on the sizes
+// and addresses' alignment, and the partials are added in a fixed order, so
+// equal inputs give equal bits.
+#include <algorithm>
+
+#include "common.h"
+#include "kernels.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kGradBatch = 64;            // tensors per launch
+constexpr int kGradChunk = 8192;          // elements per chunk
+constexpr int kGradGroups = 2048;         // most workgroups of a launch, partials per launch
+constexpr int kGradThreads = 256;
+
+struct GradList {
+  const void* g[kGradBatch];
+  void* out[kGradBatch];
+  int64_t n[kGradBatch];
+  int64_t chunk0[kGradBatch + 1];         // first chunk of each tensor
+  uint64_t bf16;                          // bit i: tensor i is BF16
+  int count;
+};
+
+__device__ __forceinline__ int tensor_of(const GradList& L, int64_t chunk) {
+  int a = 0, b = L.count - 1;
+  while (a < b) {
+    const int mid = (a + b + 1) >> 1;
+    if (L.chunk0[mid] <= chunk) a = mid; else b = mid - 1;
+  }
+  return a;
+}
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+template <typename V>
+struct Elem;
+template <>
+struct Elem<float> {
+  static constexpr int kVec = 4;   // elements of 16 bytes
+  static __device__ __forceinline__ float get(float v) { return v; }
+  static __device__ __forceinline__ float put(float v) { return v; }
+  static __device__ __forceinline__ void unpack(const u32x4& u, float (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(u[i]);
+  }
+  static __device__ __forceinline__ u32x4 scale(const u32x4& u, float c) {
+    u32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = __float_as_uint(__uint_as_float(u[i]) * c);
+    return r;
+  }
+};
+// Round to nearest even, keeping NaN a NaN and infinities (gradients may hold
+// either; the caller reads them off the norm).
+__device__ __forceinline__ uint16_t grad_bf16(float f) {
+  return f != f ? (uint16_t)0x7FC0 : f32_to_bf16(f);
+}
+template <>
+struct Elem<uint16_t> {
+  static constexpr int kVec = 8;
+  static __device__ __forceinline__ float get(uint16_t v) { return bf16_to_f32(v); }
+  static __device__ __forceinline__ uint16_t put(float v) { return grad_bf16(v); }
+  static __device__ __forceinline__ void unpack(const u32x4& u, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+  }
+  static __device__ __forceinline__ u32x4 scale(const u32x4& u, float c) {
+    u32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      r[i] = (uint32_t)grad_bf16(__uint_as_float(u[i] << 16) * c) |
+             ((uint32_t)grad_bf16(__uint_as_float(u[i] & 0xFFFF0000u) * c) << 16);
+    return r;
+  }
+};
+
+// Elements before the first 16-byte boundary of p (at most n).
+template <typename V>
+__device__ __forceinline__ int head_of(const V* p, int n) {
+  return min((int)(((16u - ((uint32_t)(uintptr_t)p & 15u)) & 15u) / sizeof(V)), n);
+}
+
+// Sum of squares of chunk elements [0, n): a scalar head up to a 16-byte
+// boundary, 16-byte loads, a scalar tail.
+template <typename V>
+__device__ __forceinline__ double chunk_squares(const V* __restrict__ p, int n) {
+  constexpr int kVec = Elem<V>::kVec;
+  double s = 0.0;
+  const int head = head_of(p, n);
+  if ((int)threadIdx.x < head) {
+    const double v = Elem<V>::get(p[threadIdx.x]);
+    s = v * v;
+  }
+  const int nv = (n - head) / kVec;
+  const u32x4* vp = reinterpret_cast<const u32x4*>(p + head);
+#pragma unroll 4
+  for (int i = threadIdx.x; i < nv; i += kGradThreads) {
+    float v[kVec];
+    Elem<V>::unpack(vp[i], v);
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) s = fma((double)v[j], (double)v[j], s);
+  }
+  for (int i = head + nv * kVec + threadIdx.x; i < n; i += kGradThreads) {
+    const double v = Elem<V>::get(p[i]);
+    s = fma(v, v, s);
+  }
+  return s;
+}
+
+__device__ __forceinline__ double block_sum(double v) {
+  __shared__ double red[kGradThreads / 64];
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  double s = red[0];
+#pragma unroll
+  for (int i = 1; i < kGradThreads / 64; ++i) s += red[i];
+  return s;
+}
+
+__global__ __launch_bounds__(kGradThreads) void grad_squares_kernel(const GradList L, double* __restrict__ partial) {
+  double s = 0.0;
+  const int64_t total = L.chunk0[L.count];
+  for (int64_t c = blockIdx.x; c < total; c += gridDim.x) {
+    const int t = tensor_of(L, c);
+    const int64_t e0 = (c - L.chunk0[t]) * kGradChunk;
+    const int n = (int)min((int64_t)kGradChunk, L.n[t] - e0);
+    if ((L.bf16 >> t) & 1)
+      s += chunk_squares(static_cast<const uint16_t*>(L.g[t]) + e0, n);
+    else
+      s += chunk_squares(static_cast<const float*>(L.g[t]) + e0, n);
+  }
+  s = block_sum(s);
+  if (threadIdx.x == 0) partial[blockIdx.x] = s;
+}
+
+__global__ __launch_bounds__(kGradThreads) void grad_norm_kernel(const double* __restrict__ partial, int n,
+                                                                 float max_norm, float* __restrict__ norm,
+                                                                 float* __restrict__ coef) {
+  double s = 0.0;
+  for (int i = threadIdx.x; i < n; i += kGradThreads) s += partial[i];
+  s = block_sum(s);
+  if (threadIdx.x == 0) {
+    const double r = sqrt(s);
+    *norm = (float)r;
+    *coef = r <= (double)max_norm ? 1.0f : (float)((double)max_norm / r);
+  }
+}
+
+// out = g c over a chunk.  The 16-byte form needs g and out equally far from a
+// boundary; otherwise element by element.
+template <typename V>
+__device__ __forceinline__ void chunk_scale(const V* g, V* out, int n, float c) {
+  constexpr int kVec = Elem<V>::kVec;
+  const bool together = (((uintptr_t)g ^ (uintptr_t)out) & 15u) == 0;
+  const int head = together ? head_of(g, n) : n;
+  for (int i = threadIdx.x; i < head; i += kGradThreads) out[i] = Elem<V>::put(Elem<V>::get(g[i]) * c);
+  const int nv = (n - head) / kVec;
+  const u32x4* gp = reinterpret_cast<const u32x4*>(g + head);
+  u32x4* op = reinterpret_cast<u32x4*>(out + head);
+  // four loads ahead of their stores (out may be g: a thread writes only what it has read)
+  for (int i = threadIdx.x; i < nv; i += 4 * kGradThreads) {
+    u32x4 u[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + j * kGradThreads < nv) u[j] = gp[i + j * kGradThreads];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + j * kGradThreads < nv) op[i + j * kGradThreads] = Elem<V>::scale(u[j], c);
+  }
+  for (int i = head + nv * kVec + threadIdx.x; i < n; i += kGradThreads) out[i] = Elem<V>::put(Elem<V>::get(g[i]) * c);
+}
+
+__global__ __launch_bounds__(kGradThreads) void grad_scale_kernel(const GradList L, const float* __restrict__ coef) {
+  const float c = *coef;
+  const int64_t total = L.chunk0[L.count];
+  for (int64_t k = blockIdx.x; k < total; k += gridDim.x) {
+    const int t = tensor_of(L, k);
+    if (c == 1.0f && L.g[t] == L.out[t]) continue;   // in place and below the limit: nothing changes
+    const int64_t e0 = (k - L.chunk0[t]) * kGradChunk;
+    const int n = (int)min((int64_t)kGradChunk, L.n[t] - e0);
+    if ((L.bf16 >> t) & 1)
+      chunk_scale(static_cast<const uint16_t*>(L.g[t]) + e0, static_cast<uint16_t*>(L.out[t]) + e0, n, c);
+    else
+      chunk_scale(static_cast<const float*>(L.g[t]) + e0, static_cast<float*>(L.out[t]) + e0, n, c);
+  }
+}
+
+// Fills L with the next non-empty tensors from i on; returns the first index
+// not taken.
+int fill_list(GradList& L, const void* const* grads, void* const* outs, const int64_t* sizes, const int* types,
+              int n_tensors, int i) {
+  L.count = 0;
+  L.bf16 = 0;
+  L.chunk0[0] = 0;
+  for (; i < n_tensors && L.count < kGradBatch; ++i) {
+    if (sizes[i] == 0) continue;
+    const int k = L.count++;
+    L.g[k] = grads[i];
+    L.out[k] = outs ? outs[i] : nullptr;
+    L.n[k] = sizes[i];
+    L.chunk0[k + 1] = L.chunk0[k] + (sizes[i] + kGradChunk - 1) / kGradChunk;
+    if (types[i] == 1) L.bf16 |= 1ull << k;
+  }
+  return i;
+}
+
+}  // namespace
+
+size_t grad_norm_workspace_bytes(int n_tensors) {
+  return (size_t)((n_tensors + kGradBatch - 1) / kGradBatch) * kGradGroups * sizeof(double);
+}
+
+hipError_t launch_grad_norm(const void* const* grads, const int64_t* sizes, const int* types, int n_tensors,
+                            float max_norm, float* norm, float* coef, double* partial, hipStream_t stream) {
+  GradList L;
+  int used = 0;
+  for (int i = 0; i < n_tensors;) {
+    i = fill_list(L, grads, nullptr, sizes, types, n_tensors, i);
+    if (L.count == 0) break;
+    const int groups = (int)std::min<int64_t>(kGradGroups, L.chunk0[L.count]);
+    hipLaunchKernelGGL(grad_squares_kernel, dim3(groups), dim3(kGradThreads), 0, stream, L, partial + used);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    used += groups;
+  }
+  hipLaunchKernelGGL(grad_norm_kernel, dim3(1), dim3(kGradThreads), 0, stream, partial, used, max_norm, norm, coef);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_scale(const void* const* grads, void* const* outs, const int64_t* sizes, const int* types,
+                             int n_tensors, const float* coef, hipStream_t stream) {
+  GradList L;
+  for (int i = 0; i < n_tensors;) {
+    i = fill_list(L, grads, outs, sizes, types, n_tensors, i);
+    if (L.count == 0) break;
+    const int groups = (int)std::min<int64_t>(2 * kGradGroups, L.chunk0[L.count]);
+    hipLaunchKernelGGL(grad_scale_kernel, dim3(groups), dim3(kGradThreads), 0, stream, L, coef);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace moe

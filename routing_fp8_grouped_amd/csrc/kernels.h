@@ -83,6 +83,24 @@ hipError_t launch_combine(const uint16_t* y, const int32_t* pos, const float* w,
                           int d, int shared_row0, const uint16_t* residual, uint16_t* out,
                           hipStream_t stream);
 
+// Residual addition + RMS norm + 1x128 quantisation, and its backward
+// (norm.hip).  kNormMaxD: the widest row a workgroup holds in registers.
+constexpr int kNormMaxD = 16384;
+hipError_t launch_rmsnorm_quant(const uint16_t* x, const uint16_t* res, const uint16_t* w, int T, int d, float eps,
+                                uint16_t* sum, uint16_t* y, uint8_t* q, float* scale, float* rstd, bool pow2,
+                                hipStream_t stream);
+int rmsnorm_backward_groups(int T, int d);
+hipError_t launch_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const uint16_t* w, const float* rstd,
+                                   const uint16_t* dres, int T, int d, uint16_t* dh, float* dw, float* partial,
+                                   hipStream_t stream);
+
+// Global gradient norm and scaling over lists of tensors (grad.hip).
+size_t grad_norm_workspace_bytes(int n_tensors);
+hipError_t launch_grad_norm(const void* const* grads, const int64_t* sizes, const int* types, int n_tensors,
+                            float max_norm, float* norm, float* coef, double* partial, hipStream_t stream);
+hipError_t launch_grad_scale(const void* const* grads, void* const* outs, const int64_t* sizes, const int* types,
+                             int n_tensors, const float* coef, hipStream_t stream);
+
 // Measured roofs (roofs.hip): FP8 MFMA issue rate and HBM read streaming.
 hipError_t launch_roof_mfma(int workgroups, int iters, float* sink, hipStream_t stream);
 hipError_t launch_roof_dma(const void* buf, size_t bytes, int K, int ahead, int workgroups, uint32_t* sink,

@@ -1,0 +1,353 @@
+// Residual addition, RMS norm and FP8 quantisation in front of the layer, and
+// the norm's backward.
+//
+// Forward, per row of d elements (all rounding steps in this order):
+//   h    = bf16(x + r)                 (h = x without a residual)
+//   rstd = fl32(1 / sqrt(sum h^2 / d + eps))   sum, quotient and root in FP64
+//   y    = bf16(fl32(fl32(h * rstd) * w))
+//   s, q = the 1x128 tiles of y, as fp8_quant_1x128 makes them
+// A BF16 square is exact in FP64 and the sum's error is below 2^-50 relative,
+// so rstd, and with it every output, does not depend on how a row is split
+// over threads (up to a sum within that distance of an FP32 rounding border).
+// The FP64 work, one conversion and one multiply-add per element, hides behind
+// the memory traffic: 9 bytes per element with a residual.
+//
+// Backward, with xh = h rstd, g = dy w:
+//   c  = sum(g xh) / d
+//   dh = bf16(rstd (g - xh c) + dres),  dw = sum over rows of dy xh
+// in FP32 products; c and the rows' sums are FP32 trees, dw's partial sums per
+// workgroup FP32 and their total FP64.  8 bytes per element with dres.
+//
+// Both are HBM-bound.  A row belongs to a team of threads, each holding NC
+// 16-byte chunks in registers between the sum and the second use, so every
+// operand is read once.
+#include <algorithm>
+
+#include "common.h"
+#include "kernels.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int NORM_THREADS = 256;   // wave teams: four rows per workgroup
+
+// ---- team reductions: a wave, or a whole workgroup through LDS ----
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+// Sum over the workgroup's waves in wave order; `buf` alternates between two
+// halves from call to call, so one barrier per call is enough: a wave writes a
+// half again only after the barrier of the call in between, which every wave
+// reaches after it has read that half.
+template <typename V>
+__device__ __forceinline__ V group_sum(V v, V* buf, int waves) {
+  v = wave_sum(v);
+  if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = v;
+  __syncthreads();
+  V s = 0;
+  for (int i = 0; i < waves; ++i) s += buf[i];
+  return s;
+}
+
+__device__ __forceinline__ void unpack8(const uint4& raw, float (&v)[8]) {
+  const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(u[i] << 16);
+    v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) u[i] = (uint32_t)f32_to_bf16(v[2 * i]) | ((uint32_t)f32_to_bf16(v[2 * i + 1]) << 16);
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// Codes of eight elements of a tile with scale s: the correctly rounded
+// quotients, as fp8_quant_1x128 divides.  A power-of-two scale divides by its
+// exact inverse.  Otherwise Divider, whose quotient is correctly rounded while
+// its reciprocal and remainders are normal numbers: with s >= 2^-60 a
+// remainder is too small for that only where the quotient lies below 2^-40,
+// whose code is a zero either way.  Smaller scales take the plain division.
+template <bool POW2>
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float s) {
+  float t[8];
+  if (POW2) {
+    const float r = 1.0f / s;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = v[i] * r;
+  } else if (s >= 0x1p-60f) {
+    const Divider div(s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = div(v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = v[i] / s;
+  }
+  return make_uint2(f32x4_to_e4m3(t[0], t[1], t[2], t[3]), f32x4_to_e4m3(t[4], t[5], t[6], t[7]));
+}
+
+// x and res are read and sum is written at the same places by the same thread,
+// the loads first, so sum may be x's or res's own memory: none is restrict.
+template <int NC, bool WAVE_ROW, bool POW2>
+__global__ __launch_bounds__(WAVE_ROW ? NORM_THREADS : 1024) void rmsnorm_quant_kernel(
+    const uint16_t* x, const uint16_t* res, const uint16_t* __restrict__ w, int T, int d, float eps, uint16_t* sum,
+    uint16_t* __restrict__ y, uint8_t* __restrict__ q, float* __restrict__ scale, float* __restrict__ rstd) {
+  __shared__ double red[2][16];
+  const int team = WAVE_ROW ? 64 : blockDim.x;
+  const int tl = WAVE_ROW ? (threadIdx.x & 63) : threadIdx.x;
+  const int per = WAVE_ROW ? NORM_THREADS / 64 : 1;   // rows per workgroup and step
+  const int chunks = d / 8;
+  int half = 0;
+  for (long row = (long)blockIdx.x * per + (WAVE_ROW ? (threadIdx.x >> 6) : 0); row < T;
+       row += (long)gridDim.x * per) {
+    const size_t base = (size_t)row * d;
+    uint4 h[NC];
+    double part = 0.0;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = tl + i * team;
+      if (c < chunks) h[i] = *reinterpret_cast<const uint4*>(x + base + c * 8);
+    }
+    if (res) {
+      uint4 r[NC];
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int c = tl + i * team;
+        if (c < chunks) r[i] = *reinterpret_cast<const uint4*>(res + base + c * 8);
+      }
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int c = tl + i * team;
+        if (c < chunks) {
+          float a[8], b[8];
+          unpack8(h[i], a);
+          unpack8(r[i], b);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) a[j] += b[j];
+          h[i] = pack8(a);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = tl + i * team;
+      if (c < chunks) {
+        if (sum) *reinterpret_cast<uint4*>(sum + base + c * 8) = h[i];
+        float a[8];
+        unpack8(h[i], a);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) part = fma((double)a[j], (double)a[j], part);
+      }
+    }
+    const double ss = WAVE_ROW ? wave_sum(part) : group_sum(part, red[half], team >> 6);
+    half ^= 1;
+    const float rs = (float)(1.0 / sqrt(ss / d + (double)eps));
+    if (rstd && tl == 0) rstd[row] = rs;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = tl + i * team;
+      if (c < chunks) {   // a 128-wide tile's 16 lanes are all in or all out
+        float a[8], g[8];
+        unpack8(h[i], a);
+        unpack8(*reinterpret_cast<const uint4*>(w + c * 8), g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[j] = (a[j] * rs) * g[j];
+        const uint4 o = pack8(a);
+        if (y) *reinterpret_cast<uint4*>(y + base + c * 8) = o;
+        if (q) {
+          float v[8], amax = 0.0f;
+          unpack8(o, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
+#pragma unroll
+          for (int s2 = 8; s2 > 0; s2 >>= 1) amax = fmaxf(amax, __shfl_xor(amax, s2));
+          const float s = tile_scale<POW2>(amax);
+          *reinterpret_cast<uint2*>(q + base + c * 8) = codes8<POW2>(v, s);
+          if ((c & 15) == 0) scale[(size_t)row * (d / 128) + (c >> 4)] = s;
+        }
+      }
+    }
+  }
+}
+
+// Rows are dealt to the teams in turn; every thread keeps the dw partial sums
+// of its columns over its team's rows.  Workgroup b writes partial[b][0..d).
+template <int NC, bool WAVE_ROW>
+__global__ __launch_bounds__(WAVE_ROW ? NORM_THREADS : 1024) void rmsnorm_backward_kernel(
+    const uint16_t* __restrict__ dy, const uint16_t* __restrict__ h, const uint16_t* __restrict__ w,
+    const float* __restrict__ rstd, const uint16_t* dres, int T, int d, uint16_t* dh, float* __restrict__ partial) {
+  __shared__ float red[2][16];
+  __shared__ float comb[WAVE_ROW ? NORM_THREADS / 64 : 1][WAVE_ROW ? NC * 512 : 1];
+  const int team = WAVE_ROW ? 64 : blockDim.x;
+  const int tl = WAVE_ROW ? (threadIdx.x & 63) : threadIdx.x;
+  const int per = WAVE_ROW ? NORM_THREADS / 64 : 1;
+  const int chunks = d / 8;
+  const float inv_d = 1.0f / d;
+  float acc[NC][8];
+  uint4 wr[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int c = tl + i * team;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
+    wr[i] = c < chunks ? *reinterpret_cast<const uint4*>(w + c * 8) : make_uint4(0, 0, 0, 0);
+  }
+  int half = 0;
+  for (long row = (long)blockIdx.x * per + (WAVE_ROW ? (threadIdx.x >> 6) : 0); row < T;
+       row += (long)gridDim.x * per) {
+    const size_t base = (size_t)row * d;
+    const float rs = rstd[row];
+    uint4 a[NC], b[NC], e[NC];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = tl + i * team;
+      a[i] = b[i] = e[i] = make_uint4(0, 0, 0, 0);
+      if (c < chunks) {
+        a[i] = *reinterpret_cast<const uint4*>(dy + base + c * 8);
+        b[i] = *reinterpret_cast<const uint4*>(h + base + c * 8);
+        if (dres) e[i] = *reinterpret_cast<const uint4*>(dres + base + c * 8);
+      }
+    }
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      float gy[8], hv[8], wv[8];
+      unpack8(a[i], gy);
+      unpack8(b[i], hv);
+      unpack8(wr[i], wv);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float p = gy[j] * (hv[j] * rs);
+        acc[i][j] += p;
+        dot = fmaf(p, wv[j], dot);
+      }
+    }
+    const float c1 = (WAVE_ROW ? wave_sum(dot) : group_sum(dot, red[half], team >> 6)) * inv_d;
+    half ^= 1;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = tl + i * team;
+      if (c < chunks) {
+        float gy[8], hv[8], wv[8], r[8];
+        unpack8(a[i], gy);
+        unpack8(b[i], hv);
+        unpack8(wr[i], wv);
+        unpack8(e[i], r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[j] = fmaf(rs, fmaf(-(hv[j] * rs), c1, gy[j] * wv[j]), r[j]);
+        *reinterpret_cast<uint4*>(dh + base + c * 8) = pack8(r);
+      }
+    }
+  }
+  float* out = partial + (size_t)blockIdx.x * d;
+  if (WAVE_ROW) {
+    float* mine = comb[threadIdx.x >> 6];
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) mine[(tl + i * 64) * 8 + j] = acc[i][j];
+    __syncthreads();
+    for (int c = threadIdx.x; c < d; c += NORM_THREADS) {
+      float s = comb[0][c];
+#pragma unroll
+      for (int v = 1; v < NORM_THREADS / 64; ++v) s += comb[v][c];
+      out[c] = s;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = tl + i * team;
+      if (c < chunks) {
+        *reinterpret_cast<float4*>(out + c * 8) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+        *reinterpret_cast<float4*>(out + c * 8 + 4) = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+      }
+    }
+  }
+}
+
+// dw[c] = sum over n partial rows, FP64, in a fixed order: 16 threads share 16
+// columns' rows (row r to thread r % 16), their sums joined in LDS.
+__global__ __launch_bounds__(1024) void rmsnorm_dw_kernel(const float* __restrict__ partial, int n, int d,
+                                                          float* __restrict__ dw) {
+  __shared__ double s[16][65];
+  const int col = blockIdx.x * 64 + (threadIdx.x & 63), part = threadIdx.x >> 6;
+  double a = 0.0;
+  for (int r = part; r < n; r += 16) a += partial[(size_t)r * d + col];
+  s[part][threadIdx.x & 63] = a;
+  __syncthreads();
+  if (part == 0) {
+#pragma unroll
+    for (int i = 1; i < 16; ++i) a += s[i][threadIdx.x];
+    dw[col] = (float)a;
+  }
+}
+
+// Up to this width a wave owns a row (NC chunks per lane), beyond it a
+// workgroup does (2 chunks per thread).
+constexpr int kWaveRowD = 2048;
+
+int group_threads(int d) { return ((d / 16) + 63) / 64 * 64; }
+
+}  // namespace
+
+hipError_t launch_rmsnorm_quant(const uint16_t* x, const uint16_t* res, const uint16_t* w, int T, int d, float eps,
+                                uint16_t* sum, uint16_t* y, uint8_t* q, float* scale, float* rstd, bool pow2,
+                                hipStream_t stream) {
+#define MOE_NORM(NC, WR, THREADS, ROWS)                                                                             \
+  do {                                                                                                              \
+    const dim3 grid((unsigned)std::min((long)(1 << 20), ((long)T + (ROWS)-1) / (ROWS)));                            \
+    if (pow2)                                                                                                       \
+      hipLaunchKernelGGL((rmsnorm_quant_kernel<NC, WR, true>), grid, dim3(THREADS), 0, stream, x, res, w, T, d,     \
+                         eps, sum, y, q, scale, rstd);                                                              \
+    else                                                                                                            \
+      hipLaunchKernelGGL((rmsnorm_quant_kernel<NC, WR, false>), grid, dim3(THREADS), 0, stream, x, res, w, T, d,    \
+                         eps, sum, y, q, scale, rstd);                                                              \
+  } while (0)
+  if (d <= 512) MOE_NORM(1, true, NORM_THREADS, NORM_THREADS / 64);
+  else if (d <= kWaveRowD) MOE_NORM(4, true, NORM_THREADS, NORM_THREADS / 64);
+  else MOE_NORM(2, false, group_threads(d), 1);
+#undef MOE_NORM
+  return hipGetLastError();
+}
+
+// Workgroups of the backward's first kernel: enough to fill the chip, few
+// enough that their partial rows stay a small part of the traffic.
+int rmsnorm_backward_groups(int T, int d) {
+  const int rows = d <= kWaveRowD ? NORM_THREADS / 64 : 1;
+  return (int)std::min((long)1024, ((long)T + rows - 1) / rows);
+}
+
+hipError_t launch_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const uint16_t* w, const float* rstd,
+                                   const uint16_t* dres, int T, int d, uint16_t* dh, float* dw, float* partial,
+                                   hipStream_t stream) {
+  const int n = T > 0 ? rmsnorm_backward_groups(T, d) : 0;   // no rows: dw = 0 alone
+  if (n == 0) {
+  } else if (d <= 512)
+    hipLaunchKernelGGL((rmsnorm_backward_kernel<1, true>), dim3(n), dim3(NORM_THREADS), 0, stream, dy, h, w, rstd,
+                       dres, T, d, dh, partial);
+  else if (d <= kWaveRowD)
+    hipLaunchKernelGGL((rmsnorm_backward_kernel<4, true>), dim3(n), dim3(NORM_THREADS), 0, stream, dy, h, w, rstd,
+                       dres, T, d, dh, partial);
+  else
+    hipLaunchKernelGGL((rmsnorm_backward_kernel<2, false>), dim3(n), dim3(group_threads(d)), 0, stream, dy, h, w,
+                       rstd, dres, T, d, dh, partial);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(rmsnorm_dw_kernel, dim3(d / 64), dim3(1024), 0, stream, partial, n, d, dw);
+  return hipGetLastError();
+}
+
+}  // namespace moe

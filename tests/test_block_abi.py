@@ -1,0 +1,128 @@
+"""include/moe_block.h: every declared symbol is exported and bound, and bad
+arguments are refused on the host before anything is enqueued (CPU only)."""
+
+import ctypes
+import os
+import subprocess
+
+import pytest
+import torch
+
+import routing_fp8_grouped_amd as moe
+from routing_fp8_grouped_amd import _lib, build
+
+P = ctypes.c_void_p
+A, B, MIS, MIS4 = P(0x100000), P(0x900000), P(0x100004), P(0x100002)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return _lib.load()
+
+
+def last(lib):
+    return lib.moe_last_error().decode()
+
+
+def test_exports_every_declared_symbol(lib):
+    declared = _lib.header_symbols(_lib.BLOCK_HEADER)
+    assert declared and not set(declared) & set(_lib.header_symbols())
+    out = subprocess.run(["nm", "-D", "--defined-only", _lib.LIB_PATH], capture_output=True, text=True,
+                         check=True).stdout
+    exported = {l.split()[-1] for l in out.splitlines() if " T " in l}
+    for name in declared:
+        assert name in exported and name in _lib.SIGNATURES and name in moe.__all__, name
+
+
+def test_header_is_c(tmp_path):
+    src = tmp_path / "c.c"
+    src.write_text('#include "moe_block.h"\nint main(void) { return (int)moe_rmsnorm_backward_workspace_bytes(0, 0); }\n')
+    assert os.path.getsize(build.build_c_program(str(src), str(tmp_path / "c"))) > 0
+
+
+@pytest.mark.parametrize("fn", ["moe_rmsnorm_quant", "moe_rmsnorm_quant_pow2"])
+def test_rmsnorm_validation(lib, fn):
+    f = getattr(lib, fn)
+
+    def call(x=A, r=None, w=A, T=4, d=256, eps=1e-6, s=None, y=B, q=None, sc=None, rstd=None):
+        return f(x, r, w, T, d, eps, s, y, q, sc, rstd, None)
+
+    for kw, code, msg in [
+            (dict(T=-1), 1, "T=-1"), (dict(d=100), 1, "d=100"), (dict(d=0), 1, "d=0"), (dict(d=-128), 1, "d=-128"),
+            (dict(d=16512), 2, "d=16512"), (dict(eps=0.0), 1, "eps"), (dict(eps=-1.0), 1, "eps"),
+            (dict(eps=float("nan")), 1, "eps"), (dict(eps=float("inf")), 1, "eps"),
+            (dict(q=A), 1, "together"), (dict(sc=A), 1, "together"), (dict(y=None), 1, "no output"),
+            (dict(x=None), 1, "x is NULL"), (dict(w=None), 1, "weight is NULL"), (dict(x=MIS), 1, "x is not"),
+            (dict(r=MIS), 1, "residual"), (dict(s=MIS), 1, "sum"), (dict(y=MIS), 1, "y is not"),
+            (dict(q=MIS, sc=A), 1, "q is not"), (dict(q=A, sc=MIS4), 1, "scale"), (dict(rstd=MIS4), 1, "rstd"),
+            (dict(y=A), 1, "y must not"), (dict(r=B), 1, "y must not")]:
+        assert call(**kw) == code and msg in last(lib), (kw, last(lib))
+    assert f(None, None, None, 0, 256, 1e-6, None, None, None, None, None, None) == 0
+
+
+def test_rmsnorm_backward_validation(lib):
+    need = lib.moe_rmsnorm_backward_workspace_bytes(5, 256)
+    assert need > 0 and lib.moe_rmsnorm_backward_workspace_bytes(1 << 20, 7168) <= 64 << 20
+    for T, d in [(0, 256), (-1, 256), (4, 100), (4, 0), (4, 16512)]:
+        assert lib.moe_rmsnorm_backward_workspace_bytes(T, d) == 0
+
+    def call(dy=A, h=A, w=A, rstd=A, dres=None, T=5, d=256, dh=B, dw=A, ws=A, n=need):
+        return lib.moe_rmsnorm_backward(dy, h, w, rstd, dres, T, d, dh, dw, ws, n, None)
+
+    for kw, code, msg in [
+            (dict(T=-1), 1, "T=-1"), (dict(d=100), 1, "d=100"), (dict(d=16512), 2, "d=16512"),
+            (dict(dy=None), 1, "dy is NULL"), (dict(h=MIS), 1, "h is not"), (dict(w=None), 1, "weight"),
+            (dict(rstd=None), 1, "rstd"), (dict(dres=MIS), 1, "dres"), (dict(dh=None), 1, "dh is NULL"),
+            (dict(dh=A), 1, "dh must not"), (dict(dw=None), 1, "dweight"), (dict(dw=MIS4), 1, "dweight"),
+            (dict(ws=None), 3, "workspace"), (dict(ws=MIS), 3, "workspace"), (dict(n=need - 1), 3, "workspace")]:
+        assert call(**kw) == code and msg in last(lib), (kw, last(lib))
+
+
+def grads(ptrs, sizes, types):
+    n = len(ptrs)
+    return ((ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * n)(*sizes), (ctypes.c_int * n)(*types), n)
+
+
+def test_grad_validation(lib):
+    need = lib.moe_grad_norm_workspace_bytes(2)
+    assert need > 0 and lib.moe_grad_norm_workspace_bytes(0) == 0 and lib.moe_grad_norm_workspace_bytes(-1) == 0
+    ok = grads([0x10000, None], [10, 0], [0, 1])
+
+    def norm(g=ok, mx=1.0, out=A, coef=A, ws=A, n=need):
+        return lib.moe_grad_norm(*g, mx, out, coef, ws, n, None)
+
+    def scale(g=ok, outs=(0x10000, None), coef=A):
+        o = None if outs is None else (ctypes.c_void_p * len(outs))(*outs)
+        return lib.moe_grad_scale(g[0], o, *g[1:], coef, None)
+
+    bad_lists = [(grads([0x10000], [-1], [0]), "sizes[0]"), (grads([0x10000], [(1 << 40) + 1], [0]), "sizes[0]"),
+                 (grads([0x10000], [1], [2]), "types[0]"), (grads([None], [1], [0]), "grads[0] is NULL"),
+                 (grads([0x10002], [1], [0]), "aligned"), (grads([0x10001], [1], [1]), "aligned"),
+                 ((None, ok[1], ok[2], 2), "grads"), ((ok[0], None, ok[2], 2), "sizes"),
+                 ((ok[0], ok[1], None, 2), "types"), ((ok[0], ok[1], ok[2], -1), "n_tensors")]
+    for g, msg in bad_lists:
+        assert norm(g=g) == 1 and msg in last(lib), last(lib)
+        assert scale(g=g) == 1 and msg in last(lib), last(lib)
+    for kw, code, msg in [(dict(mx=0.0), 1, "max_norm"), (dict(mx=-1.0), 1, "max_norm"),
+                          (dict(mx=float("nan")), 1, "max_norm"), (dict(out=None), 1, "norm"),
+                          (dict(coef=MIS4), 1, "coef"), (dict(ws=None), 3, "workspace"),
+                          (dict(ws=MIS), 3, "workspace"), (dict(n=need - 1), 3, "workspace")]:
+        assert norm(**kw) == code and msg in last(lib), (kw, last(lib))
+    for kw, msg in [(dict(outs=None), "outs"), (dict(outs=(None, None)), "outs[0] is NULL"),
+                    (dict(outs=(0x10002, None)), "aligned"), (dict(outs=(0x10010, None)), "overlaps"),
+                    (dict(outs=(0xFFF0, None)), "overlaps"), (dict(coef=None), "coef")]:
+        assert scale(**kw) == 1 and msg in last(lib), (kw, last(lib))
+    twice = grads([0x10000, 0x10000], [10, 10], [0, 0])
+    assert scale(g=twice, outs=(0x10000, 0x10000)) == 1 and "two outputs" in last(lib)
+    assert lib.moe_grad_scale(None, None, None, None, 0, A, None) == 0
+
+
+def test_binding_refusals():
+    x = torch.zeros(4, 128, dtype=torch.bfloat16)
+    w = torch.zeros(128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        moe.moe_rmsnorm_quant(x, w, 1e-6, x)
+    with pytest.raises(ValueError, match="two dimensions"):
+        moe.moe_rmsnorm_quant(w, w, 1e-6, w)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        moe.moe_rmsnorm_backward(x, x, w, w, x, w, w)
