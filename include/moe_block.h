@@ -1,8 +1,8 @@
 /*
  * moe_block.h — C ABI of libmoe.so, second part: the operators around the MoE
  * layer of moe.h.  The residual addition and RMS norm in front of it with an
- * FP8 output, forward and backward; and the global norm and clipping of its
- * gradients.
+ * FP8 output, forward and backward; the whole layer for a few tokens; and the
+ * global norm and clipping of its gradients.
  *
  * The conventions are those of moe.h: device pointers owned by the caller,
  * row-major layouts, 16-byte alignment of BF16 and byte matrices and 4-byte
@@ -73,6 +73,44 @@ size_t moe_rmsnorm_backward_workspace_bytes(int T, int d);
 moe_status moe_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const uint16_t* weight, const float* rstd,
                                 const uint16_t* dres, int T, int d, uint16_t* dh, float* dweight, void* workspace,
                                 size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace moe_layer_few needs (0 for sizes it refuses and for
+ * T = 0). */
+size_t moe_layer_few_workspace_bytes(int T, int d, int f, int E, int k);
+
+/* moe_layer_few — the whole layer for T <= 16 tokens: moe_route,
+ * fp8_quant_1x128, the grouped GEMMs and moe_combine in one call that streams
+ * the chosen experts' weights.
+ *   x         [T, d] BF16;  wg [E, d] BF16;  bias [E] FP32 or NULL; p as for
+ *             moe_route
+ *   w13, w13_s, w2, w2_s  the expert weights as for grouped_gemm_fp8_swiglu
+ *             with n_groups = E + 1: [E + 1, 2f, d] and [E + 1, d, f] E4M3 with
+ *             128x128 block scales, group E the shared expert
+ *   residual  [T, d] BF16 added to the output, or NULL
+ *   idx, w    [T, k] int32 / FP32 out: the selection and its gates, as
+ *             moe_route writes them
+ *   out       [T, d] BF16 out.  May be x's or residual's own memory.
+ *   workspace at least moe_layer_few_workspace_bytes(T, d, f, E, k) bytes,
+ *             16-byte aligned; overwritten; calls that share it must not overlap
+ * The layer's arithmetic (the activations and h in 1x128 FP8 tiles, FP32
+ * promotion of every K block) with two steps kept in higher precision: the
+ * selection ranks FP64 scores (moe_route's FP32 ones agree except within 1e-6
+ * of a tie), and the experts' outputs are summed in FP32 before the one
+ * rounding of out, without being rounded to BF16 first.
+ * T = 0 is a no-op.  Errors as moe_route and grouped_gemm_fp8_swiglu,
+ * MOE_ERR_WORKSPACE, and MOE_ERR_UNSUPPORTED for T > 16 or d > 8192. */
+moe_status moe_layer_few(const uint16_t* x, const uint16_t* wg, const float* bias, int T, int d, int f,
+                         moe_route_params p, const uint8_t* w13, const float* w13_s, const uint8_t* w2,
+                         const float* w2_s, const uint16_t* residual, int32_t* idx, float* w, uint16_t* out,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* moe_layer_few_pow2 — moe_layer_few with the power-of-two scale rule for x and
+ * h (the weights' scales may be any, as fp8_quant_128x128_pow2 writes them in
+ * that variant). */
+moe_status moe_layer_few_pow2(const uint16_t* x, const uint16_t* wg, const float* bias, int T, int d, int f,
+                              moe_route_params p, const uint8_t* w13, const float* w13_s, const uint8_t* w2,
+                              const float* w2_s, const uint16_t* residual, int32_t* idx, float* w, uint16_t* out,
+                              void* workspace, size_t workspace_bytes, void* stream);
 
 /* Element types of the gradient lists below. */
 typedef enum {

@@ -14,7 +14,8 @@ import torch
 
 from . import _lib
 from ._lib import MoEError, RouteParams  # noqa: F401
-from .block import (moe_grad_norm, moe_grad_norm_workspace_bytes, moe_grad_scale, moe_rmsnorm_backward,
+from .block import (moe_grad_norm, moe_grad_norm_workspace_bytes, moe_grad_scale, moe_layer_few,
+                    moe_layer_few_pow2, moe_layer_few_workspace_bytes, moe_rmsnorm_backward,
                     moe_rmsnorm_backward_workspace_bytes, moe_rmsnorm_quant, moe_rmsnorm_quant_pow2)
 
 __all__ = ["moe_route", "moe_route_workspace_bytes", "fp8_quant_1x128", "fp8_quant_128x128", "moe_permute_workspace_bytes",
@@ -23,7 +24,8 @@ __all__ = ["moe_route", "moe_route_workspace_bytes", "fp8_quant_1x128", "fp8_qua
            "grouped_gemm_fp8_up_e8m0", "grouped_gemm_fp8_down_e8m0", "grouped_gemm_fp8_up_train",
            "moe_transpose_fp8_blocks", "moe_combine_backward", "moe_wgrad_columns", "moe_regroup_128x1",
            "moe_swiglu_backward", "grouped_gemm_fp8_wgrad", "moe_rmsnorm_quant", "moe_rmsnorm_quant_pow2",
-           "moe_rmsnorm_backward_workspace_bytes", "moe_rmsnorm_backward", "moe_grad_norm_workspace_bytes",
+           "moe_rmsnorm_backward_workspace_bytes", "moe_rmsnorm_backward", "moe_layer_few_workspace_bytes",
+           "moe_layer_few", "moe_layer_few_pow2", "moe_grad_norm_workspace_bytes",
            "moe_grad_norm", "moe_grad_scale", "MoEWeights", "MoELayer",
            "MoEError", "RouteParams"]
 

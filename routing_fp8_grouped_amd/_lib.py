@@ -70,6 +70,9 @@ SIGNATURES = {
     "moe_rmsnorm_quant_pow2": (I, [P, P, P, I, I, ctypes.c_float, P, P, P, P, P, P]),
     "moe_rmsnorm_backward_workspace_bytes": (SZ, [I, I]),
     "moe_rmsnorm_backward": (I, [P, P, P, P, P, I, I, P, P, P, SZ, P]),
+    "moe_layer_few_workspace_bytes": (SZ, [I, I, I, I, I]),
+    "moe_layer_few": (I, [P, P, P, I, I, I, RouteParams, P, P, P, P, P, P, P, P, P, SZ, P]),
+    "moe_layer_few_pow2": (I, [P, P, P, I, I, I, RouteParams, P, P, P, P, P, P, P, P, P, SZ, P]),
     "moe_grad_norm_workspace_bytes": (SZ, [I]),
     "moe_grad_norm": (I, [P, P, P, I, ctypes.c_float, P, P, P, SZ, P]),
     "moe_grad_scale": (I, [P, P, P, P, I, P, P]),

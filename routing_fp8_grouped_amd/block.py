@@ -97,6 +97,42 @@ def moe_rmsnorm_backward(dy, h, weight, rstd, dh, dweight, workspace, dres=None,
           _ptr(dweight), _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(stream))
 
 
+def moe_layer_few_workspace_bytes(T, d, f, E, k):
+    return int(_lib.load().moe_layer_few_workspace_bytes(T, d, f, E, k))
+
+
+def _layer_few(name, x, wg, bias, n_groups, topk_groups, topk, route_scale, w13, w13_s, w2, w2_s, idx, w, out,
+               workspace, residual, stream):
+    if x.dim() != 2 or wg.dim() != 2 or w2.dim() != 3:
+        raise ValueError("x and wg must have two dimensions, w13 and w2 three")
+    T, d = x.shape
+    E, f = wg.shape[0], w2.shape[2]
+    _check(x, (x, "x", _BF16, None), (wg, "wg", _BF16, (E, d)), (bias, "bias", _FP32, (E,)),
+           (w13, "w13", _U8, (E + 1, 2 * f, d)), (w13_s, "w13_s", _FP32, (E + 1, 2 * f // 128, d // 128)),
+           (w2, "w2", _U8, (E + 1, d, f)), (w2_s, "w2_s", _FP32, (E + 1, d // 128, f // 128)),
+           (idx, "idx", _I32, (T, topk)), (w, "w", _FP32, (T, topk)), (out, "out", _BF16, (T, d)),
+           (workspace, "workspace", _U8, None), (residual, "residual", _BF16, (T, d)))
+    _call(name, _ptr(x), _ptr(wg), _ptr(bias), T, d, f, _lib.RouteParams(E, n_groups, topk_groups, topk, route_scale),
+          _ptr(w13), _ptr(w13_s), _ptr(w2), _ptr(w2_s), _ptr(residual), _ptr(idx), _ptr(w), _ptr(out),
+          _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(stream))
+
+
+def moe_layer_few(x, wg, bias, n_groups, topk_groups, topk, route_scale, w13, w13_s, w2, w2_s, idx, w, out, workspace,
+                  residual=None, stream=None):
+    """The whole layer for up to 16 tokens: out [T, d] BF16 (plus ``residual``, whose memory it may be), idx [T, k]
+    int32 and w [T, k] float32 as moe_route writes them.  The weights are MoEWeights' arrays, the shared expert last;
+    ``workspace`` is uint8 of moe_layer_few_workspace_bytes(T, d, f, E, k)."""
+    _layer_few("moe_layer_few", x, wg, bias, n_groups, topk_groups, topk, route_scale, w13, w13_s, w2, w2_s, idx, w,
+               out, workspace, residual, stream)
+
+
+def moe_layer_few_pow2(x, wg, bias, n_groups, topk_groups, topk, route_scale, w13, w13_s, w2, w2_s, idx, w, out,
+                       workspace, residual=None, stream=None):
+    """moe_layer_few with power-of-two scales for x and h."""
+    _layer_few("moe_layer_few_pow2", x, wg, bias, n_groups, topk_groups, topk, route_scale, w13, w13_s, w2, w2_s, idx,
+               w, out, workspace, residual, stream)
+
+
 # ---- gradient lists ----
 
 _GRAD_TYPES = {_FP32: 0, _BF16: 1}

@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libmoe.so")
 
 SOURCES = ["api.cpp", "quant.hip", "route.hip", "permute.hip", "gemm.hip", "gemm_small.hip",
            "combine.hip", "balance.hip", "backward.hip", "wgrad.hip", "roofs.hip",
-           "api_block.cpp", "norm.hip", "grad.hip"]
+           "api_block.cpp", "norm.hip", "few.hip", "grad.hip"]
 ARCH = os.environ.get("MOE_OFFLOAD_ARCH", "gfx950")
 
 

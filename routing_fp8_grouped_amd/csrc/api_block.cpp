@@ -53,6 +53,47 @@ size_t rmsnorm_backward_bytes(int T, int d) {
   return (size_t)moe::rmsnorm_backward_groups(T, d) * d * sizeof(float);
 }
 
+moe_status check_few(int T, int d, int f, int E, int k) {
+  REQUIRE(T >= 0, "T=%d is negative", T);
+  REQUIRE(d >= 128 && d % 128 == 0, "d=%d must be a positive multiple of 128", d);
+  REQUIRE(f >= 128 && f % 128 == 0, "f=%d must be a positive multiple of 128", f);
+  REQUIRE(E >= 1 && E <= 256, "E=%d must be in [1, 256]", E);
+  REQUIRE(k >= 1 && k <= 16 && k <= E, "k=%d must be in [1, min(16, E)]", k);
+  if (T > moe::kFewMaxT) return fail(MOE_ERR_UNSUPPORTED, "T=%d > %d is not implemented", T, moe::kFewMaxT);
+  if (d > moe::kFewMaxD) return fail(MOE_ERR_UNSUPPORTED, "d=%d > %d is not implemented", d, moe::kFewMaxD);
+  if ((uint64_t)2 * f * d > 0xFFFFFFFFull)
+    return fail(MOE_ERR_UNSUPPORTED, "2f*d=%llu bytes per expert exceeds 4 GiB", (unsigned long long)2 * f * d);
+  return MOE_OK;
+}
+
+moe_status layer_few_impl(const uint16_t* x, const uint16_t* wg, const float* bias, int T, int d, int f,
+                          moe_route_params p, const uint8_t* w13, const float* w13_s, const uint8_t* w2,
+                          const float* w2_s, const uint16_t* residual, int32_t* idx, float* w, uint16_t* out,
+                          void* workspace, size_t workspace_bytes, bool pow2, void* stream) {
+  moe_status s = check_route_params(p);
+  if (s == MOE_OK) s = check_few(T, d, f, p.n_experts, p.topk);
+  if (s != MOE_OK || T == 0) return s;
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(wg);
+  REQUIRE_ALIGNED4_OR_NULL(bias);
+  REQUIRE_PTR(w13);
+  REQUIRE_PTR4(w13_s);
+  REQUIRE_PTR(w2);
+  REQUIRE_PTR4(w2_s);
+  REQUIRE_ALIGNED_OR_NULL(residual);
+  REQUIRE_PTR4(idx);
+  REQUIRE_PTR4(w);
+  REQUIRE_PTR(out);
+  const size_t need = moe::layer_few_workspace_bytes(T, d, f, p.n_experts, p.topk);
+  if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "workspace %p of %zu bytes: %zu bytes, 16-byte aligned, needed", workspace,
+                workspace_bytes, need);
+  return hip_status(moe::launch_layer_few(x, wg, bias, T, d, f, p.n_experts, p.n_groups, p.topk_groups, p.topk,
+                                          p.route_scale, w13, w13_s, w2, w2_s, residual, idx, w, out, workspace,
+                                          pow2, static_cast<hipStream_t>(stream)),
+                    pow2 ? "moe_layer_few_pow2 launch" : "moe_layer_few launch");
+}
+
 moe_status check_grads(const void* const* grads, const int64_t* sizes, const int* types, int n_tensors) {
   REQUIRE(n_tensors >= 0, "n_tensors=%d is negative", n_tensors);
   if (n_tensors == 0) return MOE_OK;
@@ -132,6 +173,30 @@ moe_status moe_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const uin
   return hip_status(moe::launch_rmsnorm_backward(dy, h, weight, rstd, dres, T, d, dh, dweight,
                                                  static_cast<float*>(workspace), static_cast<hipStream_t>(stream)),
                     "moe_rmsnorm_backward launch");
+}
+
+size_t moe_layer_few_workspace_bytes(int T, int d, int f, int E, int k) {
+  clear_error();
+  if (T <= 0 || check_few(T, d, f, E, k) != MOE_OK) return 0;
+  return moe::layer_few_workspace_bytes(T, d, f, E, k);
+}
+
+moe_status moe_layer_few(const uint16_t* x, const uint16_t* wg, const float* bias, int T, int d, int f,
+                         moe_route_params p, const uint8_t* w13, const float* w13_s, const uint8_t* w2,
+                         const float* w2_s, const uint16_t* residual, int32_t* idx, float* w, uint16_t* out,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  clear_error();
+  return layer_few_impl(x, wg, bias, T, d, f, p, w13, w13_s, w2, w2_s, residual, idx, w, out, workspace,
+                        workspace_bytes, false, stream);
+}
+
+moe_status moe_layer_few_pow2(const uint16_t* x, const uint16_t* wg, const float* bias, int T, int d, int f,
+                              moe_route_params p, const uint8_t* w13, const float* w13_s, const uint8_t* w2,
+                              const float* w2_s, const uint16_t* residual, int32_t* idx, float* w, uint16_t* out,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  clear_error();
+  return layer_few_impl(x, wg, bias, T, d, f, p, w13, w13_s, w2, w2_s, residual, idx, w, out, workspace,
+                        workspace_bytes, true, stream);
 }
 
 size_t moe_grad_norm_workspace_bytes(int n_tensors) {

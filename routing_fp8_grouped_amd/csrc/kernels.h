@@ -94,6 +94,15 @@ hipError_t launch_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const 
                                    const uint16_t* dres, int T, int d, uint16_t* dh, float* dw, float* partial,
                                    hipStream_t stream);
 
+// The whole layer for a few tokens (few.hip).
+constexpr int kFewMaxT = 16;
+constexpr int kFewMaxD = 8192;
+size_t layer_few_workspace_bytes(int T, int d, int f, int E, int k);
+hipError_t launch_layer_few(const uint16_t* x, const uint16_t* wg, const float* bias, int T, int d, int f, int E,
+                            int G, int M, int k, float route_scale, const uint8_t* w13, const float* w13_s,
+                            const uint8_t* w2, const float* w2_s, const uint16_t* residual, int32_t* idx, float* w,
+                            uint16_t* out, void* workspace, bool pow2, hipStream_t stream);
+
 // Global gradient norm and scaling over lists of tensors (grad.hip).
 size_t grad_norm_workspace_bytes(int n_tensors);
 hipError_t launch_grad_norm(const void* const* grads, const int64_t* sizes, const int* types, int n_tensors,

@@ -78,6 +78,35 @@ def test_rmsnorm_backward_validation(lib):
         assert call(**kw) == code and msg in last(lib), (kw, last(lib))
 
 
+@pytest.mark.parametrize("fn", ["moe_layer_few", "moe_layer_few_pow2"])
+def test_layer_few_validation(lib, fn):
+    f = getattr(lib, fn)
+    need = lib.moe_layer_few_workspace_bytes(4, 256, 128, 16, 4)
+    assert need > 0
+    for bad in [(0, 256, 128, 16, 4), (-1, 256, 128, 16, 4), (17, 256, 128, 16, 4), (4, 100, 128, 16, 4),
+                (4, 8320, 128, 16, 4), (4, 256, 100, 16, 4), (4, 256, 128, 0, 4), (4, 256, 128, 257, 4),
+                (4, 256, 128, 16, 0), (4, 256, 128, 16, 17), (4, 256, 128, 3, 4), (4, 8192, 1 << 20, 16, 4)]:
+        assert lib.moe_layer_few_workspace_bytes(*bad) == 0, bad
+
+    def call(x=A, wg=A, b=None, T=4, d=256, ff=128, p=(16, 4, 2, 4, 2.5), w13=A, s13=A, w2=A, s2=A, r=None, idx=A,
+             w=A, out=B, ws=A, n=need):
+        return f(x, wg, b, T, d, ff, _lib.RouteParams(*p), w13, s13, w2, s2, r, idx, w, out, ws, n, None)
+
+    for kw, code, msg in [
+            (dict(T=-1), 1, "T=-1"), (dict(T=17), 2, "T=17"), (dict(d=100), 1, "d=100"), (dict(d=0), 1, "d=0"),
+            (dict(d=8320), 2, "d=8320"), (dict(ff=64), 1, "f=64"), (dict(ff=1 << 24), 2, "4 GiB"),
+            (dict(p=(0, 1, 1, 1, 1.0)), 1, "n_experts"), (dict(p=(300, 4, 2, 4, 1.0)), 1, "n_experts"),
+            (dict(p=(16, 3, 2, 4, 1.0)), 1, "multiple"), (dict(p=(16, 4, 5, 5, 1.0)), 1, "topk_groups"),
+            (dict(p=(16, 4, 2, 3, 1.0)), 1, "multiple"), (dict(p=(64, 1, 1, 17, 1.0)), 2, "topk=17"),
+            (dict(p=(16, 4, 2, 4, float("nan"))), 1, "route_scale"),
+            (dict(x=None), 1, "x is NULL"), (dict(wg=MIS), 1, "wg"), (dict(b=MIS4), 1, "bias"), (dict(w13=None), 1, "w13"),
+            (dict(s13=MIS4), 1, "w13_s"), (dict(w2=MIS), 1, "w2"), (dict(s2=None), 1, "w2_s"), (dict(r=MIS), 1, "residual"),
+            (dict(idx=None), 1, "idx"), (dict(w=None), 1, "w is NULL"), (dict(out=MIS), 1, "out"),
+            (dict(ws=None), 3, "workspace"), (dict(ws=MIS), 3, "workspace"), (dict(n=need - 1), 3, "workspace")]:
+        assert call(**kw) == code and msg in last(lib), (kw, last(lib))
+    assert f(None, None, None, 0, 256, 128, _lib.RouteParams(16, 4, 2, 4, 2.5), *[None] * 9, 0, None) == 0
+
+
 def grads(ptrs, sizes, types):
     n = len(ptrs)
     return ((ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * n)(*sizes), (ctypes.c_int * n)(*types), n)
