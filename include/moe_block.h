@@ -98,7 +98,7 @@ size_t moe_layer_few_workspace_bytes(int T, int d, int f, int E, int k);
  * of a tie), and the experts' outputs are summed in FP32 before the one
  * rounding of out, without being rounded to BF16 first.
  * T = 0 is a no-op.  Errors as moe_route and grouped_gemm_fp8_swiglu,
- * MOE_ERR_WORKSPACE, and MOE_ERR_UNSUPPORTED for T > 16 or d > 8192. */
+ * MOE_ERR_WORKSPACE, and MOE_ERR_UNSUPPORTED for T > 16, d > 8192 or f > 32768. */
 moe_status moe_layer_few(const uint16_t* x, const uint16_t* wg, const float* bias, int T, int d, int f,
                          moe_route_params p, const uint8_t* w13, const float* w13_s, const uint8_t* w2,
                          const float* w2_s, const uint16_t* residual, int32_t* idx, float* w, uint16_t* out,

@@ -61,8 +61,7 @@ moe_status check_few(int T, int d, int f, int E, int k) {
   REQUIRE(k >= 1 && k <= 16 && k <= E, "k=%d must be in [1, min(16, E)]", k);
   if (T > moe::kFewMaxT) return fail(MOE_ERR_UNSUPPORTED, "T=%d > %d is not implemented", T, moe::kFewMaxT);
   if (d > moe::kFewMaxD) return fail(MOE_ERR_UNSUPPORTED, "d=%d > %d is not implemented", d, moe::kFewMaxD);
-  if ((uint64_t)2 * f * d > 0xFFFFFFFFull)
-    return fail(MOE_ERR_UNSUPPORTED, "2f*d=%llu bytes per expert exceeds 4 GiB", (unsigned long long)2 * f * d);
+  if (f > moe::kFewMaxF) return fail(MOE_ERR_UNSUPPORTED, "f=%d > %d is not implemented", f, moe::kFewMaxF);
   return MOE_OK;
 }
 

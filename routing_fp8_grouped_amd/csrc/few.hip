@@ -24,6 +24,7 @@
 //     so the gated sum over experts is its accumulator and the combine, in
 //     registers: expert outputs never reach memory.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.h"
 #include "kernels.h"
@@ -37,15 +38,18 @@ constexpr int FW_THREADS = 512;
 constexpr int FW_WAVES = FW_THREADS / 64;
 constexpr int FW_MAX_E = 256;
 constexpr int FW_MAX_K = 16;
-constexpr int FW_RING = 6;              // steps of W2 loads in flight per wave
+constexpr int FR_THREADS = 512;         // router
+constexpr int FR_WAVES = FR_THREADS / 64;
+constexpr int FR_RING = 4;              // 32-element chunks in flight per wave
+constexpr int FR_MAX_SPLITS = 8;
 
 // Device workspace (byte offsets; every part 256-byte aligned).
 struct FewLayout {
-  size_t sig, xq, xs, h, hq, hsg, plan, total;
+  size_t part, xq, xs, h, hq, hsg, plan, total;
 };
 
 struct FewPlan {                        // written by the first product's workgroup 0
-  int n_active;                         // experts with a token, then the shared one
+  int n_active;                         // the shared expert, then those with a token, ascending
   int pad[3];
   int expert[FW_MAX_E + 1];
   float gate[FW_T * (FW_MAX_K + 1)];    // of row t (k + 1) + slot
@@ -61,7 +65,7 @@ FewLayout few_layout(int T, int d, int f, int E, int k) {
     return o;
   };
   const size_t rows = (size_t)T * (k + 1);
-  L.sig = take((size_t)T * E * sizeof(double));
+  L.part = take((size_t)FR_MAX_SPLITS * T * E * sizeof(double));
   L.xq = take((size_t)T * d);
   L.xs = take((size_t)T * (d / 128) * sizeof(float));
   L.h = take(rows * f * sizeof(float));
@@ -86,7 +90,8 @@ struct FewArgs {
   int32_t* idx;
   float* w;
   uint16_t* out;
-  double* sig;      // [T, E]
+  int splits;       // parts of d in the logits' partial sums
+  double* part;     // [splits, T, E] partial logits
   uint8_t* xq;      // [T, d]
   float* xs;        // [T, d/128]
   float* h;         // [T (k+1), f]
@@ -140,13 +145,27 @@ __device__ __forceinline__ v8i row_frag(const uint8_t* p) {
   return v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
 }
 
-// ---- kernel 1: affinities (one workgroup per expert) and the tiles of x ----
+// ---- kernel 1: partial logits and the tiles of x ----
+// A workgroup takes 16 experts and one of `splits` parts of d, so that the
+// 3.7 MB of V3's router come through 128 CUs; the next kernel adds the parts.
+// A BF16 MFMA multiplies 16 experts by 16 tokens over 32 elements, and those
+// partial sums, good to 2^-24 of their largest product, add up in FP64: a
+// logit is exact to 10^-8, ranked as FP64.  (The FP64 MFMA is exact but takes
+// 64 clocks for 4 elements.)
+typedef double v4d __attribute__((ext_vector_type(4)));
+
+union Bf16x8 {
+  uint4 u;
+  v8bf v;
+};
+
 template <bool POW2>
-__global__ __launch_bounds__(256) void few_route_kernel(const FewArgs p) {
-  __shared__ double red[4][FW_T];
-  const int tid = threadIdx.x;
-  if ((int)blockIdx.x >= p.E) {
-    const int tile = ((int)blockIdx.x - p.E) * 16 + (tid >> 4);
+__global__ __launch_bounds__(FR_THREADS) void few_route_kernel(const FewArgs p) {
+  __shared__ v4d red[FR_WAVES][64];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int router = (p.E + 15) / 16 * p.splits;
+  if ((int)blockIdx.x >= router) {
+    const int tile = ((int)blockIdx.x - router) * (FR_THREADS / 16) + (tid >> 4);
     const int sub = tid & 15;
     if (tile >= p.T * (p.d / 128)) return;
     const uint4 raw = *reinterpret_cast<const uint4*>(p.x + (size_t)tile * 128 + sub * 8);
@@ -169,172 +188,200 @@ __global__ __launch_bounds__(256) void few_route_kernel(const FewArgs p) {
     if (sub == 0) p.xs[tile] = s;
     return;
   }
-  // a BF16 product is exact in FP32 and its sum runs in FP64, so the scores
-  // that the selection compares are exact to 10^-15
-  const int e = blockIdx.x;
-  double acc[FW_T];
+  const int e0 = (int)blockIdx.x / p.splits * 16, split = (int)blockIdx.x % p.splits;
+  const int r16 = lane & 15, g16 = lane >> 4;
+  // rows past the last expert or token repeat it; their results are not stored
+  const uint16_t* wr = p.wg + (size_t)min(e0 + r16, p.E - 1) * p.d + g16 * 8;
+  const uint16_t* xr = p.x + (size_t)min(r16, p.T - 1) * p.d + g16 * 8;
+  const int chunks = p.d / 32;
+  v4d acc = v4d{0.0, 0.0, 0.0, 0.0};
+  const int stride = FR_WAVES * p.splits;   // the parts interleave
+  for (int c0 = split * FR_WAVES + wave; c0 < chunks; c0 += stride * FR_RING) {
+    Bf16x8 a[FR_RING], b[FR_RING];
 #pragma unroll
-  for (int t = 0; t < FW_T; ++t) acc[t] = 0.0;
-  for (int c = tid; c < p.d / 8; c += 256) {
-    const uint4 raw = *reinterpret_cast<const uint4*>(p.wg + (size_t)e * p.d + c * 8);
-    const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+    for (int r = 0; r < FR_RING; ++r) {
+      const int c = min(c0 + r * stride, chunks - 1);
+      a[r].u = *reinterpret_cast<const uint4*>(wr + c * 32);
+      b[r].u = *reinterpret_cast<const uint4*>(xr + c * 32);
+    }
 #pragma unroll
-    for (int t = 0; t < FW_T; ++t) {
-      if (t < p.T) {
-        const uint4 xr = *reinterpret_cast<const uint4*>(p.x + (size_t)t * p.d + c * 8);
-        const uint32_t xu[4] = {xr.x, xr.y, xr.z, xr.w};
+    for (int r = 0; r < FR_RING; ++r) {
+      const v4f q = mfma_bf16_16x16x32(a[r].v, b[r].v, v4f{0.f, 0.f, 0.f, 0.f});
+      if (c0 + r * stride < chunks) {   // uniform over the wave
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          acc[t] += (double)(__uint_as_float(u[i] << 16) * __uint_as_float(xu[i] << 16));
-          acc[t] += (double)(__uint_as_float(u[i] & 0xFFFF0000u) * __uint_as_float(xu[i] & 0xFFFF0000u));
-        }
+        for (int i = 0; i < 4; ++i) acc[i] += (double)q[i];
       }
     }
   }
-#pragma unroll
-  for (int t = 0; t < FW_T; ++t) {
-    if (t < p.T) {
-      double v = acc[t];
-#pragma unroll
-      for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-      if ((tid & 63) == 0) red[tid >> 6][t] = v;
-    }
-  }
+  red[wave][lane] = acc;
   __syncthreads();
-  if (tid < p.T) {
-    const double l = (red[0][tid] + red[1][tid]) + (red[2][tid] + red[3][tid]);
-    p.sig[(size_t)tid * p.E + e] = 1.0 / (1.0 + exp(-l));
+  // lane l holds rows (experts) 4 (l / 16) + i, column (token) l % 16
+  if (tid < 256) {
+    const int i = tid >> 6, e = e0 + 4 * g16 + i;
+    double l = red[0][lane][i];
+#pragma unroll
+    for (int v = 1; v < FR_WAVES; ++v) l += red[v][lane][i];
+    if (r16 < p.T && e < p.E) p.part[((size_t)split * p.T + r16) * p.E + e] = l;
   }
 }
 
-// ---- selection: a wave per token ----
+// ---- selection, by a whole workgroup, (token, expert) pairs over its threads ----
 struct SelectLds {
-  double z[FW_WAVES][FW_MAX_E];          // biased scores, later the group's best in order
-  double best[FW_WAVES][FW_MAX_E];       // [group][rank]
-  double group[FW_WAVES][64];
-  double gate[FW_WAVES][FW_MAX_K];
-  uint16_t id[FW_WAVES][FW_MAX_E];
-  uint32_t mask[FW_WAVES][FW_MAX_E / 32];
+  double z[FW_T][FW_MAX_E];              // biased scores
+  double sig[FW_T][FW_MAX_E];            // affinities
+  double best[FW_T][FW_MAX_E];           // [group][rank]: each group's best, in order
+  double group[FW_T][64];
+  double gate[FW_T][FW_MAX_K];
+  uint64_t kept[FW_T];                   // groups kept
+  uint32_t mask[FW_T][FW_MAX_E / 32];    // experts chosen
   uint32_t active[FW_MAX_E / 32];        // experts any token chose
-  int16_t chosen[FW_T][FW_MAX_K];
+  uint16_t id[FW_T][FW_MAX_E];           // of best
+  int16_t chosen[FW_T][FW_MAX_K];        // ascending
 };
 
-// Token t on this wave.  Ranks are counted, not sorted: an expert's rank in
-// its group is the number of its better ones there; the best min(k, group
-// size) of each group, in order, are all that the later steps read.  NaN
-// scores rank last, so every index stays in range whatever the inputs.
-__device__ void few_select_token(const FewArgs& p, SelectLds& S, FewPlan& P, int t, int wave, int lane,
-                                 bool write_out) {
-  const int per = p.E / p.G, n_top = p.k / p.M, keep = min(p.k, per);
-  double* z = S.z[wave];
-  const double* sig = p.sig + (size_t)t * p.E;
-  for (int e = lane; e < p.E; e += 64) {
-    const double v = sig[e] + (p.bias ? (double)p.bias[e] : 0.0);
-    z[e] = v == v ? v : -__builtin_huge_val();
+// The batch's plan in LDS.  Ranks are counted, not sorted: an expert's rank in
+// its group is the number of better ones there; the best min(k, group size) of
+// each group, in order, are all that the later steps read.  NaN scores rank
+// last, so every index stays in range whatever the inputs.
+__device__ void few_select(const FewArgs& p, SelectLds& S, FewPlan& P, bool write_out) {
+  const int tid = threadIdx.x;
+  const int per = p.E / p.G, n_top = p.k / p.M, keep = min(p.k, per), cand = p.G * keep;
+  for (int i = tid; i < p.T * p.E; i += FW_THREADS) {
+    const int t = i / p.E, e = i - t * p.E;
+    double l = p.part[i];
+    for (int q = 1; q < p.splits; ++q) l += p.part[(size_t)q * p.T * p.E + i];
+    const double s = 1.0 / (1.0 + exp(-l)), v = s + (p.bias ? (double)p.bias[e] : 0.0);
+    S.sig[t][e] = s;
+    S.z[t][e] = v == v ? v : -__builtin_huge_val();
   }
-  if (lane < FW_MAX_E / 32) S.mask[wave][lane] = 0;
-  wave_lds_fence();
-  for (int e = lane; e < p.E; e += 64) {
-    const int g = e / per;
-    const double v = z[e];
+  if (tid < FW_MAX_E / 32) S.active[tid] = 0;
+  if (tid < FW_T) S.kept[tid] = 0;
+  if (tid < FW_T * FW_MAX_E / 32) S.mask[0][tid] = 0;
+  for (int i = tid; i < (FW_MAX_E + 1) * FW_T / 4; i += FW_THREADS) reinterpret_cast<uint32_t*>(P.slot)[i] = ~0u;
+  __syncthreads();
+  for (int i = tid; i < p.T * p.E; i += FW_THREADS) {
+    const int t = i / p.E, e = i - t * p.E, g = e / per;
+    const double v = S.z[t][e];
     int r = 0;
-    for (int o = g * per; o < (g + 1) * per; ++o) r += (z[o] > v || (z[o] == v && o < e)) ? 1 : 0;
+#pragma unroll 8
+    for (int o = g * per; o < (g + 1) * per; ++o) {
+      const double ov = S.z[t][o];
+      r += (ov > v || (ov == v && o < e)) ? 1 : 0;
+    }
     if (r < keep) {
-      S.best[wave][g * keep + r] = v;
-      S.id[wave][g * keep + r] = (uint16_t)e;
+      S.best[t][g * keep + r] = v;
+      S.id[t][g * keep + r] = (uint16_t)e;
     }
   }
-  wave_lds_fence();
-  double gs = 0.0;
-  if (lane < p.G) {
-    for (int r = 0; r < n_top; ++r) gs += S.best[wave][lane * keep + r];
-    S.group[wave][lane] = gs;
+  __syncthreads();
+  for (int i = tid; i < p.T * p.G; i += FW_THREADS) {
+    const int t = i / p.G, g = i - t * p.G;
+    double s = 0.0;
+    for (int r = 0; r < n_top; ++r) s += S.best[t][g * keep + r];
+    S.group[t][g] = s;
   }
-  wave_lds_fence();
-  int gr = 0;
-  if (lane < p.G)
-    for (int o = 0; o < p.G; ++o) {
-      const double og = S.group[wave][o];
-      gr += (og > gs || (og == gs && o < lane)) ? 1 : 0;
-    }
-  const uint64_t kept = __ballot(lane < p.G && gr < p.M);
-  for (int c = lane; c < p.G * keep; c += 64) {
-    if (!((kept >> (c / keep)) & 1)) continue;
-    const double v = S.best[wave][c];
-    const int e = S.id[wave][c];
+  __syncthreads();
+  for (int i = tid; i < p.T * p.G; i += FW_THREADS) {
+    const int t = i / p.G, g = i - t * p.G;
+    const double s = S.group[t][g];
     int r = 0;
-    for (int g = 0; g < p.G; ++g) {
-      if (!((kept >> g) & 1)) continue;
+#pragma unroll 8
+    for (int o = 0; o < p.G; ++o) {
+      const double os = S.group[t][o];
+      r += (os > s || (os == s && o < g)) ? 1 : 0;
+    }
+    if (r < p.M) atomicOr(reinterpret_cast<unsigned long long*>(&S.kept[t]), 1ull << g);
+  }
+  __syncthreads();
+  for (int i = tid; i < p.T * cand; i += FW_THREADS) {
+    const int t = i / cand, c = i - t * cand;
+    const uint64_t kept = S.kept[t];
+    if (!((kept >> (c / keep)) & 1)) continue;
+    const double v = S.best[t][c];
+    const int e = S.id[t][c];
+    int r = 0;
+    for (uint64_t m = kept; m; m &= m - 1) {
+      const int g = __ffsll((unsigned long long)m) - 1;
+#pragma unroll 8
       for (int o = g * keep; o < (g + 1) * keep; ++o) {
-        const double ov = S.best[wave][o];
-        r += (ov > v || (ov == v && S.id[wave][o] < e)) ? 1 : 0;
+        const double ov = S.best[t][o];
+        r += (ov > v || (ov == v && S.id[t][o] < e)) ? 1 : 0;
       }
     }
     if (r < p.k) {
-      atomicOr(&S.mask[wave][e >> 5], 1u << (e & 31));
+      atomicOr(&S.mask[t][e >> 5], 1u << (e & 31));
       atomicOr(&S.active[e >> 5], 1u << (e & 31));
     }
   }
-  wave_lds_fence();
-  // ascending ids: lane w < 8 lists word w's experts after the lower words'
-  if (lane < FW_MAX_E / 32) {
-    int j = 0;
-    for (int i = 0; i < lane; ++i) j += __popc(S.mask[wave][i]);
-    for (uint32_t m = S.mask[wave][lane]; m; m &= m - 1) {
-      const int e = lane * 32 + __ffs(m) - 1;
-      S.chosen[t][j] = (int16_t)e;
-      S.gate[wave][j] = sig[e];
-      ++j;
-    }
-  }
-  wave_lds_fence();
-  double total = 0.0;
-  for (int j = 0; j < p.k; ++j) total += S.gate[wave][j];
-  if (lane <= p.k) {
-    const float w = lane < p.k ? (float)(p.route_scale * S.gate[wave][lane] / total) : 1.0f;
-    P.gate[t * (p.k + 1) + lane] = w;
-    if (write_out && lane < p.k) {
-      p.w[(size_t)t * p.k + lane] = w;
-      p.idx[(size_t)t * p.k + lane] = S.chosen[t][lane];
-    }
-  }
-  wave_lds_fence();
-}
-
-// The plan of the batch in LDS, by the whole workgroup.
-__device__ void few_select(const FewArgs& p, SelectLds& S, FewPlan& P, bool write_out) {
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  if (tid < FW_MAX_E / 32) S.active[tid] = 0;
-  for (int i = tid; i < (FW_MAX_E + 1) * FW_T / 4; i += FW_THREADS) reinterpret_cast<uint32_t*>(P.slot)[i] = ~0u;
   __syncthreads();
-  for (int t = wave; t < p.T; t += FW_WAVES) few_select_token(p, S, P, t, wave, lane, write_out);
-  __syncthreads();
-  auto place = [&](int e) {   // position of expert e in the ascending list
-    int a = __popc(S.active[e >> 5] & ((1u << (e & 31)) - 1u));
-    for (int i = 0; i < (e >> 5); ++i) a += __popc(S.active[i]);
+  // position of expert e among a bit mask's, ascending
+  auto place = [](const uint32_t* mask, int e) {
+    int a = __popc(mask[e >> 5] & ((1u << (e & 31)) - 1u));
+#pragma unroll
+    for (int i = 0; i < FW_MAX_E / 32; ++i) a += i < (e >> 5) ? __popc(mask[i]) : 0;
     return a;
   };
-  int n = 0;
-#pragma unroll
-  for (int i = 0; i < FW_MAX_E / 32; ++i) n += __popc(S.active[i]);
-  for (int i = tid; i < p.T * p.k; i += FW_THREADS) {
-    const int t = i / p.k, j = i - t * p.k, e = S.chosen[t][j], a = place(e);
+  // a chosen expert is one of its group's best, so the candidates hold them all
+  for (int i = tid; i < p.T * cand; i += FW_THREADS) {
+    const int t = i / cand, c = i - t * cand;
+    const int e = S.id[t][c];
+    if (!((S.kept[t] >> (c / keep)) & 1) || !((S.mask[t][e >> 5] >> (e & 31)) & 1)) continue;
+    const int j = place(S.mask[t], e), a = 1 + place(S.active, e);
+    S.chosen[t][j] = (int16_t)e;
+    S.gate[t][j] = S.sig[t][e];
     P.expert[a] = e;
     P.slot[a][t] = (uint8_t)j;
   }
-  if (tid < p.T) P.slot[n][tid] = (uint8_t)p.k;
+  if (tid < p.T) P.slot[0][tid] = (uint8_t)p.k;
   if (tid == 0) {
-    P.n_active = n + 1;
-    P.expert[n] = p.E;
+    int n = 1;
+    for (int i = 0; i < FW_MAX_E / 32; ++i) n += __popc(S.active[i]);
+    P.n_active = n;
+    P.expert[0] = p.E;
+  }
+  __syncthreads();
+  for (int i = tid; i < p.T * (p.k + 1); i += FW_THREADS) {
+    const int t = i / (p.k + 1), j = i - t * (p.k + 1);
+    float w = 1.0f;
+    if (j < p.k) {
+      double total = 0.0;
+      for (int o = 0; o < p.k; ++o) total += S.gate[t][o];
+      w = (float)(p.route_scale * S.gate[t][j] / total);
+      if (write_out) {
+        p.w[t * p.k + j] = w;
+        p.idx[t * p.k + j] = S.chosen[t][j];
+      }
+    }
+    P.gate[i] = w;
   }
   __syncthreads();
 }
 
 // ---- kernel 2: selection, then h = SiLU(G) U in FP32 ----
 // Item i: active expert i / (f/8), h columns 8 (i % (f/8)) .. +7.  Wave w owns
-// the K blocks w, w + 8, ... (NB of them at most): their activations and
-// scales stay in registers, and as each block's weights are consumed the next
-// item's are loaded into their place.
+// the K blocks w, w + 8, ... (NB = ceil(d/1024) of them): their activations
+// and scales stay in registers, and as each block's weights are consumed the
+// next item's are loaded into their place.  Nothing in that loop branches
+// around a load: the compiler counts outstanding loads along straight-line
+// code only, and a load that may or may not have been issued makes it wait for
+// all of them (measured: 3.8 TB/s with such branches).  So a wave's missing
+// last block repeats a present one with a scale of 0, and the last item has
+// code of its own.
+//
+// The products run as BF16 MFMAs on weights widened in registers (E4M3 values
+// are exact in BF16): the FP8 MFMA's sums of 128 products carry an error of
+// 2.0e-6 RMS of sum|a b|, which moves one h in some hundreds across a rounding
+// midpoint of E4M3; the BF16 MFMA's carry 1.3e-9 (both measured over 131072
+// sums).  The conversions hide behind the weight stream.
+__device__ __forceinline__ v8bf widen8(int lo, int hi) {
+  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+  const v2bf a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
+  const v2bf b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+  const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
+  const v2bf d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+  return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
 template <int NB>
 __global__ __launch_bounds__(FW_THREADS, 1) void few_up_kernel(const FewArgs p) {
   __shared__ SelectLds S;
@@ -344,63 +391,73 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_up_kernel(const FewArgs p) 
   const int g16 = lane >> 4, r16 = lane & 15;
   const int KB = p.d / 128, FB = p.f / 128;
 
+  const int per = p.f / 8;
+  // activations of this wave's blocks, widened; tokens past T repeat the last
+  v8bf xb[NB][4];
+  float xs[NB];
+  int kb[NB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    const bool mine = wave + 8 * j < KB;
+    kb[j] = mine ? wave + 8 * j : KB - 1;
+    const int t = min(r16, p.T - 1);
+    const v8i x = row_frag(p.xq + (size_t)t * p.d + kb[j] * 128 + g16 * 32);
+    xs[j] = mine ? p.xs[t * KB + kb[j]] : 0.0f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) xb[j][q] = widen8(x[2 * q], x[2 * q + 1]);
+  }
+  const size_t up = (size_t)p.f * p.d;   // from a gate row to its up row
+  const uint8_t* lane_w = p.w13 + (size_t)(r16 & 7) * p.d + (2 * g16 + (r16 >> 3)) * 16;
+  const float* lane_s = p.w13_s + (size_t)(g16 < 2 ? 0 : FB) * KB;
+  Lines b[NB];
+  float sw[NB];
+  auto bases = [&](int e, int n8, const uint8_t*& wp, const float*& sp) {
+    wp = lane_w + ((size_t)e * 2 * p.f + n8 * 8) * p.d;
+    sp = lane_s + ((size_t)e * 2 * FB + n8 / 16) * KB;
+  };
+  auto load = [&](int j, const uint8_t* wp, const float* sp) {
+    b[j] = load_weight(wp + kb[j] * 128, wp + up + kb[j] * 128);
+    sw[j] = sp[kb[j]];
+  };
+  // the first `per` items are the shared expert's, known before the selection:
+  // their loads run beneath it
+  int item = blockIdx.x, n = 0;
+  const uint8_t* wp;
+  const float* sp;
+  if (item < per) {
+    bases(p.E, item, wp, sp);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) load(j, wp, sp);
+  }
   few_select(p, S, P, blockIdx.x == 0);
   if (blockIdx.x == 0)
     for (int i = tid; i < (int)(sizeof(FewPlan) / 4); i += FW_THREADS)
       reinterpret_cast<uint32_t*>(p.plan)[i] = reinterpret_cast<const uint32_t*>(&P)[i];
-
-  v8i xf[NB];
-  float xs[NB];
+  const int total = __builtin_amdgcn_readfirstlane(P.n_active) * per;
+  if (item >= total) return;
+  if (item >= per) {
+    const int a = item / per;
+    bases(__builtin_amdgcn_readfirstlane(P.expert[a]), item - a * per, wp, sp);
 #pragma unroll
-  for (int j = 0; j < NB; ++j) {
-    const int kb = wave + 8 * j;
-    xf[j] = v8i{0, 0, 0, 0, 0, 0, 0, 0};
-    xs[j] = 0.0f;
-    if (kb < KB && r16 < p.T) {
-      xf[j] = row_frag(p.xq + (size_t)r16 * p.d + kb * 128 + g16 * 32);
-      xs[j] = p.xs[r16 * KB + kb];
-    }
+    for (int j = 0; j < NB; ++j) load(j, wp, sp);
   }
-  const int per = p.f / 8, total = P.n_active * per;
-  const size_t lane_off = (size_t)(r16 & 7) * p.d + (2 * g16 + (r16 >> 3)) * 16 + wave * 128;
-  Lines b[NB];
-  float sw[NB];
-  auto bases = [&](int item, const uint8_t*& wp, const float*& sp) {
-    const int a = item / per, n8 = item - a * per, e = __builtin_amdgcn_readfirstlane(P.expert[a]);
-    wp = p.w13 + ((size_t)e * 2 * p.f + n8 * 8) * p.d + lane_off;
-    sp = p.w13_s + ((size_t)e * 2 * FB + (g16 < 2 ? 0 : FB) + n8 / 16) * KB + wave;
-  };
-  const size_t up = (size_t)p.f * p.d;   // from a gate row to its up row
-  int item = blockIdx.x;
-  if (item < total) {
-    const uint8_t* wp;
-    const float* sp;
-    bases(item, wp, sp);
-#pragma unroll
-    for (int j = 0; j < NB; ++j)
-      if (wave + 8 * j < KB) {
-        b[j] = load_weight(wp + j * 1024, wp + up + j * 1024);
-        sw[j] = sp[8 * j];
-      }
-  }
-  for (int n = 0; item < total; ++n) {
+  auto run = [&](auto more) {           // one item; `more`: another follows
     const int next = item + gridDim.x;
-    const uint8_t* wp = nullptr;
-    const float* sp = nullptr;
-    if (next < total) bases(next, wp, sp);
+    if (more) {
+      const int a = next / per;
+      bases(__builtin_amdgcn_readfirstlane(P.expert[a]), next - a * per, wp, sp);
+    }
     v4f acc = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-      if (wave + 8 * j < KB) {
-        const v4f q = mfma_fp8_16x16x128(weight_frag(b[j]), xf[j], v4f{0.f, 0.f, 0.f, 0.f});
-        const float s = sw[j] * xs[j];
-        if (next < total) {
-          b[j] = load_weight(wp + j * 1024, wp + up + j * 1024);
-          sw[j] = sp[8 * j];
-        }
+      const v8i w = weight_frag(b[j]);
+      const float s = sw[j] * xs[j];
+      if (more) load(j, wp, sp);
+      v4f q = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = fmaf(q[i], s, acc[i]);
-      }
+      for (int i = 0; i < 4; ++i) q = mfma_bf16_16x16x32(widen8(w[2 * i], w[2 * i + 1]), xb[j][i], q);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] = fmaf(q[i], s, acc[i]);
     }
     // The waves' partial sums through LDS, in two halves in turn: one barrier
     // per item, since a half is written again only after the next item's
@@ -427,94 +484,141 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_up_kernel(const FewArgs p) 
       }
     }
     item = next;
-  }
+    ++n;
+  };
+  while (item + (int)gridDim.x < total) run(std::true_type{});
+  run(std::false_type{});
 }
 
-// ---- kernel 3: the 1x128 tiles of h (one per 16 lanes) ----
+// ---- the 1x128 tiles of h: 16 lanes per tile, 8 elements each ----
+// Codes into q; returns the scale.  The quotients are correctly rounded, as
+// fp8_quant_1x128's (by Divider, whose reciprocal and remainders are normal
+// numbers for s >= 2^-60; smaller scales take the plain division).
 template <bool POW2>
-__global__ __launch_bounds__(256) void few_quant_kernel(const FewArgs p) {
-  const int FB = p.f / 128;
-  const int tile = blockIdx.x * 16 + (threadIdx.x >> 4), sub = threadIdx.x & 15;
-  if (tile >= p.T * (p.k + 1) * FB) return;
-  const float4 lo = *reinterpret_cast<const float4*>(p.h + (size_t)tile * 128 + sub * 8);
-  const float4 hi = *reinterpret_cast<const float4*>(p.h + (size_t)tile * 128 + sub * 8 + 4);
-  const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+__device__ __forceinline__ float quant_h(const float* h, uint2& q) {
+  const float4 lo = *reinterpret_cast<const float4*>(h);
+  const float4 hi = *reinterpret_cast<const float4*>(h + 4);
+  float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
   float amax = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
   const float s = tile_scale<POW2>(amax);
+  if (s >= 0x1p-60f) {
+    const Divider div(s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = div(v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = v[i] / s;
+  }
+  q.x = f32x4_to_e4m3(v[0], v[1], v[2], v[3]);
+  q.y = f32x4_to_e4m3(v[4], v[5], v[6], v[7]);
+  return s;
+}
+
+// ---- kernel 3, for batches whose h few_down_kernel does not stage ----
+template <bool POW2>
+__global__ __launch_bounds__(256) void few_quant_kernel(const FewArgs p) {
+  const int FB = p.f / 128;
+  const int tile = blockIdx.x * 16 + (threadIdx.x >> 4), sub = threadIdx.x & 15;
+  if (tile >= p.T * (p.k + 1) * FB) return;
   uint2 q;
-  q.x = f32x4_to_e4m3(v[0] / s, v[1] / s, v[2] / s, v[3] / s);
-  q.y = f32x4_to_e4m3(v[4] / s, v[5] / s, v[6] / s, v[7] / s);
+  const float s = quant_h<POW2>(p.h + (size_t)tile * 128 + sub * 8, q);
   *reinterpret_cast<uint2*>(p.hq + (size_t)tile * 128 + sub * 8) = q;
   if (sub == 0) p.hsg[tile] = s * p.plan->gate[tile / FB];
 }
 
 // ---- kernel 4: out = sum over active experts of gate W2 h, + residual ----
-// Item i: output columns 16 i .. +15.  The steps (active expert, K block) are
-// dealt to the waves in turn; each keeps FW_RING steps of loads in flight.
+// Workgroup b owns an even share of the output columns, in units of 4, and
+// takes them 16 at a time (the last time what is left, its missing fragment
+// rows repeating the last).  A pass's steps (active expert, U adjacent K
+// blocks) are dealt to the waves in turn, `per` to each (steps past the last
+// repeat it and add nothing).  The passes follow each other as one stream of
+// steps with RING of them in flight per wave; loads are free of branches
+// except in the stream's last steps, for the reason above.
+//
+// STAGE: the workgroup quantises h itself, into LDS, beneath its first weight
+// loads; otherwise the tiles come from few_quant_kernel through memory.
+constexpr int FW_STAGE_BYTES = 96 * 1024;
+
+template <int U, bool STAGE>
+struct DownStep {
+  Lines b[U];
+  float sw[U];
+  v8i hf[STAGE ? 1 : U];
+  float sh[STAGE ? 1 : U];
+  int hrow;       // row of h for this lane's token
+  int kb;
+  bool live;      // this lane's token chose the expert, and the step is no repeat
+};
+
+template <int U, int RING, bool STAGE, bool POW2>
 __global__ __launch_bounds__(FW_THREADS, 1) void few_down_kernel(const FewArgs p) {
   __shared__ FewPlan P;
-  __shared__ __attribute__((aligned(16))) v4f red[FW_WAVES][64];
+  __shared__ __attribute__((aligned(16))) v4f red[2][FW_WAVES][64];
+  __shared__ __attribute__((aligned(16))) uint8_t stage[STAGE ? FW_STAGE_BYTES : 16];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int g16 = lane >> 4, r16 = lane & 15;
-  const int FB = p.f / 128;
+  const int FB = p.f / 128, FU = FB / U;
   for (int i = tid; i < (int)(sizeof(FewPlan) / 4); i += FW_THREADS)
     reinterpret_cast<uint32_t*>(&P)[i] = reinterpret_cast<const uint32_t*>(p.plan)[i];
   __syncthreads();
-  const int steps = P.n_active * FB;
-  const size_t lane_off = (size_t)(r16 & 7) * p.f + (2 * g16 + (r16 >> 3)) * 16;
+  const int steps = __builtin_amdgcn_readfirstlane(P.n_active) * FU, per = (steps + 7) / 8;
+  const int units = p.d / 4;
+  const int c_begin = 4 * (int)((long)units * blockIdx.x / gridDim.x);
+  const int c_end = 4 * (int)((long)units * (blockIdx.x + 1) / gridDim.x);
+  const int count = (c_end - c_begin + 15) / 16 * per;   // steps of this wave's stream
+  // a step's expert: step / FU by a rounded-up reciprocal, exact for step * FU < 2^32
+  const uint32_t inv = (uint32_t)((0x100000000ull + FU - 1) / FU);
+  const uint8_t* lane_w = p.w2 + (2 * g16 + (r16 >> 3)) * 16;
+  const int hstride = p.f + 16;         // staged rows, 16 bytes apart in the banks
+  float* const stage_s = reinterpret_cast<float*>(stage + p.T * (p.k + 1) * hstride);
 
-  for (int item = blockIdx.x; item < p.d / 16; item += gridDim.x) {
-    struct Step {
-      Lines b;
-      v8i hf;
-      float s;
-      bool live;      // this lane's token chose the expert
-    } ring[FW_RING];
-    const uint8_t* wbase = p.w2 + (size_t)item * 16 * p.f + lane_off;
-    auto load = [&](Step& st, int step) {
-      const int a = step / FB, kb = step - a * FB;
-      const int e = __builtin_amdgcn_readfirstlane(P.expert[a]);
-      const uint8_t* wp = wbase + (size_t)e * p.d * p.f + kb * 128;
-      st.b = load_weight(wp, wp + (size_t)8 * p.f);
-      const int slot = P.slot[a][r16];
-      st.hf = v8i{0, 0, 0, 0, 0, 0, 0, 0};
-      st.s = 0.0f;
-      st.live = slot != 255;
-      if (st.live) {
-        const int row = r16 * (p.k + 1) + slot;
-        st.hf = row_frag(p.hq + (size_t)row * p.f + kb * 128 + g16 * 32);
-        st.s = p.hsg[row * FB + kb] * p.w2_s[((size_t)e * (p.d / 128) + item / 8) * FB + kb];
-      }
-    };
-    v4f acc = v4f{0.f, 0.f, 0.f, 0.f};
+  DownStep<U, STAGE> ring[RING];
+  int lc = c_begin, lk = 0;             // the next load's first column and step within the pass
+  auto load = [&](DownStep<U, STAGE>& st) {
+    const int raw = wave + 8 * lk, step = min(raw, steps - 1);
+    const int a = FU == 1 ? step : (int)__umulhi((uint32_t)step, inv), kb = (step - a * FU) * U;
+    const int e = __builtin_amdgcn_readfirstlane(P.expert[a]);
+    const int r0 = min(lc + (r16 & 7), c_end - 1), r1 = min(lc + 8 + (r16 & 7), c_end - 1);
+    const uint8_t* wp = lane_w + (size_t)e * p.d * p.f + kb * 128;
+    const float* sp = p.w2_s + ((size_t)e * (p.d / 128) + min(lc + 4 * g16, c_end - 1) / 128) * FB + kb;
+    const uint8_t* w0 = wp + (size_t)r0 * p.f;
+    const uint8_t* w1 = wp + (size_t)r1 * p.f;
 #pragma unroll
-    for (int r = 0; r < FW_RING; ++r)
-      if (wave + 8 * r < steps) load(ring[r], wave + 8 * r);
-    for (int s0 = wave; s0 < steps; s0 += 8 * FW_RING) {
+    for (int q = 0; q < U; ++q) {
+      st.b[q] = load_weight(w0 + q * 128, w1 + q * 128);
+      st.sw[q] = sp[q];
+    }
+    const int slot = P.slot[a][r16];
+    st.live = slot != 255 && raw < steps;
+    // lanes without a token of this expert all read one row, so that they add one line to the load
+    st.hrow = slot != 255 ? r16 * (p.k + 1) + slot : p.k;
+    st.kb = kb;
+    if (!STAGE) {
 #pragma unroll
-      for (int r = 0; r < FW_RING; ++r) {
-        const int step = s0 + 8 * r;
-        if (step < steps) {
-          const v4f q = mfma_fp8_16x16x128(weight_frag(ring[r].b), ring[r].hf, v4f{0.f, 0.f, 0.f, 0.f});
-          const float s = ring[r].s;
-          const bool live = ring[r].live;   // other tokens take nothing, not even a NaN weight's product with 0
-          if (step + 8 * FW_RING < steps) load(ring[r], step + 8 * FW_RING);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[i] = live ? fmaf(q[i], s, acc[i]) : acc[i];
-        }
+      for (int q = 0; q < U; ++q) {
+        st.hf[q] = row_frag(p.hq + (size_t)st.hrow * p.f + (kb + q) * 128 + g16 * 32);
+        st.sh[q] = p.hsg[st.hrow * FB + kb + q];
       }
     }
-    red[wave][lane] = acc;
-    __syncthreads();
-    if (wave == 0 && r16 < p.T) {
-      v4f s = red[0][lane];
+    if (++lk == per) {
+      lk = 0;
+      lc += 16;
+    }
+  };
+  v4f acc = v4f{0.f, 0.f, 0.f, 0.f};
+  int col = c_begin, k = 0, n = 0;      // the next consumed step's
+  auto finish = [&]() {
+    red[n & 1][wave][lane] = acc;
+    lds_barrier();                      // halves in turn: see few_up_kernel
+    if (wave == (n & 7) && r16 < p.T && col + 4 * g16 < c_end) {
+      v4f s = red[n & 1][0][lane];
 #pragma unroll
-      for (int v = 1; v < FW_WAVES; ++v) s += red[v][lane];
-      const size_t at = (size_t)r16 * p.d + item * 16 + g16 * 4;
+      for (int v = 1; v < FW_WAVES; ++v) s += red[n & 1][v][lane];
+      const size_t at = (size_t)r16 * p.d + col + g16 * 4;
       if (p.residual) {
         const uint2 r = *reinterpret_cast<const uint2*>(p.residual + at);
         s[0] += __uint_as_float(r.x << 16);
@@ -527,7 +631,52 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_down_kernel(const FewArgs p
       o.y = (uint32_t)f32_to_bf16(s[2]) | ((uint32_t)f32_to_bf16(s[3]) << 16);
       *reinterpret_cast<uint2*>(p.out + at) = o;
     }
-    __syncthreads();
+    acc = v4f{0.f, 0.f, 0.f, 0.f};
+    k = 0;
+    col += 16;
+    ++n;
+  };
+  auto use = [&](const DownStep<U, STAGE>& st, auto&& refill) {
+    v4f q[U];
+    float s[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const v8i h = STAGE ? row_frag(stage + st.hrow * hstride + (st.kb + i) * 128 + g16 * 32) : st.hf[STAGE ? 0 : i];
+      s[i] = (STAGE ? stage_s[st.hrow * FB + st.kb + i] : st.sh[STAGE ? 0 : i]) * st.sw[i];
+      q[i] = mfma_fp8_16x16x128(weight_frag(st.b[i]), h, v4f{0.f, 0.f, 0.f, 0.f});
+    }
+    const bool live = st.live;   // other tokens take nothing, not even a NaN weight's product with 0
+    refill();
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[j] = live ? fmaf(q[i][j], s[i], acc[j]) : acc[j];
+    if (++k == per) finish();
+  };
+#pragma unroll
+  for (int r = 0; r < RING; ++r)
+    if (r < count) load(ring[r]);
+  if (STAGE) {
+    for (int tile = tid >> 4; tile < p.T * (p.k + 1) * FB; tile += FW_THREADS / 16) {
+      const int row = tile / FB, sub = tid & 15;
+      uint2 q;
+      const float s = quant_h<POW2>(p.h + (size_t)tile * 128 + sub * 8, q);
+      *reinterpret_cast<uint2*>(stage + row * hstride + (tile - row * FB) * 128 + sub * 8) = q;
+      if (sub == 0) stage_s[tile] = s * P.gate[row];
+    }
+    lds_barrier();
+  }
+  int u = 0;
+  for (; u + 2 * RING <= count; u += RING) {
+#pragma unroll
+    for (int r = 0; r < RING; ++r) use(ring[r], [&] { load(ring[r]); });
+  }
+  for (; u < count; u += RING) {
+#pragma unroll
+    for (int r = 0; r < RING; ++r)
+      if (u + r < count) use(ring[r], [&] {
+        if (u + r + RING < count) load(ring[r]);
+      });
   }
 }
 
@@ -540,31 +689,56 @@ hipError_t launch_layer_few(const uint16_t* x, const uint16_t* wg, const float* 
                             const uint8_t* w2, const float* w2_s, const uint16_t* residual, int32_t* idx, float* w,
                             uint16_t* out, void* workspace, bool pow2, hipStream_t stream) {
   const FewLayout L = few_layout(T, d, f, E, k);
+  // parts of d: enough workgroups to spread the router's rows, few enough that
+  // every workgroup of the next kernel adds them up quickly
+  const int splits = std::max(1, std::min(d / 32 / FR_WAVES, T <= 4 ? FR_MAX_SPLITS : 32 / T));
   char* ws = static_cast<char*>(workspace);
   FewArgs p{T, d, f, E, G, M, k, (double)route_scale, x, wg, bias, w13, w13_s, w2, w2_s, residual, idx, w, out,
-            reinterpret_cast<double*>(ws + L.sig), reinterpret_cast<uint8_t*>(ws + L.xq),
+            splits, reinterpret_cast<double*>(ws + L.part), reinterpret_cast<uint8_t*>(ws + L.xq),
             reinterpret_cast<float*>(ws + L.xs), reinterpret_cast<float*>(ws + L.h),
             reinterpret_cast<uint8_t*>(ws + L.hq), reinterpret_cast<float*>(ws + L.hsg),
             reinterpret_cast<FewPlan*>(ws + L.plan)};
   const int KB = d / 128, FB = f / 128;
-  const dim3 g1(E + (T * KB + 15) / 16), g3((T * (k + 1) * FB + 15) / 16);
-  if (pow2) hipLaunchKernelGGL(few_route_kernel<true>, g1, dim3(256), 0, stream, p);
-  else hipLaunchKernelGGL(few_route_kernel<false>, g1, dim3(256), 0, stream, p);
+  const dim3 g1((E + 15) / 16 * splits + (T * KB + FR_THREADS / 16 - 1) / (FR_THREADS / 16)), g3((T * (k + 1) * FB + 15) / 16);
+  if (pow2) hipLaunchKernelGGL(few_route_kernel<true>, g1, dim3(FR_THREADS), 0, stream, p);
+  else hipLaunchKernelGGL(few_route_kernel<false>, g1, dim3(FR_THREADS), 0, stream, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   // no more workgroups than items (each active expert has f/8)
   const dim3 g2(std::min(256, std::min(E, T * k) * (f / 8) + f / 8));
-  if (KB <= 8) hipLaunchKernelGGL(few_up_kernel<1>, g2, dim3(FW_THREADS), 0, stream, p);
-  else if (KB <= 16) hipLaunchKernelGGL(few_up_kernel<2>, g2, dim3(FW_THREADS), 0, stream, p);
-  else if (KB <= 32) hipLaunchKernelGGL(few_up_kernel<4>, g2, dim3(FW_THREADS), 0, stream, p);
-  else hipLaunchKernelGGL(few_up_kernel<8>, g2, dim3(FW_THREADS), 0, stream, p);
+  switch ((KB + 7) / 8) {
+    case 1: hipLaunchKernelGGL(few_up_kernel<1>, g2, dim3(FW_THREADS), 0, stream, p); break;
+    case 2: hipLaunchKernelGGL(few_up_kernel<2>, g2, dim3(FW_THREADS), 0, stream, p); break;
+    case 3: hipLaunchKernelGGL(few_up_kernel<3>, g2, dim3(FW_THREADS), 0, stream, p); break;
+    case 4: hipLaunchKernelGGL(few_up_kernel<4>, g2, dim3(FW_THREADS), 0, stream, p); break;
+    case 5: hipLaunchKernelGGL(few_up_kernel<5>, g2, dim3(FW_THREADS), 0, stream, p); break;
+    case 6: hipLaunchKernelGGL(few_up_kernel<6>, g2, dim3(FW_THREADS), 0, stream, p); break;
+    case 7: hipLaunchKernelGGL(few_up_kernel<7>, g2, dim3(FW_THREADS), 0, stream, p); break;
+    default: hipLaunchKernelGGL(few_up_kernel<8>, g2, dim3(FW_THREADS), 0, stream, p); break;
+  }
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (pow2) hipLaunchKernelGGL(few_quant_kernel<true>, g3, dim3(256), 0, stream, p);
-  else hipLaunchKernelGGL(few_quant_kernel<false>, g3, dim3(256), 0, stream, p);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(few_down_kernel, dim3(std::min(256, d / 16)), dim3(FW_THREADS), 0, stream, p);
+  const int rows = T * (k + 1);
+  const bool stage = (long)rows * (f + 16 + FB * 4) <= FW_STAGE_BYTES;
+  if (!stage) {
+    if (pow2) hipLaunchKernelGGL(few_quant_kernel<true>, g3, dim3(256), 0, stream, p);
+    else hipLaunchKernelGGL(few_quant_kernel<false>, g3, dim3(256), 0, stream, p);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const dim3 g4(std::min(256, d / 4));
+#define MOE_FEW_DOWN(U, RING, STAGE, POW2) \
+  hipLaunchKernelGGL((few_down_kernel<U, RING, STAGE, POW2>), g4, dim3(FW_THREADS), 0, stream, p)
+  if (FB % 2 == 0) {
+    if (!stage) MOE_FEW_DOWN(2, 4, false, false);
+    else if (pow2) MOE_FEW_DOWN(2, 6, true, true);
+    else MOE_FEW_DOWN(2, 6, true, false);
+  } else {
+    if (!stage) MOE_FEW_DOWN(1, 8, false, false);
+    else if (pow2) MOE_FEW_DOWN(1, 12, true, true);
+    else MOE_FEW_DOWN(1, 12, true, false);
+  }
+#undef MOE_FEW_DOWN
   return hipGetLastError();
 }
 

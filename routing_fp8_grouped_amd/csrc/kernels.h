@@ -97,6 +97,7 @@ hipError_t launch_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const 
 // The whole layer for a few tokens (few.hip).
 constexpr int kFewMaxT = 16;
 constexpr int kFewMaxD = 8192;
+constexpr int kFewMaxF = 32768;
 size_t layer_few_workspace_bytes(int T, int d, int f, int E, int k);
 hipError_t launch_layer_few(const uint16_t* x, const uint16_t* wg, const float* bias, int T, int d, int f, int E,
                             int G, int M, int k, float route_scale, const uint8_t* w13, const float* w13_s,
