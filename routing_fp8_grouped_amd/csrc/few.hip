@@ -90,7 +90,9 @@ struct FewArgs {
   int32_t* idx;
   float* w;
   uint16_t* out;
-  int splits;       // parts of d in the logits' partial sums
+  int splits;       // parts of d in the logits' partial sums: 8, 4 or 2
+  int e_log2;       // experts and candidates of a token, rounded up to powers of two
+  int c_log2;
   double* part;     // [splits, T, E] partial logits
   uint8_t* xq;      // [T, d]
   float* xs;        // [T, d/128]
@@ -227,93 +229,154 @@ __global__ __launch_bounds__(FR_THREADS) void few_route_kernel(const FewArgs p) 
 
 // ---- selection, by a whole workgroup, (token, expert) pairs over its threads ----
 struct SelectLds {
+  uint64_t key[FW_T][FW_MAX_E];          // score order, then lower index: larger is better
+  uint64_t best[FW_T][FW_MAX_E];         // [group][rank]: keys of each group's best, in order
   double z[FW_T][FW_MAX_E];              // biased scores
   double sig[FW_T][FW_MAX_E];            // affinities
-  double best[FW_T][FW_MAX_E];           // [group][rank]: each group's best, in order
   double group[FW_T][64];
   double gate[FW_T][FW_MAX_K];
   uint64_t kept[FW_T];                   // groups kept
   uint32_t mask[FW_T][FW_MAX_E / 32];    // experts chosen
   uint32_t active[FW_MAX_E / 32];        // experts any token chose
-  uint16_t id[FW_T][FW_MAX_E];           // of best
   int16_t chosen[FW_T][FW_MAX_K];        // ascending
 };
 
+// The partial logits of this thread's (token, expert) pairs: pair tid + 512 i
+// of the tokens' rows of 2^e_log2.  `splits` parts of 16 / splits pairs each
+// way are 16 loads, issued before the first weights (behind which they would
+// queue for 4 us) and added up after.
+struct PartialLogits {
+  double v[16];
+
+  template <int SPLITS>
+  __device__ __forceinline__ void load_as(const FewArgs& p) {
+#pragma unroll
+    for (int i = 0; i < 16 / SPLITS; ++i) {
+      const int at = threadIdx.x + FW_THREADS * i, t = min(at >> p.e_log2, p.T - 1);
+      const int e = min(at & ((1 << p.e_log2) - 1), p.E - 1);
+#pragma unroll
+      for (int s = 0; s < SPLITS; ++s) v[i * SPLITS + s] = p.part[((size_t)s * p.T + t) * p.E + e];
+    }
+  }
+  __device__ __forceinline__ void load(const FewArgs& p) {
+    if (p.splits == 8) load_as<8>(p);
+    else if (p.splits == 4) load_as<4>(p);
+    else load_as<2>(p);
+  }
+  // l[i]: the logit of pair i (i < 16 / splits)
+  template <int SPLITS>
+  __device__ __forceinline__ void sum_as(double (&l)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 16 / SPLITS; ++i) {
+      l[i] = v[i * SPLITS];
+#pragma unroll
+      for (int s = 1; s < SPLITS; ++s) l[i] += v[i * SPLITS + s];
+    }
+  }
+  __device__ __forceinline__ void sum(int splits, double (&l)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) l[i] = 0.0;
+    if (splits == 8) sum_as<8>(l);
+    else if (splits == 4) sum_as<4>(l);
+    else sum_as<2>(l);
+  }
+};
+
+// Doubles in an unsigned order, the low byte giving way to 255 - e: keys are
+// distinct, equal scores rank by the lower index, and a score moves by at most
+// 2^-44 of itself, far below the logits' own error.  NaN scores rank last, so
+// every index below stays in range whatever the inputs.
+__device__ __forceinline__ uint64_t score_key(double z, int e) {
+  if (!(z == z)) z = -__builtin_huge_val();
+  uint64_t u = (uint64_t)__double_as_longlong(z + 0.0);   // -0 as +0
+  u = (u >> 63) ? ~u : u | 0x8000000000000000ull;
+  return (u & ~255ull) | (uint32_t)(255 - e);
+}
+__device__ __forceinline__ int key_expert(uint64_t k) { return 255 - (int)(k & 255); }
+
+// Entries of list[0..n) above k.
+__device__ __forceinline__ int count_above(const uint64_t* list, int n, uint64_t k) {
+  int r = 0;
+#pragma unroll 8
+  for (int i = 0; i < n; ++i) r += list[i] > k ? 1 : 0;
+  return r;
+}
+
 // The batch's plan in LDS.  Ranks are counted, not sorted: an expert's rank in
 // its group is the number of better ones there; the best min(k, group size) of
-// each group, in order, are all that the later steps read.  NaN scores rank
-// last, so every index stays in range whatever the inputs.
-__device__ void few_select(const FewArgs& p, SelectLds& S, FewPlan& P, bool write_out) {
+// each group, in order, are all that the later steps read.
+__device__ void few_select(const FewArgs& p, SelectLds& S, FewPlan& P, const PartialLogits& part, bool write_out) {
   const int tid = threadIdx.x;
   const int per = p.E / p.G, n_top = p.k / p.M, keep = min(p.k, per), cand = p.G * keep;
-  for (int i = tid; i < p.T * p.E; i += FW_THREADS) {
-    const int t = i / p.E, e = i - t * p.E;
-    double l = p.part[i];
-    for (int q = 1; q < p.splits; ++q) l += p.part[(size_t)q * p.T * p.E + i];
-    const double s = 1.0 / (1.0 + exp(-l)), v = s + (p.bias ? (double)p.bias[e] : 0.0);
-    S.sig[t][e] = s;
-    S.z[t][e] = v == v ? v : -__builtin_huge_val();
+  // i / per and i / keep for i < 256 by 16-bit reciprocals (exact: the error 255 / 65536 is below 1 / 256)
+  const uint32_t inv_per = (65536 + per - 1) / per, inv_keep = (65536 + keep - 1) / keep;
+  const int e_mask = (1 << p.e_log2) - 1, c_mask = (1 << p.c_log2) - 1;
+  const int pairs = p.T << p.e_log2, cands = p.T << p.c_log2;
+  {
+    double l[8];
+    part.sum(p.splits, l);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int at = tid + FW_THREADS * i, t = at >> p.e_log2, e = at & e_mask;
+      if (at >= pairs) break;
+      if (e < p.E) {
+        const double s = 1.0 / (1.0 + exp(-l[i])), z = s + (p.bias ? (double)p.bias[e] : 0.0);
+        S.sig[t][e] = s;
+        S.z[t][e] = z;
+        S.key[t][e] = score_key(z, e);
+      }
+    }
   }
   if (tid < FW_MAX_E / 32) S.active[tid] = 0;
   if (tid < FW_T) S.kept[tid] = 0;
   if (tid < FW_T * FW_MAX_E / 32) S.mask[0][tid] = 0;
   for (int i = tid; i < (FW_MAX_E + 1) * FW_T / 4; i += FW_THREADS) reinterpret_cast<uint32_t*>(P.slot)[i] = ~0u;
-  __syncthreads();
-  for (int i = tid; i < p.T * p.E; i += FW_THREADS) {
-    const int t = i / p.E, e = i - t * p.E, g = e / per;
-    const double v = S.z[t][e];
-    int r = 0;
-#pragma unroll 8
-    for (int o = g * per; o < (g + 1) * per; ++o) {
-      const double ov = S.z[t][o];
-      r += (ov > v || (ov == v && o < e)) ? 1 : 0;
-    }
-    if (r < keep) {
-      S.best[t][g * keep + r] = v;
-      S.id[t][g * keep + r] = (uint16_t)e;
-    }
+  lds_barrier();
+  for (int at = tid; at < pairs; at += FW_THREADS) {
+    const int t = at >> p.e_log2, e = at & e_mask, g = (int)(e * inv_per >> 16);
+    if (e >= p.E) continue;
+    const uint64_t k = S.key[t][e];
+    const int r = count_above(&S.key[t][g * per], per, k);
+    if (r < keep) S.best[t][g * keep + r] = k;
   }
-  __syncthreads();
-  for (int i = tid; i < p.T * p.G; i += FW_THREADS) {
-    const int t = i / p.G, g = i - t * p.G;
+  lds_barrier();
+  for (int at = tid; at < p.T * 64; at += FW_THREADS) {
+    const int t = at >> 6, g = at & 63;
+    if (g >= p.G) continue;
     double s = 0.0;
-    for (int r = 0; r < n_top; ++r) s += S.best[t][g * keep + r];
+    for (int r = 0; r < n_top; ++r) s += S.z[t][key_expert(S.best[t][g * keep + r])];
     S.group[t][g] = s;
   }
-  __syncthreads();
-  for (int i = tid; i < p.T * p.G; i += FW_THREADS) {
-    const int t = i / p.G, g = i - t * p.G;
+  lds_barrier();
+  for (int at = tid; at < p.T * 64; at += FW_THREADS) {
+    const int t = at >> 6, g = at & 63;
+    if (g >= p.G) continue;
     const double s = S.group[t][g];
     int r = 0;
 #pragma unroll 8
     for (int o = 0; o < p.G; ++o) {
       const double os = S.group[t][o];
-      r += (os > s || (os == s && o < g)) ? 1 : 0;
+      // a NaN sum ranks last, among its like by index
+      r += (os > s || (s != s && os == os) || ((os == s || (s != s && os != os)) && o < g)) ? 1 : 0;
     }
     if (r < p.M) atomicOr(reinterpret_cast<unsigned long long*>(&S.kept[t]), 1ull << g);
   }
-  __syncthreads();
-  for (int i = tid; i < p.T * cand; i += FW_THREADS) {
-    const int t = i / cand, c = i - t * cand;
+  lds_barrier();
+  for (int at = tid; at < cands; at += FW_THREADS) {
+    const int t = at >> p.c_log2, c = at & c_mask, g = (int)(c * inv_keep >> 16);
     const uint64_t kept = S.kept[t];
-    if (!((kept >> (c / keep)) & 1)) continue;
-    const double v = S.best[t][c];
-    const int e = S.id[t][c];
-    int r = 0;
-    for (uint64_t m = kept; m; m &= m - 1) {
-      const int g = __ffsll((unsigned long long)m) - 1;
-#pragma unroll 8
-      for (int o = g * keep; o < (g + 1) * keep; ++o) {
-        const double ov = S.best[t][o];
-        r += (ov > v || (ov == v && S.id[t][o] < e)) ? 1 : 0;
-      }
-    }
+    if (c >= cand || !((kept >> g) & 1)) continue;
+    const uint64_t k = S.best[t][c];
+    int r = c - g * keep;
+    for (uint64_t m = kept & ~(1ull << g); m; m &= m - 1)
+      r += count_above(&S.best[t][(__ffsll((unsigned long long)m) - 1) * keep], keep, k);
     if (r < p.k) {
+      const int e = key_expert(k);
       atomicOr(&S.mask[t][e >> 5], 1u << (e & 31));
       atomicOr(&S.active[e >> 5], 1u << (e & 31));
     }
   }
-  __syncthreads();
+  lds_barrier();
   // position of expert e among a bit mask's, ascending
   auto place = [](const uint32_t* mask, int e) {
     int a = __popc(mask[e >> 5] & ((1u << (e & 31)) - 1u));
@@ -322,10 +385,11 @@ __device__ void few_select(const FewArgs& p, SelectLds& S, FewPlan& P, bool writ
     return a;
   };
   // a chosen expert is one of its group's best, so the candidates hold them all
-  for (int i = tid; i < p.T * cand; i += FW_THREADS) {
-    const int t = i / cand, c = i - t * cand;
-    const int e = S.id[t][c];
-    if (!((S.kept[t] >> (c / keep)) & 1) || !((S.mask[t][e >> 5] >> (e & 31)) & 1)) continue;
+  for (int at = tid; at < cands; at += FW_THREADS) {
+    const int t = at >> p.c_log2, c = at & c_mask, g = (int)(c * inv_keep >> 16);
+    if (c >= cand || !((S.kept[t] >> g) & 1)) continue;
+    const int e = key_expert(S.best[t][c]);
+    if (!((S.mask[t][e >> 5] >> (e & 31)) & 1)) continue;
     const int j = place(S.mask[t], e), a = 1 + place(S.active, e);
     S.chosen[t][j] = (int16_t)e;
     S.gate[t][j] = S.sig[t][e];
@@ -333,28 +397,31 @@ __device__ void few_select(const FewArgs& p, SelectLds& S, FewPlan& P, bool writ
     P.slot[a][t] = (uint8_t)j;
   }
   if (tid < p.T) P.slot[0][tid] = (uint8_t)p.k;
-  if (tid == 0) {
+  if (tid == FW_THREADS - 1) {
     int n = 1;
+#pragma unroll
     for (int i = 0; i < FW_MAX_E / 32; ++i) n += __popc(S.active[i]);
     P.n_active = n;
     P.expert[0] = p.E;
   }
-  __syncthreads();
-  for (int i = tid; i < p.T * (p.k + 1); i += FW_THREADS) {
-    const int t = i / (p.k + 1), j = i - t * (p.k + 1);
-    float w = 1.0f;
-    if (j < p.k) {
-      double total = 0.0;
-      for (int o = 0; o < p.k; ++o) total += S.gate[t][o];
-      w = (float)(p.route_scale * S.gate[t][j] / total);
-      if (write_out) {
+  lds_barrier();
+  // only workgroup 0's gates are read: by the later kernels, and by the caller
+  if (write_out) {
+    for (int at = tid; at < p.T * 32; at += FW_THREADS) {
+      const int t = at >> 5, j = at & 31;
+      if (j > p.k) continue;
+      float w = 1.0f;
+      if (j < p.k) {
+        double total = 0.0;
+        for (int o = 0; o < p.k; ++o) total += S.gate[t][o];
+        w = (float)(p.route_scale * S.gate[t][j] / total);
         p.w[t * p.k + j] = w;
         p.idx[t * p.k + j] = S.chosen[t][j];
       }
+      P.gate[t * (p.k + 1) + j] = w;
     }
-    P.gate[i] = w;
+    lds_barrier();
   }
-  __syncthreads();
 }
 
 // ---- kernel 2: selection, then h = SiLU(G) U in FP32 ----
@@ -384,16 +451,19 @@ __device__ __forceinline__ v8bf widen8(int lo, int hi) {
 
 template <int NB>
 __global__ __launch_bounds__(FW_THREADS, 1) void few_up_kernel(const FewArgs p) {
-  __shared__ SelectLds S;
+  __shared__ __attribute__((aligned(16))) SelectLds S;
   __shared__ FewPlan P;
-  __shared__ __attribute__((aligned(16))) v4f red[2][FW_WAVES][64];
+  // the waves' sums, where the selection's keys were (16 of their 32 KB)
+  v4f (*const red)[FW_WAVES][64] = reinterpret_cast<v4f(*)[FW_WAVES][64]>(&S.key);
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int g16 = lane >> 4, r16 = lane & 15;
   const int KB = p.d / 128, FB = p.f / 128;
 
   const int per = p.f / 8;
-  // activations of this wave's blocks, widened; tokens past T repeat the last
-  v8bf xb[NB][4];
+  PartialLogits part;
+  part.load(p);
+  // activations of this wave's blocks; tokens past T repeat the last
+  v8i xq[NB];
   float xs[NB];
   int kb[NB];
 #pragma unroll
@@ -401,10 +471,9 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_up_kernel(const FewArgs p) 
     const bool mine = wave + 8 * j < KB;
     kb[j] = mine ? wave + 8 * j : KB - 1;
     const int t = min(r16, p.T - 1);
-    const v8i x = row_frag(p.xq + (size_t)t * p.d + kb[j] * 128 + g16 * 32);
-    xs[j] = mine ? p.xs[t * KB + kb[j]] : 0.0f;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) xb[j][q] = widen8(x[2 * q], x[2 * q + 1]);
+    xq[j] = row_frag(p.xq + (size_t)t * p.d + kb[j] * 128 + g16 * 32);
+    xs[j] = p.xs[t * KB + kb[j]];
+    if (!mine) xs[j] = 0.0f;
   }
   const size_t up = (size_t)p.f * p.d;   // from a gate row to its up row
   const uint8_t* lane_w = p.w13 + (size_t)(r16 & 7) * p.d + (2 * g16 + (r16 >> 3)) * 16;
@@ -429,7 +498,12 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_up_kernel(const FewArgs p) 
 #pragma unroll
     for (int j = 0; j < NB; ++j) load(j, wp, sp);
   }
-  few_select(p, S, P, blockIdx.x == 0);
+  v8bf xb[NB][4];
+#pragma unroll
+  for (int j = 0; j < NB; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) xb[j][q] = widen8(xq[j][2 * q], xq[j][2 * q + 1]);
+  few_select(p, S, P, part, blockIdx.x == 0);
   if (blockIdx.x == 0)
     for (int i = tid; i < (int)(sizeof(FewPlan) / 4); i += FW_THREADS)
       reinterpret_cast<uint32_t*>(p.plan)[i] = reinterpret_cast<const uint32_t*>(&P)[i];
@@ -490,33 +564,40 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_up_kernel(const FewArgs p) 
   run(std::false_type{});
 }
 
-// ---- the 1x128 tiles of h: 16 lanes per tile, 8 elements each ----
-// Codes into q; returns the scale.  The quotients are correctly rounded, as
-// fp8_quant_1x128's (by Divider, whose reciprocal and remainders are normal
-// numbers for s >= 2^-60; smaller scales take the plain division).
-template <bool POW2>
-__device__ __forceinline__ float quant_h(const float* h, uint2& q) {
-  const float4 lo = *reinterpret_cast<const float4*>(h);
-  const float4 hi = *reinterpret_cast<const float4*>(h + 4);
-  float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-  float amax = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
-  const float s = tile_scale<POW2>(amax);
-  if (s >= 0x1p-60f) {
-    const Divider div(s);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = div(v[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = v[i] / s;
+// ---- a 1x128 tile of h: 16 lanes, 8 elements each ----
+struct HTile {
+  float v[8];
+
+  __device__ __forceinline__ void load(const float* h) {
+    const float4 lo = *reinterpret_cast<const float4*>(h);
+    const float4 hi = *reinterpret_cast<const float4*>(h + 4);
+    v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
+    v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
   }
-  q.x = f32x4_to_e4m3(v[0], v[1], v[2], v[3]);
-  q.y = f32x4_to_e4m3(v[4], v[5], v[6], v[7]);
-  return s;
-}
+  // Codes into q; returns the scale.  The quotients are correctly rounded, as
+  // fp8_quant_1x128's (by Divider, whose reciprocal and remainders are normal
+  // numbers for s >= 2^-60; smaller scales take the plain division).
+  template <bool POW2>
+  __device__ __forceinline__ float quantise(uint2& q) {
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
+    const float s = tile_scale<POW2>(amax);
+    if (s >= 0x1p-60f) {
+      const Divider div(s);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = div(v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = v[i] / s;
+    }
+    q.x = f32x4_to_e4m3(v[0], v[1], v[2], v[3]);
+    q.y = f32x4_to_e4m3(v[4], v[5], v[6], v[7]);
+    return s;
+  }
+};
 
 // ---- kernel 3, for batches whose h few_down_kernel does not stage ----
 template <bool POW2>
@@ -524,8 +605,10 @@ __global__ __launch_bounds__(256) void few_quant_kernel(const FewArgs p) {
   const int FB = p.f / 128;
   const int tile = blockIdx.x * 16 + (threadIdx.x >> 4), sub = threadIdx.x & 15;
   if (tile >= p.T * (p.k + 1) * FB) return;
+  HTile h;
+  h.load(p.h + (size_t)tile * 128 + sub * 8);
   uint2 q;
-  const float s = quant_h<POW2>(p.h + (size_t)tile * 128 + sub * 8, q);
+  const float s = h.template quantise<POW2>(q);
   *reinterpret_cast<uint2*>(p.hq + (size_t)tile * 128 + sub * 8) = q;
   if (sub == 0) p.hsg[tile] = s * p.plan->gate[tile / FB];
 }
@@ -559,12 +642,20 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_down_kernel(const FewArgs p
   __shared__ FewPlan P;
   __shared__ __attribute__((aligned(16))) v4f red[2][FW_WAVES][64];
   __shared__ __attribute__((aligned(16))) uint8_t stage[STAGE ? FW_STAGE_BYTES : 16];
+  constexpr int EARLY = 5;              // tiles of h a thread loads before the weights (9 rows of f 2048)
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int g16 = lane >> 4, r16 = lane & 15;
   const int FB = p.f / 128, FU = FB / U;
+  const int tiles = p.T * (p.k + 1) * FB;
   for (int i = tid; i < (int)(sizeof(FewPlan) / 4); i += FW_THREADS)
     reinterpret_cast<uint32_t*>(&P)[i] = reinterpret_cast<const uint32_t*>(p.plan)[i];
-  __syncthreads();
+  HTile early[STAGE ? EARLY : 1];
+  if (STAGE) {
+#pragma unroll
+    for (int i = 0; i < EARLY; ++i)
+      early[i].load(p.h + (size_t)min((tid >> 4) + i * (FW_THREADS / 16), tiles - 1) * 128 + (tid & 15) * 8);
+  }
+  lds_barrier();
   const int steps = __builtin_amdgcn_readfirstlane(P.n_active) * FU, per = (steps + 7) / 8;
   const int units = p.d / 4;
   const int c_begin = 4 * (int)((long)units * blockIdx.x / gridDim.x);
@@ -657,12 +748,22 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_down_kernel(const FewArgs p
   for (int r = 0; r < RING; ++r)
     if (r < count) load(ring[r]);
   if (STAGE) {
-    for (int tile = tid >> 4; tile < p.T * (p.k + 1) * FB; tile += FW_THREADS / 16) {
-      const int row = tile / FB, sub = tid & 15;
+    auto put = [&](int tile, HTile& h) {
+      const int row = tile / FB;
       uint2 q;
-      const float s = quant_h<POW2>(p.h + (size_t)tile * 128 + sub * 8, q);
-      *reinterpret_cast<uint2*>(stage + row * hstride + (tile - row * FB) * 128 + sub * 8) = q;
-      if (sub == 0) stage_s[tile] = s * P.gate[row];
+      const float s = h.template quantise<POW2>(q);
+      *reinterpret_cast<uint2*>(stage + row * hstride + (tile - row * FB) * 128 + (tid & 15) * 8) = q;
+      if ((tid & 15) == 0) stage_s[tile] = s * P.gate[row];
+    };
+#pragma unroll
+    for (int i = 0; i < EARLY; ++i) {
+      const int tile = (tid >> 4) + i * (FW_THREADS / 16);
+      if (tile < tiles) put(tile, early[i]);
+    }
+    for (int tile = (tid >> 4) + EARLY * (FW_THREADS / 16); tile < tiles; tile += FW_THREADS / 16) {
+      HTile h;
+      h.load(p.h + (size_t)tile * 128 + (tid & 15) * 8);
+      put(tile, h);
     }
     lds_barrier();
   }
@@ -689,12 +790,16 @@ hipError_t launch_layer_few(const uint16_t* x, const uint16_t* wg, const float* 
                             const uint8_t* w2, const float* w2_s, const uint16_t* residual, int32_t* idx, float* w,
                             uint16_t* out, void* workspace, bool pow2, hipStream_t stream) {
   const FewLayout L = few_layout(T, d, f, E, k);
-  // parts of d: enough workgroups to spread the router's rows, few enough that
-  // every workgroup of the next kernel adds them up quickly
-  const int splits = std::max(1, std::min(d / 32 / FR_WAVES, T <= 4 ? FR_MAX_SPLITS : 32 / T));
+  const int keep = std::min(k, E / G);
+  int e_log2 = 0, c_log2 = 0;
+  while ((1 << e_log2) < E) ++e_log2;
+  while ((1 << c_log2) < G * keep) ++c_log2;
+  // parts of d: as many as let a thread of the next kernel load all parts of its pairs by 16 loads
+  const int pairs = ((T << e_log2) + FW_THREADS - 1) / FW_THREADS;
+  const int splits = pairs <= 2 ? 8 : pairs <= 4 ? 4 : 2;
   char* ws = static_cast<char*>(workspace);
   FewArgs p{T, d, f, E, G, M, k, (double)route_scale, x, wg, bias, w13, w13_s, w2, w2_s, residual, idx, w, out,
-            splits, reinterpret_cast<double*>(ws + L.part), reinterpret_cast<uint8_t*>(ws + L.xq),
+            splits, e_log2, c_log2, reinterpret_cast<double*>(ws + L.part), reinterpret_cast<uint8_t*>(ws + L.xq),
             reinterpret_cast<float*>(ws + L.xs), reinterpret_cast<float*>(ws + L.h),
             reinterpret_cast<uint8_t*>(ws + L.hq), reinterpret_cast<float*>(ws + L.hsg),
             reinterpret_cast<FewPlan*>(ws + L.plan)};
