@@ -90,7 +90,7 @@ struct FewArgs {
   int32_t* idx;
   float* w;
   uint16_t* out;
-  int splits;       // parts of d in the logits' partial sums: 8, 4 or 2
+  int s_log2;       // parts of d in the logits' partial sums: 8, 4 or 2
   int e_log2;       // experts and candidates of a token, rounded up to powers of two
   int c_log2;
   double* part;     // [splits, T, E] partial logits
@@ -108,26 +108,46 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-__device__ __forceinline__ void wave_lds_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+// Weights come through buffer loads: a 64-bit base in scalar registers and a
+// 32-bit offset per lane, which keeps the address arithmetic off the vector
+// units, and a bound that turns a load into nothing.  A load of an empty
+// buffer, or at kNowhere, reads no memory and returns zeros, so the places
+// where a stream has nothing more to load need no branch.  That matters
+// twice: the compiler counts outstanding loads along straight-line code only,
+// and waits for all of them after a load that may not have been issued
+// (measured: 3.8 TB/s instead of 6.5); and a second copy of the loop for its
+// end would have to be fetched as code, at about 0.15 us per 128 bytes the
+// first time it is reached in a launch.
+constexpr uint32_t kNowhere = 0x7FFFFFF0u;
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+// The buffer of everything from a wave-uniform base on (offsets stay below
+// kNowhere), or an empty one.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* base, bool there) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(uniform_ptr(base)), 0, there ? 0x7FFFFFE0 : 0,
+                                           0x00020000);
 }
+__device__ __forceinline__ float load_scale(__amdgpu_buffer_rsrc_t b, uint32_t off) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(b, off, 0, 0));
+}
+
+// Nothing is scheduled across: left alone, the compiler gathers a loop's loads
+// at its end and waits for all of them at its beginning.
+__device__ __forceinline__ void pin_loads() { __builtin_amdgcn_sched_barrier(0); }
 
 // Weight fragment loads: 16 rows of 128 bytes as two whole-line loads (8 rows
 // each), then two DPP moves per register give the MFMA's operand layout.  Lane
 // (g, j) loads 16 bytes of chunk 2g + (j >= 8) from row j % 8 of each half;
 // rotating each 16-lane row by 8 and taking half of its lanes leaves lane
 // (g, j) with chunks 2g and 2g + 1 of fragment row j.
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-
 struct Lines {
   i32x4 x, y;
 };
 
-__device__ __forceinline__ Lines load_weight(const uint8_t* x, const uint8_t* y) {
-  return {__builtin_nontemporal_load(reinterpret_cast<const i32x4*>(x)),
-          __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(y))};
+__device__ __forceinline__ Lines load_weight(__amdgpu_buffer_rsrc_t b, uint32_t x, uint32_t y) {
+  constexpr int kNonTemporal = 2;
+  return {__builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(b, x, 0, kNonTemporal)),
+          __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(b, y, 0, kNonTemporal))};
 }
 
 __device__ __forceinline__ v8i weight_frag(const Lines& l) {
@@ -165,7 +185,7 @@ template <bool POW2>
 __global__ __launch_bounds__(FR_THREADS) void few_route_kernel(const FewArgs p) {
   __shared__ v4d red[FR_WAVES][64];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  const int router = (p.E + 15) / 16 * p.splits;
+  const int router = (p.E + 15) / 16 << p.s_log2;
   if ((int)blockIdx.x >= router) {
     const int tile = ((int)blockIdx.x - router) * (FR_THREADS / 16) + (tid >> 4);
     const int sub = tid & 15;
@@ -190,14 +210,14 @@ __global__ __launch_bounds__(FR_THREADS) void few_route_kernel(const FewArgs p) 
     if (sub == 0) p.xs[tile] = s;
     return;
   }
-  const int e0 = (int)blockIdx.x / p.splits * 16, split = (int)blockIdx.x % p.splits;
+  const int e0 = ((int)blockIdx.x >> p.s_log2) * 16, split = (int)blockIdx.x & ((1 << p.s_log2) - 1);
   const int r16 = lane & 15, g16 = lane >> 4;
   // rows past the last expert or token repeat it; their results are not stored
   const uint16_t* wr = p.wg + (size_t)min(e0 + r16, p.E - 1) * p.d + g16 * 8;
   const uint16_t* xr = p.x + (size_t)min(r16, p.T - 1) * p.d + g16 * 8;
   const int chunks = p.d / 32;
   v4d acc = v4d{0.0, 0.0, 0.0, 0.0};
-  const int stride = FR_WAVES * p.splits;   // the parts interleave
+  const int stride = FR_WAVES << p.s_log2;   // the parts interleave
   for (int c0 = split * FR_WAVES + wave; c0 < chunks; c0 += stride * FR_RING) {
     Bf16x8 a[FR_RING], b[FR_RING];
 #pragma unroll
@@ -242,43 +262,34 @@ struct SelectLds {
 };
 
 // The partial logits of this thread's (token, expert) pairs: pair tid + 512 i
-// of the tokens' rows of 2^e_log2.  `splits` parts of 16 / splits pairs each
-// way are 16 loads, issued before the first weights (behind which they would
-// queue for 4 us) and added up after.
+// of the tokens' rows of 2^e_log2, in 2^s_log2 parts each, 16 loads in all.
+// They are issued before the first weights (behind which they would queue for
+// 4 us) and added up after.
 struct PartialLogits {
   double v[16];
+  float bias;       // of this thread's expert, the same for all its pairs
 
-  template <int SPLITS>
-  __device__ __forceinline__ void load_as(const FewArgs& p) {
-#pragma unroll
-    for (int i = 0; i < 16 / SPLITS; ++i) {
-      const int at = threadIdx.x + FW_THREADS * i, t = min(at >> p.e_log2, p.T - 1);
-      const int e = min(at & ((1 << p.e_log2) - 1), p.E - 1);
-#pragma unroll
-      for (int s = 0; s < SPLITS; ++s) v[i * SPLITS + s] = p.part[((size_t)s * p.T + t) * p.E + e];
-    }
-  }
+
   __device__ __forceinline__ void load(const FewArgs& p) {
-    if (p.splits == 8) load_as<8>(p);
-    else if (p.splits == 4) load_as<4>(p);
-    else load_as<2>(p);
-  }
-  // l[i]: the logit of pair i (i < 16 / splits)
-  template <int SPLITS>
-  __device__ __forceinline__ void sum_as(double (&l)[8]) const {
+    const uint32_t e = min((int)threadIdx.x & ((1 << p.e_log2) - 1), p.E - 1);
+    const uint32_t t0 = threadIdx.x >> p.e_log2, dt = FW_THREADS >> p.e_log2;
 #pragma unroll
-    for (int i = 0; i < 16 / SPLITS; ++i) {
-      l[i] = v[i * SPLITS];
-#pragma unroll
-      for (int s = 1; s < SPLITS; ++s) l[i] += v[i * SPLITS + s];
+    for (int q = 0; q < 16; ++q) {
+      const uint32_t s = q & ((1 << p.s_log2) - 1), t = min(t0 + (q >> p.s_log2) * dt, (uint32_t)p.T - 1);
+      v[q] = p.part[(s * p.T + t) * p.E + e];
     }
+    bias = p.bias ? p.bias[e] : 0.0f;
   }
-  __device__ __forceinline__ void sum(int splits, double (&l)[8]) const {
+  // l[i]: the logit of pair i, i < 16 >> s_log2
+  __device__ __forceinline__ void sum(int s_log2, double (&l)[8]) const {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) l[i] = 0.0;
-    if (splits == 8) sum_as<8>(l);
-    else if (splits == 4) sum_as<4>(l);
-    else sum_as<2>(l);
+    for (int i = 0; i < 8; ++i) l[i] = v[2 * i] + v[2 * i + 1];
+    if (s_log2 > 1)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) l[i] = l[2 * i] + l[2 * i + 1];
+    if (s_log2 > 2)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) l[i] = l[2 * i] + l[2 * i + 1];
   }
 };
 
@@ -314,18 +325,21 @@ __device__ void few_select(const FewArgs& p, SelectLds& S, FewPlan& P, const Par
   const int pairs = p.T << p.e_log2, cands = p.T << p.c_log2;
   {
     double l[8];
-    part.sum(p.splits, l);
+    part.sum(p.s_log2, l);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int at = tid + FW_THREADS * i, t = at >> p.e_log2, e = at & e_mask;
-      if (at >= pairs) break;
-      if (e < p.E) {
-        const double s = 1.0 / (1.0 + exp(-l[i])), z = s + (p.bias ? (double)p.bias[e] : 0.0);
-        S.sig[t][e] = s;
-        S.z[t][e] = z;
-        S.key[t][e] = score_key(z, e);
-      }
+      const int at = tid + FW_THREADS * i;
+      if (at < pairs) S.z[at >> p.e_log2][at & e_mask] = l[i];
     }
+  }
+#pragma unroll 1
+  for (int at = tid; at < pairs; at += FW_THREADS) {   // one copy of exp; each thread's own entries
+    const int t = at >> p.e_log2, e = at & e_mask;
+    if (e >= p.E) continue;
+    const double s = 1.0 / (1.0 + exp(-S.z[t][e])), z = s + (double)part.bias;
+    S.sig[t][e] = s;
+    S.z[t][e] = z;
+    S.key[t][e] = score_key(z, e);
   }
   if (tid < FW_MAX_E / 32) S.active[tid] = 0;
   if (tid < FW_T) S.kept[tid] = 0;
@@ -428,12 +442,7 @@ __device__ void few_select(const FewArgs& p, SelectLds& S, FewPlan& P, const Par
 // Item i: active expert i / (f/8), h columns 8 (i % (f/8)) .. +7.  Wave w owns
 // the K blocks w, w + 8, ... (NB = ceil(d/1024) of them): their activations
 // and scales stay in registers, and as each block's weights are consumed the
-// next item's are loaded into their place.  Nothing in that loop branches
-// around a load: the compiler counts outstanding loads along straight-line
-// code only, and a load that may or may not have been issued makes it wait for
-// all of them (measured: 3.8 TB/s with such branches).  So a wave's missing
-// last block repeats a present one with a scale of 0, and the last item has
-// code of its own.
+// next item's are loaded into their place.
 //
 // The products run as BF16 MFMAs on weights widened in registers (E4M3 values
 // are exact in BF16): the FP8 MFMA's sums of 128 products carry an error of
@@ -457,111 +466,119 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_up_kernel(const FewArgs p) 
   v4f (*const red)[FW_WAVES][64] = reinterpret_cast<v4f(*)[FW_WAVES][64]>(&S.key);
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int g16 = lane >> 4, r16 = lane & 15;
-  const int KB = p.d / 128, FB = p.f / 128;
+  const int KB = p.d / 128, FB = p.f / 128, per = p.f / 8;
 
-  const int per = p.f / 8;
   PartialLogits part;
   part.load(p);
-  // activations of this wave's blocks; tokens past T repeat the last
+  // activations of this wave's blocks; tokens past T repeat the last, a
+  // missing last block the block KB - 1 (its weights read as zeros)
   v8i xq[NB];
   float xs[NB];
-  int kb[NB];
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
-    const bool mine = wave + 8 * j < KB;
-    kb[j] = mine ? wave + 8 * j : KB - 1;
-    const int t = min(r16, p.T - 1);
-    xq[j] = row_frag(p.xq + (size_t)t * p.d + kb[j] * 128 + g16 * 32);
-    xs[j] = p.xs[t * KB + kb[j]];
-    if (!mine) xs[j] = 0.0f;
+    const int kb = min(wave + 8 * j, KB - 1), t = min(r16, p.T - 1);
+    xq[j] = row_frag(p.xq + (size_t)t * p.d + kb * 128 + g16 * 32);
+    xs[j] = p.xs[t * KB + kb];
   }
-  const size_t up = (size_t)p.f * p.d;   // from a gate row to its up row
-  const uint8_t* lane_w = p.w13 + (size_t)(r16 & 7) * p.d + (2 * g16 + (r16 >> 3)) * 16;
-  const float* lane_s = p.w13_s + (size_t)(g16 < 2 ? 0 : FB) * KB;
+  // offsets of this lane's loads from an item's first gate row and its scale
+  const uint32_t gate_off = (r16 & 7) * p.d + (2 * g16 + (r16 >> 3)) * 16 + wave * 128;
+  const uint32_t up_off = gate_off + (uint32_t)p.f * p.d;
+  const uint32_t scale_off = ((g16 < 2 ? 0 : FB) * KB + wave) * 4;
+  const bool last = wave + 8 * (NB - 1) < KB;   // this wave has the last block too
   Lines b[NB];
   float sw[NB];
-  auto bases = [&](int e, int n8, const uint8_t*& wp, const float*& sp) {
-    wp = lane_w + ((size_t)e * 2 * p.f + n8 * 8) * p.d;
-    sp = lane_s + ((size_t)e * 2 * FB + n8 / 16) * KB;
+  auto load = [&](int j, __amdgpu_buffer_rsrc_t wb, __amdgpu_buffer_rsrc_t sb) {
+    const bool there = j + 1 < NB || last;
+    b[j] = load_weight(wb, there ? gate_off + j * 1024 : kNowhere, there ? up_off + j * 1024 : kNowhere);
+    sw[j] = load_scale(sb, there ? scale_off + j * 32 : kNowhere);
   };
-  auto load = [&](int j, const uint8_t* wp, const float* sp) {
-    b[j] = load_weight(wp + kb[j] * 128, wp + up + kb[j] * 128);
-    sw[j] = sp[kb[j]];
+  auto weights_of = [&](int e, int n8, bool there) {
+    return buffer_at(p.w13 + ((size_t)e * 2 * p.f + n8 * 8) * p.d, there);
+  };
+  auto scales_of = [&](int e, int n8, bool there) {
+    return buffer_at(p.w13_s + ((size_t)e * 2 * FB + n8 / 16) * KB, there);
   };
   // the first `per` items are the shared expert's, known before the selection:
   // their loads run beneath it
-  int item = blockIdx.x, n = 0;
-  const uint8_t* wp;
-  const float* sp;
-  if (item < per) {
-    bases(p.E, item, wp, sp);
+  int item = blockIdx.x;
+  const bool early = item < per;
 #pragma unroll
-    for (int j = 0; j < NB; ++j) load(j, wp, sp);
+  for (int j = 0; j < NB; ++j) {
+    load(j, weights_of(p.E, item, early), scales_of(p.E, item, early));
+    pin_loads();   // in the loop's order
   }
-  v8bf xb[NB][4];
-#pragma unroll
-  for (int j = 0; j < NB; ++j)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) xb[j][q] = widen8(xq[j][2 * q], xq[j][2 * q + 1]);
   few_select(p, S, P, part, blockIdx.x == 0);
   if (blockIdx.x == 0)
     for (int i = tid; i < (int)(sizeof(FewPlan) / 4); i += FW_THREADS)
       reinterpret_cast<uint32_t*>(p.plan)[i] = reinterpret_cast<const uint32_t*>(&P)[i];
   const int total = __builtin_amdgcn_readfirstlane(P.n_active) * per;
-  if (item >= total) return;
-  if (item >= per) {
-    const int a = item / per;
-    bases(__builtin_amdgcn_readfirstlane(P.expert[a]), item - a * per, wp, sp);
+  v8bf xb[NB][4];
 #pragma unroll
-    for (int j = 0; j < NB; ++j) load(j, wp, sp);
-  }
-  auto run = [&](auto more) {           // one item; `more`: another follows
-    const int next = item + gridDim.x;
-    if (more) {
-      const int a = next / per;
-      bases(__builtin_amdgcn_readfirstlane(P.expert[a]), next - a * per, wp, sp);
-    }
+  for (int j = 0; j < NB; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) xb[j][q] = widen8(xq[j][2 * q], xq[j][2 * q + 1]);
+
+  // A workgroup whose first item was not known runs the loop once on zeros for
+  // the loads that it makes: n counts from -1 and stores nothing then.
+  int next = early ? item + gridDim.x : item;
+  for (int n = early ? 0 : -1; item < total; ++n) {
+    const int a = next / per, n8 = next - a * per;
+    const bool more = next < total;
+    const int e = __builtin_amdgcn_readfirstlane(P.expert[more ? a : 0]);
+    const __amdgpu_buffer_rsrc_t wb = weights_of(e, n8, more), sb = scales_of(e, n8, more);
     v4f acc = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       const v8i w = weight_frag(b[j]);
-      const float s = sw[j] * xs[j];
-      if (more) load(j, wp, sp);
+      float s = sw[j] * xs[j];
+      asm volatile("" : "+v"(s));   // the product is made, and sw[j] free, before it is loaded again
+      pin_loads();
+      load(j, wb, sb);
       v4f q = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < 4; ++i) q = mfma_bf16_16x16x32(widen8(w[2 * i], w[2 * i + 1]), xb[j][i], q);
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[i] = fmaf(q[i], s, acc[i]);
+      pin_loads();
     }
-    // The waves' partial sums through LDS, in two halves in turn: one barrier
-    // per item, since a half is written again only after the next item's
-    // barrier, which the wave that reads it reaches afterwards.
-    red[n & 1][wave][lane] = acc;
-    lds_barrier();
-    if (wave == (n & 7)) {
-      v4f s = red[n & 1][0][lane];
+    if (n >= 0) {
+      // The waves' partial sums through LDS, in two halves in turn: one barrier
+      // per item, since a half is written again only after the next item's
+      // barrier, which the wave that reads it reaches afterwards.
+      red[n & 1][wave][lane] = acc;
+      lds_barrier();
+      if (wave == (n & 7)) {
+        v4f s = red[n & 1][0][lane];
 #pragma unroll
-      for (int v = 1; v < FW_WAVES; ++v) s += red[n & 1][v][lane];
-      // lanes 0..31 hold G (columns 4 g16 .. +3), lanes 32..63 U
-      v4f u;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) u[i] = __shfl_xor(s[i], 32);
-      const int a = item / per, n8 = item - a * per;
-      const int slot = P.slot[a][r16];
-      if (g16 < 2 && slot != 255) {
-        float4 h;
-        h.x = swiglu_f32(s[0], u[0]);
-        h.y = swiglu_f32(s[1], u[1]);
-        h.z = swiglu_f32(s[2], u[2]);
-        h.w = swiglu_f32(s[3], u[3]);
-        *reinterpret_cast<float4*>(p.h + (size_t)(r16 * (p.k + 1) + slot) * p.f + n8 * 8 + g16 * 4) = h;
+        for (int v = 1; v < FW_WAVES; ++v) s += red[n & 1][v][lane];
+        // lanes 0..31 hold G (columns 4 g16 .. +3), lanes 32..63 U of the same
+        // columns: each half takes two of the four
+        const bool hi = g16 >= 2;
+        const float g0 = hi ? s[0] : s[2], g1 = hi ? s[1] : s[3];     // what the other half needs
+        const float o0 = __shfl_xor(g0, 32), o1 = __shfl_xor(g1, 32);
+        const float h0 = swiglu_f32(hi ? o0 : s[0], hi ? s[2] : o0);
+        const float h1 = swiglu_f32(hi ? o1 : s[1], hi ? s[3] : o1);
+        const int ai = item / per, slot = P.slot[ai][r16];
+        if (slot != 255)
+          *reinterpret_cast<float2*>(p.h + (size_t)(r16 * (p.k + 1) + slot) * p.f + (item - ai * per) * 8 +
+                                     (g16 & 1) * 4 + (hi ? 2 : 0)) = make_float2(h0, h1);
       }
+      item = next;
     }
-    item = next;
-    ++n;
-  };
-  while (item + (int)gridDim.x < total) run(std::true_type{});
-  run(std::false_type{});
+    next += gridDim.x;
+  }
+}
+
+// Largest of the 16 lanes of a DPP row, by rotations within it.
+__device__ __forceinline__ float row_max(float v) {
+#define MOE_ROW_MAX(N)                                                                                              \
+  v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 + (N), 0xF, 0xF, true)))
+  MOE_ROW_MAX(8);
+  MOE_ROW_MAX(4);
+  MOE_ROW_MAX(2);
+  MOE_ROW_MAX(1);
+#undef MOE_ROW_MAX
+  return v;
 }
 
 // ---- a 1x128 tile of h: 16 lanes, 8 elements each ----
@@ -575,24 +592,18 @@ struct HTile {
     v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
   }
   // Codes into q; returns the scale.  The quotients are correctly rounded, as
-  // fp8_quant_1x128's (by Divider, whose reciprocal and remainders are normal
-  // numbers for s >= 2^-60; smaller scales take the plain division).
+  // fp8_quant_1x128's: by Divider, for which tiles with a scale below 2^-60
+  // are lifted by an exact power of two so that its reciprocal and its
+  // remainders are normal numbers.
   template <bool POW2>
   __device__ __forceinline__ float quantise(uint2& q) {
     float amax = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+    const float s = tile_scale<POW2>(row_max(amax)), lift = s < 0x1p-60f ? 0x1p80f : 1.0f;
+    const Divider div(s * lift);
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
-    const float s = tile_scale<POW2>(amax);
-    if (s >= 0x1p-60f) {
-      const Divider div(s);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = div(v[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = v[i] / s;
-    }
+    for (int i = 0; i < 8; ++i) v[i] = div(v[i] * lift);
     q.x = f32x4_to_e4m3(v[0], v[1], v[2], v[3]);
     q.y = f32x4_to_e4m3(v[4], v[5], v[6], v[7]);
     return s;
@@ -614,38 +625,37 @@ __global__ __launch_bounds__(256) void few_quant_kernel(const FewArgs p) {
 }
 
 // ---- kernel 4: out = sum over active experts of gate W2 h, + residual ----
-// Workgroup b owns an even share of the output columns, in units of 4, and
-// takes them 16 at a time (the last time what is left, its missing fragment
-// rows repeating the last).  A pass's steps (active expert, U adjacent K
-// blocks) are dealt to the waves in turn, `per` to each (steps past the last
-// repeat it and add nothing).  The passes follow each other as one stream of
-// steps with RING of them in flight per wave; loads are free of branches
-// except in the stream's last steps, for the reason above.
+// Workgroup b owns an even share of the output columns, in units of 4: at most
+// 16 C of them, in C fragments (missing rows of the last read as zeros).  The
+// steps (active expert, K block) are dealt to the waves in turn, with RING of
+// them in flight per wave; a step's h serves all fragments.  One barrier joins
+// the waves' sums at the end.
 //
 // STAGE: the workgroup quantises h itself, into LDS, beneath its first weight
-// loads; otherwise the tiles come from few_quant_kernel through memory.
-constexpr int FW_STAGE_BYTES = 96 * 1024;
+// loads; otherwise the tiles come from few_quant_kernel through memory, and
+// lanes whose token did not choose the expert load nothing.
+constexpr int FW_STAGE_BYTES = 48 * 1024;
+static_assert(kFewMaxD <= 256 * 32, "a workgroup's columns fit two fragments");
 
-template <int U, bool STAGE>
+template <int C, bool STAGE>
 struct DownStep {
-  Lines b[U];
-  float sw[U];
-  v8i hf[STAGE ? 1 : U];
-  float sh[STAGE ? 1 : U];
-  int hrow;       // row of h for this lane's token
-  int kb;
-  bool live;      // this lane's token chose the expert, and the step is no repeat
+  Lines b[C];
+  float sw[C];
+  v8i hf;         // not STAGE
+  float sh;
+  int row, kb;    // STAGE: this lane's h
+  bool live;      // this lane's token chose the expert
 };
 
-template <int U, int RING, bool STAGE, bool POW2>
+template <int C, int RING, bool STAGE, bool POW2>
 __global__ __launch_bounds__(FW_THREADS, 1) void few_down_kernel(const FewArgs p) {
   __shared__ FewPlan P;
-  __shared__ __attribute__((aligned(16))) v4f red[2][FW_WAVES][64];
+  __shared__ __attribute__((aligned(16))) v4f red[C][FW_WAVES][64];
   __shared__ __attribute__((aligned(16))) uint8_t stage[STAGE ? FW_STAGE_BYTES : 16];
   constexpr int EARLY = 5;              // tiles of h a thread loads before the weights (9 rows of f 2048)
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int g16 = lane >> 4, r16 = lane & 15;
-  const int FB = p.f / 128, FU = FB / U;
+  const int FB = p.f / 128;
   const int tiles = p.T * (p.k + 1) * FB;
   for (int i = tid; i < (int)(sizeof(FewPlan) / 4); i += FW_THREADS)
     reinterpret_cast<uint32_t*>(&P)[i] = reinterpret_cast<const uint32_t*>(p.plan)[i];
@@ -656,110 +666,89 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_down_kernel(const FewArgs p
       early[i].load(p.h + (size_t)min((tid >> 4) + i * (FW_THREADS / 16), tiles - 1) * 128 + (tid & 15) * 8);
   }
   lds_barrier();
-  const int steps = __builtin_amdgcn_readfirstlane(P.n_active) * FU, per = (steps + 7) / 8;
+  const int steps = __builtin_amdgcn_readfirstlane(P.n_active) * FB;
   const int units = p.d / 4;
   const int c_begin = 4 * (int)((long)units * blockIdx.x / gridDim.x);
   const int c_end = 4 * (int)((long)units * (blockIdx.x + 1) / gridDim.x);
-  const int count = (c_end - c_begin + 15) / 16 * per;   // steps of this wave's stream
-  // a step's expert: step / FU by a rounded-up reciprocal, exact for step * FU < 2^32
-  const uint32_t inv = (uint32_t)((0x100000000ull + FU - 1) / FU);
-  const uint8_t* lane_w = p.w2 + (2 * g16 + (r16 >> 3)) * 16;
+  // a step's expert: step / FB by a rounded-up reciprocal, exact for step * FB < 2^32
+  const uint32_t inv = (uint32_t)((0x100000000ull + FB - 1) / FB);
   const int hstride = p.f + 16;         // staged rows, 16 bytes apart in the banks
   float* const stage_s = reinterpret_cast<float*>(stage + p.T * (p.k + 1) * hstride);
-
-  DownStep<U, STAGE> ring[RING];
-  int lc = c_begin, lk = 0;             // the next load's first column and step within the pass
-  auto load = [&](DownStep<U, STAGE>& st) {
-    const int raw = wave + 8 * lk, step = min(raw, steps - 1);
-    const int a = FU == 1 ? step : (int)__umulhi((uint32_t)step, inv), kb = (step - a * FU) * U;
-    const int e = __builtin_amdgcn_readfirstlane(P.expert[a]);
-    const int r0 = min(lc + (r16 & 7), c_end - 1), r1 = min(lc + 8 + (r16 & 7), c_end - 1);
-    const uint8_t* wp = lane_w + (size_t)e * p.d * p.f + kb * 128;
-    const float* sp = p.w2_s + ((size_t)e * (p.d / 128) + min(lc + 4 * g16, c_end - 1) / 128) * FB + kb;
-    const uint8_t* w0 = wp + (size_t)r0 * p.f;
-    const uint8_t* w1 = wp + (size_t)r1 * p.f;
+  // this lane's offsets from an expert's weights and scales
+  uint32_t wo[C][2], so[C];
 #pragma unroll
-    for (int q = 0; q < U; ++q) {
-      st.b[q] = load_weight(w0 + q * 128, w1 + q * 128);
-      st.sw[q] = sp[q];
+  for (int c = 0; c < C; ++c) {
+    const int col = c_begin + 16 * c;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = col + 8 * i + (r16 & 7);
+      wo[c][i] = r < c_end ? (uint32_t)r * p.f + (2 * g16 + (r16 >> 3)) * 16 : kNowhere;
+    }
+    so[c] = col + 4 * g16 < c_end ? (uint32_t)(col + 4 * g16) / 128 * FB * 4 : kNowhere;
+  }
+  const __amdgpu_buffer_rsrc_t hb = buffer_at(p.hq, true), gb = buffer_at(p.hsg, true);
+
+  DownStep<C, STAGE> ring[RING];
+  int next = wave;                      // the step to load next
+  auto load = [&](DownStep<C, STAGE>& st) {
+    const bool there = next < steps;
+    const int a = !there ? 0 : FB == 1 ? next : (int)__umulhi((uint32_t)next, inv);
+    const int kb = there ? next - a * FB : 0;
+    const int e = __builtin_amdgcn_readfirstlane(P.expert[a]);
+    const __amdgpu_buffer_rsrc_t wb = buffer_at(p.w2 + (size_t)e * p.d * p.f + kb * 128, there);
+    const __amdgpu_buffer_rsrc_t sb = buffer_at(p.w2_s + (size_t)e * (p.d / 128) * FB + kb, there);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      st.b[c] = load_weight(wb, wo[c][0], wo[c][1]);
+      st.sw[c] = load_scale(sb, so[c]);
     }
     const int slot = P.slot[a][r16];
-    st.live = slot != 255 && raw < steps;
-    // lanes without a token of this expert all read one row, so that they add one line to the load
-    st.hrow = slot != 255 ? r16 * (p.k + 1) + slot : p.k;
-    st.kb = kb;
-    if (!STAGE) {
+    st.live = slot != 255;
+    const uint32_t row = r16 * (p.k + 1) + slot;
+    if (STAGE) {
+      st.row = st.live ? row : 0;
+      st.kb = kb;
+    } else {
+      const uint32_t at = st.live ? row * p.f + kb * 128 + g16 * 32 : kNowhere;
+      const i32x4 lo = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(hb, at, 0, 0));
+      const i32x4 hi = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(hb, at + 16, 0, 0));
+      st.hf = v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      st.sh = load_scale(gb, st.live ? (row * FB + kb) * 4 : kNowhere);
+    }
+    next += FW_WAVES;
+  };
+  v4f acc[C];
 #pragma unroll
-      for (int q = 0; q < U; ++q) {
-        st.hf[q] = row_frag(p.hq + (size_t)st.hrow * p.f + (kb + q) * 128 + g16 * 32);
-        st.sh[q] = p.hsg[st.hrow * FB + kb + q];
+  for (int c = 0; c < C; ++c) acc[c] = v4f{0.f, 0.f, 0.f, 0.f};
+  auto use = [&](const DownStep<C, STAGE>& st) {
+    const v8i h = STAGE ? row_frag(stage + st.row * hstride + st.kb * 128 + g16 * 32) : st.hf;
+    const float sh = STAGE ? stage_s[st.row * FB + st.kb] : st.sh;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const float s = sh * st.sw[c];
+      const v4f q = mfma_fp8_16x16x128(weight_frag(st.b[c]), h, v4f{0.f, 0.f, 0.f, 0.f});
+      if (st.live) {   // other tokens take nothing, not even a NaN weight's product with 0
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[c][j] = fmaf(q[j], s, acc[c][j]);
       }
     }
-    if (++lk == per) {
-      lk = 0;
-      lc += 16;
-    }
-  };
-  v4f acc = v4f{0.f, 0.f, 0.f, 0.f};
-  int col = c_begin, k = 0, n = 0;      // the next consumed step's
-  auto finish = [&]() {
-    red[n & 1][wave][lane] = acc;
-    lds_barrier();                      // halves in turn: see few_up_kernel
-    if (wave == (n & 7) && r16 < p.T && col + 4 * g16 < c_end) {
-      v4f s = red[n & 1][0][lane];
-#pragma unroll
-      for (int v = 1; v < FW_WAVES; ++v) s += red[n & 1][v][lane];
-      const size_t at = (size_t)r16 * p.d + col + g16 * 4;
-      if (p.residual) {
-        const uint2 r = *reinterpret_cast<const uint2*>(p.residual + at);
-        s[0] += __uint_as_float(r.x << 16);
-        s[1] += __uint_as_float(r.x & 0xFFFF0000u);
-        s[2] += __uint_as_float(r.y << 16);
-        s[3] += __uint_as_float(r.y & 0xFFFF0000u);
-      }
-      uint2 o;
-      o.x = (uint32_t)f32_to_bf16(s[0]) | ((uint32_t)f32_to_bf16(s[1]) << 16);
-      o.y = (uint32_t)f32_to_bf16(s[2]) | ((uint32_t)f32_to_bf16(s[3]) << 16);
-      *reinterpret_cast<uint2*>(p.out + at) = o;
-    }
-    acc = v4f{0.f, 0.f, 0.f, 0.f};
-    k = 0;
-    col += 16;
-    ++n;
-  };
-  auto use = [&](const DownStep<U, STAGE>& st, auto&& refill) {
-    v4f q[U];
-    float s[U];
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const v8i h = STAGE ? row_frag(stage + st.hrow * hstride + (st.kb + i) * 128 + g16 * 32) : st.hf[STAGE ? 0 : i];
-      s[i] = (STAGE ? stage_s[st.hrow * FB + st.kb + i] : st.sh[STAGE ? 0 : i]) * st.sw[i];
-      q[i] = mfma_fp8_16x16x128(weight_frag(st.b[i]), h, v4f{0.f, 0.f, 0.f, 0.f});
-    }
-    const bool live = st.live;   // other tokens take nothing, not even a NaN weight's product with 0
-    refill();
-#pragma unroll
-    for (int i = 0; i < U; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[j] = live ? fmaf(q[i][j], s[i], acc[j]) : acc[j];
-    if (++k == per) finish();
   };
 #pragma unroll
-  for (int r = 0; r < RING; ++r)
-    if (r < count) load(ring[r]);
+  for (int r = 0; r < RING; ++r) {
+    load(ring[r]);
+    pin_loads();
+  }
   if (STAGE) {
     auto put = [&](int tile, HTile& h) {
-      const int row = tile / FB;
+      const int row = FB == 1 ? tile : (int)__umulhi((uint32_t)tile, inv);
       uint2 q;
       const float s = h.template quantise<POW2>(q);
       *reinterpret_cast<uint2*>(stage + row * hstride + (tile - row * FB) * 128 + (tid & 15) * 8) = q;
       if ((tid & 15) == 0) stage_s[tile] = s * P.gate[row];
     };
 #pragma unroll
-    for (int i = 0; i < EARLY; ++i) {
-      const int tile = (tid >> 4) + i * (FW_THREADS / 16);
-      if (tile < tiles) put(tile, early[i]);
-    }
+    for (int i = 0; i < EARLY; ++i)   // past the last tile the last again, the same bytes
+      put(min((tid >> 4) + i * (FW_THREADS / 16), tiles - 1), early[i]);
     for (int tile = (tid >> 4) + EARLY * (FW_THREADS / 16); tile < tiles; tile += FW_THREADS / 16) {
       HTile h;
       h.load(p.h + (size_t)tile * 128 + (tid & 15) * 8);
@@ -767,17 +756,36 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_down_kernel(const FewArgs p
     }
     lds_barrier();
   }
-  int u = 0;
-  for (; u + 2 * RING <= count; u += RING) {
+  // whole groups of RING steps: those past the end are zeros
+  for (int u = 0; u * FW_WAVES < steps; u += RING) {
 #pragma unroll
-    for (int r = 0; r < RING; ++r) use(ring[r], [&] { load(ring[r]); });
+    for (int r = 0; r < RING; ++r) {
+      use(ring[r]);
+      pin_loads();
+      load(ring[r]);
+      pin_loads();
+    }
   }
-  for (; u < count; u += RING) {
 #pragma unroll
-    for (int r = 0; r < RING; ++r)
-      if (u + r < count) use(ring[r], [&] {
-        if (u + r + RING < count) load(ring[r]);
-      });
+  for (int c = 0; c < C; ++c) red[c][wave][lane] = acc[c];
+  lds_barrier();
+  const int col = c_begin + 16 * wave + 4 * g16;   // wave c writes fragment c
+  if (wave < C && r16 < p.T && col < c_end) {
+    v4f s = red[wave][0][lane];
+#pragma unroll
+    for (int v = 1; v < FW_WAVES; ++v) s += red[wave][v][lane];
+    const size_t at = (size_t)r16 * p.d + col;
+    if (p.residual) {
+      const uint2 r = *reinterpret_cast<const uint2*>(p.residual + at);
+      s[0] += __uint_as_float(r.x << 16);
+      s[1] += __uint_as_float(r.x & 0xFFFF0000u);
+      s[2] += __uint_as_float(r.y << 16);
+      s[3] += __uint_as_float(r.y & 0xFFFF0000u);
+    }
+    uint2 o;
+    o.x = (uint32_t)f32_to_bf16(s[0]) | ((uint32_t)f32_to_bf16(s[1]) << 16);
+    o.y = (uint32_t)f32_to_bf16(s[2]) | ((uint32_t)f32_to_bf16(s[3]) << 16);
+    *reinterpret_cast<uint2*>(p.out + at) = o;
   }
 }
 
@@ -796,15 +804,15 @@ hipError_t launch_layer_few(const uint16_t* x, const uint16_t* wg, const float* 
   while ((1 << c_log2) < G * keep) ++c_log2;
   // parts of d: as many as let a thread of the next kernel load all parts of its pairs by 16 loads
   const int pairs = ((T << e_log2) + FW_THREADS - 1) / FW_THREADS;
-  const int splits = pairs <= 2 ? 8 : pairs <= 4 ? 4 : 2;
+  const int s_log2 = pairs <= 2 ? 3 : pairs <= 4 ? 2 : 1;
   char* ws = static_cast<char*>(workspace);
   FewArgs p{T, d, f, E, G, M, k, (double)route_scale, x, wg, bias, w13, w13_s, w2, w2_s, residual, idx, w, out,
-            splits, e_log2, c_log2, reinterpret_cast<double*>(ws + L.part), reinterpret_cast<uint8_t*>(ws + L.xq),
+            s_log2, e_log2, c_log2, reinterpret_cast<double*>(ws + L.part), reinterpret_cast<uint8_t*>(ws + L.xq),
             reinterpret_cast<float*>(ws + L.xs), reinterpret_cast<float*>(ws + L.h),
             reinterpret_cast<uint8_t*>(ws + L.hq), reinterpret_cast<float*>(ws + L.hsg),
             reinterpret_cast<FewPlan*>(ws + L.plan)};
   const int KB = d / 128, FB = f / 128;
-  const dim3 g1((E + 15) / 16 * splits + (T * KB + FR_THREADS / 16 - 1) / (FR_THREADS / 16)), g3((T * (k + 1) * FB + 15) / 16);
+  const dim3 g1(((E + 15) / 16 << s_log2) + (T * KB + FR_THREADS / 16 - 1) / (FR_THREADS / 16)), g3((T * (k + 1) * FB + 15) / 16);
   if (pow2) hipLaunchKernelGGL(few_route_kernel<true>, g1, dim3(FR_THREADS), 0, stream, p);
   else hipLaunchKernelGGL(few_route_kernel<false>, g1, dim3(FR_THREADS), 0, stream, p);
   hipError_t e = hipGetLastError();
@@ -824,7 +832,11 @@ hipError_t launch_layer_few(const uint16_t* x, const uint16_t* wg, const float* 
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int rows = T * (k + 1);
-  const bool stage = (long)rows * (f + 16 + FB * 4) <= FW_STAGE_BYTES;
+  // h in the last kernel's LDS, quantised by every workgroup for itself, or by a
+  // kernel of its own: V3, us a call, 76.5 against 84.9 at T = 1 (18432
+  // elements of h), 135 against 138 at T = 2, 190 against 188 at T = 3
+  const bool stage = rows * f <= 40960;
+  static_assert(40960 + 16 * FW_T * (FW_MAX_K + 1) + 40960 / 32 <= FW_STAGE_BYTES, "h, its row padding and scales");
   if (!stage) {
     if (pow2) hipLaunchKernelGGL(few_quant_kernel<true>, g3, dim3(256), 0, stream, p);
     else hipLaunchKernelGGL(few_quant_kernel<false>, g3, dim3(256), 0, stream, p);
@@ -832,9 +844,9 @@ hipError_t launch_layer_few(const uint16_t* x, const uint16_t* wg, const float* 
     if (e != hipSuccess) return e;
   }
   const dim3 g4(std::min(256, d / 4));
-#define MOE_FEW_DOWN(U, RING, STAGE, POW2) \
-  hipLaunchKernelGGL((few_down_kernel<U, RING, STAGE, POW2>), g4, dim3(FW_THREADS), 0, stream, p)
-  if (FB % 2 == 0) {
+#define MOE_FEW_DOWN(C, RING, STAGE, POW2) \
+  hipLaunchKernelGGL((few_down_kernel<C, RING, STAGE, POW2>), g4, dim3(FW_THREADS), 0, stream, p)
+  if (d > 256 * 16) {   // more than 16 columns a workgroup
     if (!stage) MOE_FEW_DOWN(2, 4, false, false);
     else if (pow2) MOE_FEW_DOWN(2, 6, true, true);
     else MOE_FEW_DOWN(2, 6, true, false);
