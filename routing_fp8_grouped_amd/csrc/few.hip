@@ -851,9 +851,9 @@ hipError_t launch_layer_few(const uint16_t* x, const uint16_t* wg, const float* 
     else if (pow2) MOE_FEW_DOWN(2, 6, true, true);
     else MOE_FEW_DOWN(2, 6, true, false);
   } else {
-    if (!stage) MOE_FEW_DOWN(1, 8, false, false);
-    else if (pow2) MOE_FEW_DOWN(1, 12, true, true);
-    else MOE_FEW_DOWN(1, 12, true, false);
+    if (!stage) MOE_FEW_DOWN(1, 6, false, false);
+    else if (pow2) MOE_FEW_DOWN(1, 6, true, true);
+    else MOE_FEW_DOWN(1, 6, true, false);
   }
 #undef MOE_FEW_DOWN
   return hipGetLastError();
