@@ -449,6 +449,11 @@ class MoELayer:
             mark("route")
             quant(x, self.xq, self.xs, stream)
             mark("quant")
+        return self._experts(weights, stream, mark, train)
+
+    def _experts(self, weights, stream, mark, train, residual=None):
+        """The layer after the router and the quantiser: permute, both expert
+        GEMMs, combine (with ``residual`` added)."""
         if self.dispatch:
             moe_permute(self.idx, self.E, self.offsets, self.pos, self.row_token, self.ws,
                         self.xq, self.xs, self.xq_perm, self.xs_perm, stream)
@@ -471,8 +476,40 @@ class MoELayer:
         mark("gemm_up")
         down(self.h, self.hs, self.offsets, weights.w2q, weights.w2s, self.y, stream)
         mark("gemm_down")
-        moe_combine(self.y, self.pos, self.w, self.T * self.k, self.out, stream)
+        moe_combine(self.y, self.pos, self.w, self.T * self.k, self.out, stream, residual=residual)
         mark("combine")
+        return self.out
+
+    def forward_normed(self, x, norm_weight, eps, wg, bias, weights, residual=None, stream=None, mark=None,
+                       train=False):
+        """The pre-norm block around the layer: s = x + residual,
+        out = s + layer(rmsnorm(s) * norm_weight), with the layer's FP8 input
+        written by the norm itself.  x, residual [T, d] BF16 (residual may be
+        None), norm_weight [d] BF16.  Returns out; ``self.hsum`` holds s."""
+        mark = mark or (lambda name: None)
+        if getattr(self, "hsum", None) is None:
+            self.hsum, self.xn = torch.empty_like(self.out), torch.empty_like(self.out)
+            self.rstd = torch.empty(self.T, dtype=torch.float32, device=self.out.device)
+        norm = moe_rmsnorm_quant_pow2 if self.pow2 else moe_rmsnorm_quant
+        norm(x, norm_weight, eps, self.xn, residual=residual, sum_out=self.hsum, q=self.xq, scale=self.xs,
+             rstd=self.rstd, stream=stream)
+        mark("norm")
+        moe_route(self.xn, wg, bias, self.n_groups, self.topk_groups, self.k, self.route_scale, self.idx, self.w,
+                  stream, workspace=self.route_ws)
+        mark("route")
+        return self._experts(weights, stream, mark, train, residual=self.hsum)
+
+    def forward_few(self, x, wg, bias, weights, residual=None, stream=None):
+        """The layer on x [T, d] for T <= 16 by moe_layer_few: the same
+        operation as ``forward`` in three or four kernels, its selection ranked
+        in FP64 and its expert outputs not rounded to BF16 before they are
+        combined.  ``residual`` [T, d] is added to the output when given."""
+        if getattr(self, "few_ws", None) is None:
+            n = moe_layer_few_workspace_bytes(self.T, self.d, self.f, self.E, self.k)
+            self.few_ws = torch.empty(max(16, n), dtype=torch.uint8, device=self.out.device)
+        few = moe_layer_few_pow2 if self.pow2 else moe_layer_few
+        few(x, wg, bias, self.n_groups, self.topk_groups, self.k, self.route_scale, weights.w13q, weights.w13s,
+            weights.w2q, weights.w2s, self.idx, self.w, self.out, self.few_ws, residual=residual, stream=stream)
         return self.out
 
     def _train_buffers(self):
@@ -538,6 +575,39 @@ class MoELayer:
                                self.dw13, stream)
         mark("wgrad_w13")
         return self.dx, self.dw13, self.dw2, self.dw
+
+    def backward_normed(self, dout, norm_weight, weights_t, stream=None, mark=None):
+        """Backward of the last ``forward_normed(..., train=True)``.  Returns
+        (ds [T, d] BF16, the gradient of x and of the residual alike, dweight
+        [d] FP32 of the norm, dW13, dW2, gate gradients); as in ``backward``,
+        the gates' gradients are not propagated into the router."""
+        mark = mark or (lambda name: None)
+        dx, dw13, dw2, dgate = self.backward(dout, weights_t, stream, mark)
+        if getattr(self, "dnorm", None) is None:
+            self.dnorm = torch.empty(self.d, dtype=torch.float32, device=self.out.device)
+            self.dsum = torch.empty_like(self.out)
+            n = moe_rmsnorm_backward_workspace_bytes(self.T, self.d)
+            self.norm_ws = torch.empty(max(16, n), dtype=torch.uint8, device=self.out.device)
+        moe_rmsnorm_backward(dx, self.hsum, norm_weight, self.rstd, self.dsum, self.dnorm, self.norm_ws, dres=dout,
+                             stream=stream)
+        mark("norm_bwd")
+        return self.dsum, self.dnorm, dw13, dw2, dgate
+
+    def clip_grads(self, max_norm, extra=(), stream=None):
+        """After a backward: scales its weight gradients (and ``extra``, a
+        list of further FP32 or BF16 gradients) in place so that their joint
+        L2 norm is at most ``max_norm``.  Returns the norm before, [1] FP32 on
+        the device; nothing waits on the host."""
+        grads = [self.dw13, self.dw2, *extra]
+        if getattr(self, "grad_norm", None) is None:
+            self.grad_norm = torch.empty(1, dtype=torch.float32, device=self.out.device)
+            self.grad_coef = torch.empty_like(self.grad_norm)
+        n = moe_grad_norm_workspace_bytes(len(grads))
+        if getattr(self, "grad_ws", None) is None or self.grad_ws.numel() < n:
+            self.grad_ws = torch.empty(n, dtype=torch.uint8, device=self.out.device)
+        moe_grad_norm(grads, max_norm, self.grad_norm, self.grad_coef, self.grad_ws, stream)
+        moe_grad_scale(grads, self.grad_coef, stream=stream)
+        return self.grad_norm
 
     def update_bias(self, bias, gamma, stream=None):
         """After forward(): one step of the balancing controller on ``bias``

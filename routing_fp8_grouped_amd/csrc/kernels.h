@@ -83,6 +83,9 @@ hipError_t launch_combine(const uint16_t* y, const int32_t* pos, const float* w,
                           int d, int shared_row0, const uint16_t* residual, uint16_t* out,
                           hipStream_t stream);
 
+// The last-level cache: data of calls that move more than this goes past it.
+constexpr size_t kCacheBytes = size_t(256) << 20;
+
 // Residual addition + RMS norm + 1x128 quantisation, and its backward
 // (norm.hip).  kNormMaxD: the widest row a workgroup holds in registers.
 constexpr int kNormMaxD = 16384;

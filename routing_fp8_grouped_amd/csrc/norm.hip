@@ -59,6 +59,33 @@ __device__ __forceinline__ V group_sum(V v, V* buf, int waves) {
   return s;
 }
 
+// Row data; STREAM: past the caches, where a call moves more than they hold.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+template <bool STREAM>
+__device__ __forceinline__ uint4 load16(const uint16_t* p) {
+  const u32x4* v = reinterpret_cast<const u32x4*>(p);
+  const u32x4 u = STREAM ? __builtin_nontemporal_load(v) : *v;
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+template <bool STREAM>
+__device__ __forceinline__ void store16(uint16_t* p, const uint4& v) {
+  const u32x4 u = {v.x, v.y, v.z, v.w};
+  if (STREAM) __builtin_nontemporal_store(u, reinterpret_cast<u32x4*>(p));
+  else *reinterpret_cast<u32x4*>(p) = u;
+}
+
+// Largest of the 16 lanes of a DPP row, by rotations within it.
+__device__ __forceinline__ float row_max(float v) {
+#define MOE_ROW_MAX(N)                                                                                              \
+  v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 + (N), 0xF, 0xF, true)))
+  MOE_ROW_MAX(8);
+  MOE_ROW_MAX(4);
+  MOE_ROW_MAX(2);
+  MOE_ROW_MAX(1);
+#undef MOE_ROW_MAX
+  return v;
+}
+
 __device__ __forceinline__ void unpack8(const uint4& raw, float (&v)[8]) {
   const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
@@ -119,14 +146,14 @@ __global__ __launch_bounds__(WAVE_ROW ? NORM_THREADS : 1024) void rmsnorm_quant_
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = tl + i * team;
-      if (c < chunks) h[i] = *reinterpret_cast<const uint4*>(x + base + c * 8);
+      if (c < chunks) h[i] = load16<false>(x + base + c * 8);
     }
     if (res) {
       uint4 r[NC];
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const int c = tl + i * team;
-        if (c < chunks) r[i] = *reinterpret_cast<const uint4*>(res + base + c * 8);
+        if (c < chunks) r[i] = load16<false>(res + base + c * 8);
       }
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
@@ -145,7 +172,7 @@ __global__ __launch_bounds__(WAVE_ROW ? NORM_THREADS : 1024) void rmsnorm_quant_
     for (int i = 0; i < NC; ++i) {
       const int c = tl + i * team;
       if (c < chunks) {
-        if (sum) *reinterpret_cast<uint4*>(sum + base + c * 8) = h[i];
+        if (sum) store16<false>(sum + base + c * 8, h[i]);
         float a[8];
         unpack8(h[i], a);
 #pragma unroll
@@ -166,15 +193,13 @@ __global__ __launch_bounds__(WAVE_ROW ? NORM_THREADS : 1024) void rmsnorm_quant_
 #pragma unroll
         for (int j = 0; j < 8; ++j) a[j] = (a[j] * rs) * g[j];
         const uint4 o = pack8(a);
-        if (y) *reinterpret_cast<uint4*>(y + base + c * 8) = o;
+        if (y) store16<false>(y + base + c * 8, o);
         if (q) {
           float v[8], amax = 0.0f;
           unpack8(o, v);
 #pragma unroll
           for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
-#pragma unroll
-          for (int s2 = 8; s2 > 0; s2 >>= 1) amax = fmaxf(amax, __shfl_xor(amax, s2));
-          const float s = tile_scale<POW2>(amax);
+          const float s = tile_scale<POW2>(row_max(amax));
           *reinterpret_cast<uint2*>(q + base + c * 8) = codes8<POW2>(v, s);
           if ((c & 15) == 0) scale[(size_t)row * (d / 128) + (c >> 4)] = s;
         }
@@ -185,8 +210,8 @@ __global__ __launch_bounds__(WAVE_ROW ? NORM_THREADS : 1024) void rmsnorm_quant_
 
 // Rows are dealt to the teams in turn; every thread keeps the dw partial sums
 // of its columns over its team's rows.  Workgroup b writes partial[b][0..d).
-template <int NC, bool WAVE_ROW>
-__global__ __launch_bounds__(WAVE_ROW ? NORM_THREADS : 1024) void rmsnorm_backward_kernel(
+template <int NC, int THREADS, bool WAVE_ROW, bool STREAM>
+__global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(
     const uint16_t* __restrict__ dy, const uint16_t* __restrict__ h, const uint16_t* __restrict__ w,
     const float* __restrict__ rstd, const uint16_t* dres, int T, int d, uint16_t* dh, float* __restrict__ partial) {
   __shared__ float red[2][16];
@@ -216,9 +241,9 @@ __global__ __launch_bounds__(WAVE_ROW ? NORM_THREADS : 1024) void rmsnorm_backwa
       const int c = tl + i * team;
       a[i] = b[i] = e[i] = make_uint4(0, 0, 0, 0);
       if (c < chunks) {
-        a[i] = *reinterpret_cast<const uint4*>(dy + base + c * 8);
-        b[i] = *reinterpret_cast<const uint4*>(h + base + c * 8);
-        if (dres) e[i] = *reinterpret_cast<const uint4*>(dres + base + c * 8);
+        a[i] = load16<STREAM>(dy + base + c * 8);
+        b[i] = load16<STREAM>(h + base + c * 8);
+        if (dres) e[i] = load16<STREAM>(dres + base + c * 8);
       }
     }
     float dot = 0.0f;
@@ -248,7 +273,7 @@ __global__ __launch_bounds__(WAVE_ROW ? NORM_THREADS : 1024) void rmsnorm_backwa
         unpack8(e[i], r);
 #pragma unroll
         for (int j = 0; j < 8; ++j) r[j] = fmaf(rs, fmaf(-(hv[j] * rs), c1, gy[j] * wv[j]), r[j]);
-        *reinterpret_cast<uint4*>(dh + base + c * 8) = pack8(r);
+        store16<STREAM>(dh + base + c * 8, pack8(r));
       }
     }
   }
@@ -278,19 +303,28 @@ __global__ __launch_bounds__(WAVE_ROW ? NORM_THREADS : 1024) void rmsnorm_backwa
   }
 }
 
-// dw[c] = sum over n partial rows, FP64, in a fixed order: 16 threads share 16
-// columns' rows (row r to thread r % 16), their sums joined in LDS.
+// dw[c] = sum over n partial rows, FP64, in a fixed order: 32 threads share a
+// column's rows (row r to thread r % 32, eight loads in flight), their sums
+// joined in LDS.
 __global__ __launch_bounds__(1024) void rmsnorm_dw_kernel(const float* __restrict__ partial, int n, int d,
                                                           float* __restrict__ dw) {
-  __shared__ double s[16][65];
-  const int col = blockIdx.x * 64 + (threadIdx.x & 63), part = threadIdx.x >> 6;
+  __shared__ double s[32][33];
+  const int x = threadIdx.x & 31, part = threadIdx.x >> 5, col = blockIdx.x * 32 + x;
   double a = 0.0;
-  for (int r = part; r < n; r += 16) a += partial[(size_t)r * d + col];
-  s[part][threadIdx.x & 63] = a;
+  int r = part;
+  for (; r + 7 * 32 < n; r += 8 * 32) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = partial[(size_t)(r + 32 * i) * d + col];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a += v[i];
+  }
+  for (; r < n; r += 32) a += partial[(size_t)r * d + col];
+  s[part][x] = a;
   __syncthreads();
   if (part == 0) {
 #pragma unroll
-    for (int i = 1; i < 16; ++i) a += s[i][threadIdx.x];
+    for (int i = 1; i < 32; ++i) a += s[i][x];
     dw[col] = (float)a;
   }
 }
@@ -327,26 +361,33 @@ hipError_t launch_rmsnorm_quant(const uint16_t* x, const uint16_t* res, const ui
 // enough that their partial rows stay a small part of the traffic.
 int rmsnorm_backward_groups(int T, int d) {
   const int rows = d <= kWaveRowD ? NORM_THREADS / 64 : 1;
-  return (int)std::min((long)1024, ((long)T + rows - 1) / rows);
+  return (int)std::min((long)512, ((long)T + rows - 1) / rows);
 }
 
 hipError_t launch_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const uint16_t* w, const float* rstd,
                                    const uint16_t* dres, int T, int d, uint16_t* dh, float* dw, float* partial,
                                    hipStream_t stream) {
   const int n = T > 0 ? rmsnorm_backward_groups(T, d) : 0;   // no rows: dw = 0 alone
-  if (n == 0) {
-  } else if (d <= 512)
-    hipLaunchKernelGGL((rmsnorm_backward_kernel<1, true>), dim3(n), dim3(NORM_THREADS), 0, stream, dy, h, w, rstd,
-                       dres, T, d, dh, partial);
-  else if (d <= kWaveRowD)
-    hipLaunchKernelGGL((rmsnorm_backward_kernel<4, true>), dim3(n), dim3(NORM_THREADS), 0, stream, dy, h, w, rstd,
-                       dres, T, d, dh, partial);
-  else
-    hipLaunchKernelGGL((rmsnorm_backward_kernel<2, false>), dim3(n), dim3(group_threads(d)), 0, stream, dy, h, w,
-                       rstd, dres, T, d, dh, partial);
+  const bool stream_rows = (size_t)T * d * 8 > kCacheBytes;
+#define MOE_NORM_BWD(NC, MAX, WR, THREADS)                                                                           \
+  do {                                                                                                               \
+    if (stream_rows)                                                                                                 \
+      hipLaunchKernelGGL((rmsnorm_backward_kernel<NC, MAX, WR, true>), dim3(n), dim3(THREADS), 0, stream, dy, h, w, rstd, \
+                         dres, T, d, dh, partial);                                                                   \
+    else                                                                                                             \
+      hipLaunchKernelGGL((rmsnorm_backward_kernel<NC, MAX, WR, false>), dim3(n), dim3(THREADS), 0, stream, dy, h, w,      \
+                         rstd, dres, T, d, dh, partial);                                                             \
+  } while (0)
+  if (n > 0) {
+    if (d <= 512) MOE_NORM_BWD(1, NORM_THREADS, true, NORM_THREADS);
+    else if (d <= kWaveRowD) MOE_NORM_BWD(4, NORM_THREADS, true, NORM_THREADS);
+    else if (d <= 8192) MOE_NORM_BWD(2, 512, false, group_threads(d));
+    else MOE_NORM_BWD(2, 1024, false, group_threads(d));
+  }
+#undef MOE_NORM_BWD
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(rmsnorm_dw_kernel, dim3(d / 64), dim3(1024), 0, stream, partial, n, d, dw);
+  hipLaunchKernelGGL(rmsnorm_dw_kernel, dim3(d / 32), dim3(1024), 0, stream, partial, n, d, dw);
   return hipGetLastError();
 }
 
