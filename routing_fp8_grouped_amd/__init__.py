@@ -413,6 +413,8 @@ class MoELayer:
         self.row_token = torch.empty(rows, dtype=torch.int32, **dev)
         self.ws = torch.empty(max(16, moe_permute_workspace_bytes(T, topk, E)), dtype=torch.uint8, **dev)
         self.route_ws = torch.empty(max(16, moe_route_workspace_bytes(T, E)), dtype=torch.uint8, **dev)
+        n = moe_layer_few_workspace_bytes(T, d, f, E, topk)     # 0 for batches that form does not take
+        self.few_ws = torch.empty(max(16, n), dtype=torch.uint8, **dev)
         self.xq_perm = torch.empty(rows, d, dtype=torch.uint8, **dev) if dispatch else None
         self.xs_perm = torch.empty(rows, d // 128, dtype=torch.float32, **dev) if dispatch else None
         self.h = torch.empty(rows, f, dtype=torch.uint8, **dev)
@@ -504,9 +506,6 @@ class MoELayer:
         operation as ``forward`` in three or four kernels, its selection ranked
         in FP64 and its expert outputs not rounded to BF16 before they are
         combined.  ``residual`` [T, d] is added to the output when given."""
-        if getattr(self, "few_ws", None) is None:
-            n = moe_layer_few_workspace_bytes(self.T, self.d, self.f, self.E, self.k)
-            self.few_ws = torch.empty(max(16, n), dtype=torch.uint8, device=self.out.device)
         few = moe_layer_few_pow2 if self.pow2 else moe_layer_few
         few(x, wg, bias, self.n_groups, self.topk_groups, self.k, self.route_scale, weights.w13q, weights.w13s,
             weights.w2q, weights.w2s, self.idx, self.w, self.out, self.few_ws, residual=residual, stream=stream)

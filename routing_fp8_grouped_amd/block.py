@@ -7,6 +7,7 @@ checked here; the library checks the rest.
 """
 
 from array import array
+from operator import attrgetter
 
 import torch
 
@@ -148,32 +149,26 @@ def moe_layer_few_pow2(x, wg, bias, n_groups, topk_groups, topk, route_scale, w1
 _GRAD_TYPES = {_FP32: 0, _BF16: 1}
 
 
-def _grad_list(grads, outs):
-    """Host arrays (pointers, output pointers, sizes, types) of a gradient list
-    and its outputs, checked, and the current device."""
-    dev = torch.cuda.current_device()
+_dtype = attrgetter("dtype")
+_data_ptr, _numel = torch.Tensor.data_ptr, torch.Tensor.numel
+_get_device, _is_contiguous = torch.Tensor.get_device, torch.Tensor.is_contiguous
+
+
+def _grad_arrays(tensors, what, dev):
+    """Host arrays (pointers, sizes, types) of a list of gradients, checked.
+    Over the list by map: a step's list has tens to hundreds of tensors."""
     try:
-        types = array("i", [_GRAD_TYPES[t.dtype] for t in grads])
+        types = array("i", [_GRAD_TYPES[t] for t in map(_dtype, tensors)])
     except KeyError:
-        i = next(i for i, t in enumerate(grads) if t.dtype not in _GRAD_TYPES)
-        raise ValueError(f"gradient {i} must be float32 or bfloat16, got {grads[i].dtype}") from None
-    for i, t in enumerate(grads):
-        if t.get_device() != dev:
-            raise ValueError(f"gradient {i} is on {t.device}, the current device is cuda:{dev}")
-        if not t.is_contiguous():
-            raise ValueError(f"gradient {i} must be contiguous")
-    ptrs = array("Q", [t.data_ptr() for t in grads])
-    to = ptrs
-    if outs is not None and outs is not grads:
-        if len(outs) != len(grads):
-            raise ValueError(f"{len(outs)} outputs for {len(grads)} gradients")
-        for i, (t, o) in enumerate(zip(grads, outs)):
-            if o is not t and (o.dtype is not t.dtype or o.shape != t.shape or o.get_device() != dev or
-                               not o.is_contiguous()):
-                raise ValueError(f"output {i} must be a contiguous {t.dtype} tensor of shape {tuple(t.shape)} on "
-                                 f"{t.device}")
-        to = array("Q", [t.data_ptr() for t in outs])
-    return ptrs, to, array("q", [t.numel() for t in grads]), types, dev
+        i, t = next((i, t) for i, t in enumerate(tensors) if t.dtype not in _GRAD_TYPES)
+        raise ValueError(f"{what} {i} must be float32 or bfloat16, got {t.dtype}") from None
+    if set(map(_get_device, tensors)) - {dev}:
+        i, t = next((i, t) for i, t in enumerate(tensors) if t.get_device() != dev)
+        raise ValueError(f"{what} {i} is on {t.device}, the current device is cuda:{dev}")
+    if not all(map(_is_contiguous, tensors)):
+        i = next(i for i, t in enumerate(tensors) if not t.is_contiguous())
+        raise ValueError(f"{what} {i} must be contiguous")
+    return array("Q", map(_data_ptr, tensors)), array("q", map(_numel, tensors)), types
 
 
 def moe_grad_norm_workspace_bytes(n_tensors):
@@ -183,7 +178,8 @@ def moe_grad_norm_workspace_bytes(n_tensors):
 def moe_grad_norm(grads, max_norm, norm, coef, workspace, stream=None):
     """norm [1] float32 = L2 norm over every element of ``grads`` (float32 and bfloat16 tensors), coef [1] float32 =
     the factor that clips them to ``max_norm`` (1 where they are within it)."""
-    g, _, sizes, types, dev = _grad_list(grads, None)
+    dev = torch.cuda.current_device()
+    g, sizes, types = _grad_arrays(grads, "gradient", dev)
     _check(dev, ((norm, "norm", _FP32, (1,)), (coef, "coef", _FP32, (1,)), (workspace, "workspace", _U8, None)))
     _call("moe_grad_norm", g.buffer_info()[0], sizes.buffer_info()[0], types.buffer_info()[0], len(grads), max_norm,
           _ptr(norm), _ptr(coef), _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(stream, dev))
@@ -191,7 +187,15 @@ def moe_grad_norm(grads, max_norm, norm, coef, workspace, stream=None):
 
 def moe_grad_scale(grads, coef, outs=None, stream=None):
     """outs[i] = grads[i] * coef, in place without ``outs``."""
-    g, o, sizes, types, dev = _grad_list(grads, outs)
+    dev = torch.cuda.current_device()
+    o = g, sizes, types = _grad_arrays(grads, "gradient", dev)
+    if outs is not None and outs is not grads:
+        if len(outs) != len(grads):
+            raise ValueError(f"{len(outs)} outputs for {len(grads)} gradients")
+        o = _grad_arrays(outs, "output", dev)
+        if o[1] != sizes or o[2] != types:
+            i = next(i for i in range(len(sizes)) if o[1][i] != sizes[i] or o[2][i] != types[i])
+            raise ValueError(f"output {i} must be a {grads[i].dtype} tensor of {sizes[i]} elements")
     _check(dev, ((coef, "coef", _FP32, (1,)),))
-    _call("moe_grad_scale", g.buffer_info()[0], o.buffer_info()[0], sizes.buffer_info()[0], types.buffer_info()[0],
+    _call("moe_grad_scale", g.buffer_info()[0], o[0].buffer_info()[0], sizes.buffer_info()[0], types.buffer_info()[0],
           len(grads), _ptr(coef), _stream(stream, dev))

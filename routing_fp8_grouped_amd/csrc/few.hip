@@ -17,12 +17,18 @@
 //     permutation, no row counts; the activations of the K blocks a wave owns
 //     stay in its registers for the whole kernel.
 //   * The eight waves of a workgroup split K, so a work item is only 16 weight
-//     rows: 8 gate and the 8 matching up rows (fragment rows 0..7 and 8..15),
-//     or 16 rows of W2 of every active expert in turn.  With 9 experts there
-//     are still several items per CU, and all waves of the chip stream.
-//   * The second product walks all active experts for its 16 output columns,
-//     so the gated sum over experts is its accumulator and the combine, in
-//     registers: expert outputs never reach memory.
+//     rows: 8 gate and the 8 matching up rows (fragment rows 0..7 and 8..15).
+//     With 9 experts there are still nine items per CU, and all waves stream.
+//   * A workgroup of the second product owns some output columns (28 at d
+//     7168) and walks every active expert for them, so the gated sum over
+//     experts is its accumulator and the combine, in registers: expert outputs
+//     never reach memory.
+//
+// Bound by HBM reads from T = 4 on: at d 7168, f 2048, E 256, k 8 the products
+// run at 6.4 to 6.8 TB/s (a plain read of the card's memory: 7.05).  At T = 1
+// (400 MB) the launches (4.8 us for the router), the selection (9 us, of which
+// the first item's weights cover 4) and the products' starts and ends are a
+// quarter of the 77 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -167,19 +173,29 @@ __device__ __forceinline__ v8i row_frag(const uint8_t* p) {
   return v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
 }
 
+// Largest of the 16 lanes of a DPP row, by rotations within it.
+__device__ __forceinline__ float row_max(float v) {
+#define MOE_ROW_MAX(N)                                                                                              \
+  v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 + (N), 0xF, 0xF, true)))
+  MOE_ROW_MAX(8);
+  MOE_ROW_MAX(4);
+  MOE_ROW_MAX(2);
+  MOE_ROW_MAX(1);
+#undef MOE_ROW_MAX
+  return v;
+}
+
 // ---- kernel 1: partial logits and the tiles of x ----
 // A workgroup takes 16 experts and one of `splits` parts of d, so that the
 // 3.7 MB of V3's router come through 128 CUs; the next kernel adds the parts.
-// A BF16 MFMA multiplies 16 experts by 16 tokens over 32 elements, and those
-// partial sums, good to 2^-24 of their largest product, add up in FP64: a
-// logit is exact to 10^-8, ranked as FP64.  (The FP64 MFMA is exact but takes
-// 64 clocks for 4 elements.)
+// The products run on the FP64 MFMA (16 experts by 16 tokens by 4 elements):
+// BF16 values are exact there, so the scores that the selection compares carry
+// errors of 10^-15 only, whatever the order of the sum.  (The BF16 MFMA would
+// be eight times as fast, but its logits were 3.5e-8 RMS off, 1.7e-7 at most:
+// as far as neighbouring scores can be apart.)  A lane loads eight consecutive
+// elements of its row and feeds them to eight MFMAs; which four elements meet
+// in one does not matter as long as both operands agree.
 typedef double v4d __attribute__((ext_vector_type(4)));
-
-union Bf16x8 {
-  uint4 u;
-  v8bf v;
-};
 
 template <bool POW2>
 __global__ __launch_bounds__(FR_THREADS) void few_route_kernel(const FewArgs p) {
@@ -200,9 +216,7 @@ __global__ __launch_bounds__(FR_THREADS) void few_route_kernel(const FewArgs p) 
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
-    const float s = tile_scale<POW2>(amax);
+    const float s = tile_scale<POW2>(row_max(amax));
     uint2 q;
     q.x = f32x4_to_e4m3(v[0] / s, v[1] / s, v[2] / s, v[3] / s);
     q.y = f32x4_to_e4m3(v[4] / s, v[5] / s, v[6] / s, v[7] / s);
@@ -219,27 +233,32 @@ __global__ __launch_bounds__(FR_THREADS) void few_route_kernel(const FewArgs p) 
   v4d acc = v4d{0.0, 0.0, 0.0, 0.0};
   const int stride = FR_WAVES << p.s_log2;   // the parts interleave
   for (int c0 = split * FR_WAVES + wave; c0 < chunks; c0 += stride * FR_RING) {
-    Bf16x8 a[FR_RING], b[FR_RING];
+    uint4 a[FR_RING], b[FR_RING];
 #pragma unroll
     for (int r = 0; r < FR_RING; ++r) {
       const int c = min(c0 + r * stride, chunks - 1);
-      a[r].u = *reinterpret_cast<const uint4*>(wr + c * 32);
-      b[r].u = *reinterpret_cast<const uint4*>(xr + c * 32);
+      a[r] = *reinterpret_cast<const uint4*>(wr + c * 32);
+      b[r] = *reinterpret_cast<const uint4*>(xr + c * 32);
     }
 #pragma unroll
     for (int r = 0; r < FR_RING; ++r) {
-      const v4f q = mfma_bf16_16x16x32(a[r].v, b[r].v, v4f{0.f, 0.f, 0.f, 0.f});
       if (c0 + r * stride < chunks) {   // uniform over the wave
+        const uint32_t au[4] = {a[r].x, a[r].y, a[r].z, a[r].w}, bu[4] = {b[r].x, b[r].y, b[r].z, b[r].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] += (double)q[i];
+        for (int i = 0; i < 4; ++i) {
+          acc = __builtin_amdgcn_mfma_f64_16x16x4f64(__uint_as_float(au[i] << 16), __uint_as_float(bu[i] << 16), acc,
+                                                     0, 0, 0);
+          acc = __builtin_amdgcn_mfma_f64_16x16x4f64(__uint_as_float(au[i] & 0xFFFF0000u),
+                                                     __uint_as_float(bu[i] & 0xFFFF0000u), acc, 0, 0, 0);
+        }
       }
     }
   }
   red[wave][lane] = acc;
   __syncthreads();
-  // lane l holds rows (experts) 4 (l / 16) + i, column (token) l % 16
+  // an FP64 MFMA leaves lane l with rows (experts) l / 16 + 4 i, column (token) l % 16
   if (tid < 256) {
-    const int i = tid >> 6, e = e0 + 4 * g16 + i;
+    const int i = tid >> 6, e = e0 + g16 + 4 * i;
     double l = red[0][lane][i];
 #pragma unroll
     for (int v = 1; v < FR_WAVES; ++v) l += red[v][lane][i];
@@ -268,7 +287,6 @@ struct SelectLds {
 struct PartialLogits {
   double v[16];
   float bias;       // of this thread's expert, the same for all its pairs
-
 
   __device__ __forceinline__ void load(const FewArgs& p) {
     const uint32_t e = min((int)threadIdx.x & ((1 << p.e_log2) - 1), p.E - 1);
@@ -569,18 +587,6 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_up_kernel(const FewArgs p) 
   }
 }
 
-// Largest of the 16 lanes of a DPP row, by rotations within it.
-__device__ __forceinline__ float row_max(float v) {
-#define MOE_ROW_MAX(N)                                                                                              \
-  v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 + (N), 0xF, 0xF, true)))
-  MOE_ROW_MAX(8);
-  MOE_ROW_MAX(4);
-  MOE_ROW_MAX(2);
-  MOE_ROW_MAX(1);
-#undef MOE_ROW_MAX
-  return v;
-}
-
 // ---- a 1x128 tile of h: 16 lanes, 8 elements each ----
 struct HTile {
   float v[8];
@@ -726,7 +732,8 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_down_kernel(const FewArgs p
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const float s = sh * st.sw[c];
-      const v4f q = mfma_fp8_16x16x128(weight_frag(st.b[c]), h, v4f{0.f, 0.f, 0.f, 0.f});
+      v4f q = mfma_fp8_16x16x128(weight_frag(st.b[c]), h, v4f{0.f, 0.f, 0.f, 0.f});
+      asm volatile("" : "+v"(q));   // the product is the whole wave's, made before lanes part
       if (st.live) {   // other tokens take nothing, not even a NaN weight's product with 0
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[c][j] = fmaf(q[j], s, acc[c][j]);
