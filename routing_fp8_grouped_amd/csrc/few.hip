@@ -859,8 +859,8 @@ hipError_t launch_layer_few(const uint16_t* x, const uint16_t* wg, const float* 
   hipLaunchKernelGGL((few_down_kernel<C, RING, STAGE, POW2>), g4, dim3(FW_THREADS), 0, stream, p)
   if (d > 256 * 16) {   // more than 16 columns a workgroup
     if (!stage) MOE_FEW_DOWN(2, 4, false, false);
-    else if (pow2) MOE_FEW_DOWN(2, 6, true, true);
-    else MOE_FEW_DOWN(2, 6, true, false);
+    else if (pow2) MOE_FEW_DOWN(2, 5, true, true);
+    else MOE_FEW_DOWN(2, 5, true, false);
   } else {
     if (!stage) MOE_FEW_DOWN(1, 6, false, false);
     else if (pow2) MOE_FEW_DOWN(1, 6, true, true);
