@@ -282,8 +282,8 @@ struct SelectLds {
 
 // The partial logits of this thread's (token, expert) pairs: pair tid + 512 i
 // of the tokens' rows of 2^e_log2, in 2^s_log2 parts each, 16 loads in all.
-// They are issued before the first weights (behind which they would queue for
-// 4 us) and added up after.
+// The scores are made of them before the first weights are asked for: beside
+// the chip's weight loads that took 3 us instead of 1.
 struct PartialLogits {
   double v[16];
   float bias;       // of this thread's expert, the same for all its pairs
@@ -298,16 +298,22 @@ struct PartialLogits {
     }
     bias = p.bias ? p.bias[e] : 0.0f;
   }
-  // l[i]: the logit of pair i, i < 16 >> s_log2
-  __device__ __forceinline__ void sum(int s_log2, double (&l)[8]) const {
+  // The pairs' logits into z, each thread's own entries.
+  __device__ __forceinline__ void store(const FewArgs& p, double (*z)[FW_MAX_E]) {
+    double l[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) l[i] = v[2 * i] + v[2 * i + 1];
-    if (s_log2 > 1)
+    if (p.s_log2 > 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i) l[i] = l[2 * i] + l[2 * i + 1];
-    if (s_log2 > 2)
+    if (p.s_log2 > 2)
 #pragma unroll
       for (int i = 0; i < 2; ++i) l[i] = l[2 * i] + l[2 * i + 1];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int at = threadIdx.x + FW_THREADS * i;
+      if (at < (p.T << p.e_log2)) z[at >> p.e_log2][at & ((1 << p.e_log2) - 1)] = l[i];
+    }
   }
 };
 
@@ -331,39 +337,40 @@ __device__ __forceinline__ int count_above(const uint64_t* list, int n, uint64_t
   return r;
 }
 
+// Affinities, biased scores and keys from the logits in S.z (each thread's own
+// entries), and the cleared rest of the selection's LDS.
+__device__ __forceinline__ void few_scores(const FewArgs& p, SelectLds& S, FewPlan& P, float bias) {
+  const int tid = threadIdx.x, e_mask = (1 << p.e_log2) - 1, pairs = p.T << p.e_log2;
+  if (tid < FW_MAX_E / 32) S.active[tid] = 0;
+  if (tid < FW_T) S.kept[tid] = 0;
+  if (tid < FW_T * FW_MAX_E / 32) S.mask[0][tid] = 0;
+  for (int i = tid; i < (FW_MAX_E + 1) * FW_T / 4; i += FW_THREADS) reinterpret_cast<uint32_t*>(P.slot)[i] = ~0u;
+#pragma unroll 1
+  for (int at = tid; at < pairs; at += FW_THREADS) {   // one copy of exp
+    const int t = at >> p.e_log2, e = at & e_mask;
+    if (e >= p.E) continue;
+    const double s = 1.0 / (1.0 + exp(-S.z[t][e])), z = s + (double)bias;
+    S.sig[t][e] = s;
+    S.z[t][e] = z;
+    S.key[t][e] = score_key(z, e);
+  }
+}
+
 // The batch's plan in LDS.  Ranks are counted, not sorted: an expert's rank in
 // its group is the number of better ones there; the best min(k, group size) of
-// each group, in order, are all that the later steps read.
-__device__ void few_select(const FewArgs& p, SelectLds& S, FewPlan& P, const PartialLogits& part, bool write_out) {
+// each group, in order, are all that the later steps read.  `between` runs after
+// each of the first four barriers: the caller issues loads there.
+template <typename Between>
+__device__ __forceinline__ void few_select(const FewArgs& p, SelectLds& S, FewPlan& P, bool write_out,
+                                           Between between) {
   const int tid = threadIdx.x;
   const int per = p.E / p.G, n_top = p.k / p.M, keep = min(p.k, per), cand = p.G * keep;
   // i / per and i / keep for i < 256 by 16-bit reciprocals (exact: the error 255 / 65536 is below 1 / 256)
   const uint32_t inv_per = (65536 + per - 1) / per, inv_keep = (65536 + keep - 1) / keep;
   const int e_mask = (1 << p.e_log2) - 1, c_mask = (1 << p.c_log2) - 1;
   const int pairs = p.T << p.e_log2, cands = p.T << p.c_log2;
-  {
-    double l[8];
-    part.sum(p.s_log2, l);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int at = tid + FW_THREADS * i;
-      if (at < pairs) S.z[at >> p.e_log2][at & e_mask] = l[i];
-    }
-  }
-#pragma unroll 1
-  for (int at = tid; at < pairs; at += FW_THREADS) {   // one copy of exp; each thread's own entries
-    const int t = at >> p.e_log2, e = at & e_mask;
-    if (e >= p.E) continue;
-    const double s = 1.0 / (1.0 + exp(-S.z[t][e])), z = s + (double)part.bias;
-    S.sig[t][e] = s;
-    S.z[t][e] = z;
-    S.key[t][e] = score_key(z, e);
-  }
-  if (tid < FW_MAX_E / 32) S.active[tid] = 0;
-  if (tid < FW_T) S.kept[tid] = 0;
-  if (tid < FW_T * FW_MAX_E / 32) S.mask[0][tid] = 0;
-  for (int i = tid; i < (FW_MAX_E + 1) * FW_T / 4; i += FW_THREADS) reinterpret_cast<uint32_t*>(P.slot)[i] = ~0u;
   lds_barrier();
+  between(std::integral_constant<int, 0>{});
   for (int at = tid; at < pairs; at += FW_THREADS) {
     const int t = at >> p.e_log2, e = at & e_mask, g = (int)(e * inv_per >> 16);
     if (e >= p.E) continue;
@@ -372,6 +379,7 @@ __device__ void few_select(const FewArgs& p, SelectLds& S, FewPlan& P, const Par
     if (r < keep) S.best[t][g * keep + r] = k;
   }
   lds_barrier();
+  between(std::integral_constant<int, 1>{});
   for (int at = tid; at < p.T * 64; at += FW_THREADS) {
     const int t = at >> 6, g = at & 63;
     if (g >= p.G) continue;
@@ -380,6 +388,7 @@ __device__ void few_select(const FewArgs& p, SelectLds& S, FewPlan& P, const Par
     S.group[t][g] = s;
   }
   lds_barrier();
+  between(std::integral_constant<int, 2>{});
   for (int at = tid; at < p.T * 64; at += FW_THREADS) {
     const int t = at >> 6, g = at & 63;
     if (g >= p.G) continue;
@@ -394,6 +403,7 @@ __device__ void few_select(const FewArgs& p, SelectLds& S, FewPlan& P, const Par
     if (r < p.M) atomicOr(reinterpret_cast<unsigned long long*>(&S.kept[t]), 1ull << g);
   }
   lds_barrier();
+  between(std::integral_constant<int, 3>{});
   for (int at = tid; at < cands; at += FW_THREADS) {
     const int t = at >> p.c_log2, c = at & c_mask, g = (int)(c * inv_keep >> 16);
     const uint64_t kept = S.kept[t];
@@ -498,6 +508,9 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_up_kernel(const FewArgs p) 
     xq[j] = row_frag(p.xq + (size_t)t * p.d + kb * 128 + g16 * 32);
     xs[j] = p.xs[t * KB + kb];
   }
+  part.store(p, S.z);
+  few_scores(p, S, P, part.bias);
+  pin_loads();
   // offsets of this lane's loads from an item's first gate row and its scale
   const uint32_t gate_off = (r16 & 7) * p.d + (2 * g16 + (r16 >> 3)) * 16 + wave * 128;
   const uint32_t up_off = gate_off + (uint32_t)p.f * p.d;
@@ -516,16 +529,25 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_up_kernel(const FewArgs p) 
   auto scales_of = [&](int e, int n8, bool there) {
     return buffer_at(p.w13_s + ((size_t)e * 2 * FB + n8 / 16) * KB, there);
   };
-  // the first `per` items are the shared expert's, known before the selection:
-  // their loads run beneath it
+  // The first `per` items are the shared expert's, known before the selection:
+  // their loads run beneath it, three sevenths now and a seventh after each of
+  // its first steps.  A CU takes some 50 KB of loads at once; with all 115 KB
+  // here the later waves stood 3 us before the first barrier.
   int item = blockIdx.x;
   const bool early = item < per;
+  const __amdgpu_buffer_rsrc_t wb0 = weights_of(p.E, item, early), sb0 = scales_of(p.E, item, early);
+  auto load_part = [&](auto step) {
+    constexpr int from = step == 0 ? 0 : (NB * (2 + step) + 6) / 7, to = (NB * (3 + step) + 6) / 7;
+    pin_loads();
 #pragma unroll
-  for (int j = 0; j < NB; ++j) {
-    load(j, weights_of(p.E, item, early), scales_of(p.E, item, early));
-    pin_loads();   // in the loop's order
-  }
-  few_select(p, S, P, part, blockIdx.x == 0);
+    for (int j = from; j < to; ++j) {
+      load(j, wb0, sb0);
+      pin_loads();   // in the loop's order
+    }
+  };
+  load_part(std::integral_constant<int, 0>{});
+  few_select(p, S, P, blockIdx.x == 0,
+             [&](auto i) { load_part(std::integral_constant<int, decltype(i)::value + 1>{}); });
   if (blockIdx.x == 0)
     for (int i = tid; i < (int)(sizeof(FewPlan) / 4); i += FW_THREADS)
       reinterpret_cast<uint32_t*>(p.plan)[i] = reinterpret_cast<const uint32_t*>(&P)[i];
