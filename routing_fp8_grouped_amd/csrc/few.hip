@@ -655,9 +655,10 @@ __global__ __launch_bounds__(256) void few_quant_kernel(const FewArgs p) {
 // ---- kernel 4: out = sum over active experts of gate W2 h, + residual ----
 // Workgroup b owns an even share of the output columns, in units of 4: at most
 // 16 C of them, in C fragments (missing rows of the last read as zeros).  The
-// steps (active expert, K block) are dealt to the waves in turn, with RING of
-// them in flight per wave; a step's h serves all fragments.  One barrier joins
-// the waves' sums at the end.
+// steps (active expert, K block; 2 C KB of weights) are dealt to the waves in
+// turn, with RING of them in flight per wave: 64 KB per CU, beyond which rings
+// of 3 to 7 at V3 changed nothing.  A step's h serves all fragments, and one
+// barrier joins the waves' sums at the end.
 //
 // STAGE: the workgroup quantises h itself, into LDS, beneath its first weight
 // loads; otherwise the tiles come from few_quant_kernel through memory, and
@@ -880,13 +881,13 @@ hipError_t launch_layer_few(const uint16_t* x, const uint16_t* wg, const float* 
 #define MOE_FEW_DOWN(C, RING, STAGE, POW2) \
   hipLaunchKernelGGL((few_down_kernel<C, RING, STAGE, POW2>), g4, dim3(FW_THREADS), 0, stream, p)
   if (d > 256 * 16) {   // more than 16 columns a workgroup
-    if (!stage) MOE_FEW_DOWN(2, 4, false, false);
-    else if (pow2) MOE_FEW_DOWN(2, 5, true, true);
-    else MOE_FEW_DOWN(2, 5, true, false);
+    if (!stage) MOE_FEW_DOWN(2, 2, false, false);
+    else if (pow2) MOE_FEW_DOWN(2, 2, true, true);
+    else MOE_FEW_DOWN(2, 2, true, false);
   } else {
-    if (!stage) MOE_FEW_DOWN(1, 6, false, false);
-    else if (pow2) MOE_FEW_DOWN(1, 6, true, true);
-    else MOE_FEW_DOWN(1, 6, true, false);
+    if (!stage) MOE_FEW_DOWN(1, 2, false, false);
+    else if (pow2) MOE_FEW_DOWN(1, 3, true, true);
+    else MOE_FEW_DOWN(1, 3, true, false);
   }
 #undef MOE_FEW_DOWN
   return hipGetLastError();
