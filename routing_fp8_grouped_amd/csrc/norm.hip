@@ -107,7 +107,8 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 // exact inverse.  Otherwise Divider, whose quotient is correctly rounded while
 // its reciprocal and remainders are normal numbers: with s >= 2^-60 a
 // remainder is too small for that only where the quotient lies below 2^-40,
-// whose code is a zero either way.  Smaller scales take the plain division.
+// whose code is a zero either way.  Smaller scales, and the infinite one of a
+// tile that holds an infinity, take the plain division.
 template <bool POW2>
 __device__ __forceinline__ uint2 codes8(const float (&v)[8], float s) {
   float t[8];
@@ -115,7 +116,7 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], float s) {
     const float r = 1.0f / s;
 #pragma unroll
     for (int i = 0; i < 8; ++i) t[i] = v[i] * r;
-  } else if (s >= 0x1p-60f) {
+  } else if (s >= 0x1p-60f && s <= 0x1p126f) {
     const Divider div(s);
 #pragma unroll
     for (int i = 0; i < 8; ++i) t[i] = div(v[i]);

@@ -74,6 +74,25 @@ def test_extreme_magnitudes(form, scale, eps):
 
 
 @pytest.mark.parametrize("form", sorted(FORMS))
+def test_tiles_with_infinities_and_nan_are_the_quantisers(form):
+    """Infinities from a product beyond BF16's range, and a row with a NaN: y's tiles are what the quantiser makes of
+    them all the same, and the rows beside them are untouched."""
+    T, d = 4, 384
+    x, w = rows(11, T, d), weight(11, d)
+    w[3], w[200] = 3e38, -3e38
+    x[0, 3], x[2, 200] = 50.0, 50.0
+    x[3, 7] = float("nan")
+    o = buffers(T, d)
+    FORMS[form](x.to(DEV), w.to(DEV), EPS, **o)
+    assert o["y"][0, 3] == float("inf") and o["y"][2, 200] == -float("inf") and o["y"][3].isnan().all()
+    q, s = torch.empty_like(o["q"]), torch.empty_like(o["scale"])
+    (moe.fp8_quant_1x128_pow2 if form == "pow2" else moe.fp8_quant_1x128)(o["y"], q, s)
+    assert torch.equal(q, o["q"]) and torch.equal(s, o["scale"])
+    ref = onorm.rmsnorm(x[1:2].float().numpy(), None, w.float().numpy(), EPS, form)
+    assert np.array_equal(to_np(o["y"][1:2]), ref["y"])
+
+
+@pytest.mark.parametrize("form", sorted(FORMS))
 def test_tiles_are_the_quantisers(form):
     T, d = 33, 7168
     x, w = rows(1, T, d).to(DEV), weight(1, d).to(DEV)
