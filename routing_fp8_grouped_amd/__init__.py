@@ -601,10 +601,12 @@ class MoELayer:
         if getattr(self, "grad_norm", None) is None:
             self.grad_norm = torch.empty(1, dtype=torch.float32, device=self.out.device)
             self.grad_coef = torch.empty_like(self.grad_norm)
+            self.grad_ws = {}
+        # one workspace per size, kept: a captured graph may hold any of them
         n = moe_grad_norm_workspace_bytes(len(grads))
-        if getattr(self, "grad_ws", None) is None or self.grad_ws.numel() < n:
-            self.grad_ws = torch.empty(n, dtype=torch.uint8, device=self.out.device)
-        moe_grad_norm(grads, max_norm, self.grad_norm, self.grad_coef, self.grad_ws, stream)
+        if n not in self.grad_ws:
+            self.grad_ws[n] = torch.empty(n, dtype=torch.uint8, device=self.out.device)
+        moe_grad_norm(grads, max_norm, self.grad_norm, self.grad_coef, self.grad_ws[n], stream)
         moe_grad_scale(grads, self.grad_coef, stream=stream)
         return self.grad_norm
 

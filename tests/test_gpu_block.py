@@ -134,3 +134,33 @@ def test_decode_step_in_a_graph():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(L.out, want)
+
+
+def test_captured_clipping_keeps_its_workspace():
+    """A graph that clips goes on using the workspace of its own list's size after an eager call with a longer list
+    has needed a larger one."""
+    T = 33
+    cfg, x, wg, b, res, wn, W, L = setup(T)
+    L.dw13 = torch.randn(cfg.E + 1, 2 * cfg.f, cfg.d, device=DEV)
+    L.dw2 = torch.randn(cfg.E + 1, cfg.d, cfg.f, device=DEV)
+    fresh = [t.clone() for t in (L.dw13, L.dw2)]
+    L.clip_grads(1e30)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        L.clip_grads(1.0)
+    held = {n: t.data_ptr() for n, t in L.grad_ws.items()}
+    extra = [torch.randn(50 + i, device=DEV) for i in range(130)]
+    for rep in range(3):
+        L.clip_grads(1.0, extra=extra)
+        assert all(L.grad_ws[n].data_ptr() == p for n, p in held.items()) and len(L.grad_ws) == 2
+        other = torch.full((max(held),), 7, dtype=torch.uint8, device=DEV)
+        for t, f in zip((L.dw13, L.dw2), fresh):
+            t.copy_(f).mul_(rep + 1)
+        g.replay()
+        torch.cuda.synchronize()
+        assert (other == 7).all()
+        n, c = onorm.grad_norm([(f.cpu() * (rep + 1)).numpy() for f in fresh], 1.0)
+        assert abs(float(L.grad_norm) - n) <= 2.0 ** -23 * n
+        assert torch.equal(L.dw13, fresh[0] * (rep + 1) * L.grad_coef)
