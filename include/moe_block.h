@@ -36,10 +36,10 @@ extern "C" {
  * Per row: h = bf16(x + residual); rstd = fl32(1 / sqrt(sum(h^2) / d + eps)),
  * evaluated in FP64; y = bf16(fl32(fl32(h * rstd) * weight)).  (q, scale) are
  * bit for bit what fp8_quant_1x128 makes of y, whether y is stored or not.
- * No other output may overlap an input or another output.
+ * No output may otherwise overlap an input or another output.
  * T = 0 is a no-op.  MOE_ERR_INVALID_ARG: d not a positive multiple of 128,
  * eps not positive and finite, q without scale or the reverse, no output at
- * all.  MOE_ERR_UNSUPPORTED: d > 16384. */
+ * all, outputs that overlap.  MOE_ERR_UNSUPPORTED: d > 16384. */
 moe_status moe_rmsnorm_quant(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int T, int d,
                              float eps, uint16_t* sum, uint16_t* y, uint8_t* q, float* scale, float* rstd,
                              void* stream);
@@ -89,7 +89,8 @@ size_t moe_layer_few_workspace_bytes(int T, int d, int f, int E, int k);
  *   residual  [T, d] BF16 added to the output, or NULL
  *   idx, w    [T, k] int32 / FP32 out: the selection and its gates, as
  *             moe_route writes them
- *   out       [T, d] BF16 out.  May be x's or residual's own memory.
+ *   out       [T, d] BF16 out.  May be x's or residual's own memory.  No
+ *             output may otherwise overlap an input or another output.
  *   workspace at least moe_layer_few_workspace_bytes(T, d, f, E, k) bytes,
  *             16-byte aligned; overwritten; calls that share it must not overlap
  * The layer's arithmetic (the activations and h in 1x128 FP8 tiles, FP32
@@ -147,7 +148,8 @@ moe_status moe_grad_norm(const void* const* grads, const int64_t* sizes, const i
  * product rounded to the tensor's type (round to nearest even).
  *   grads, outs, sizes, types  HOST arrays as for moe_grad_norm; outs[i] may be
  *              grads[i] (in place: with a coef of 1 nothing is then read or
- *              written), and must not overlap it otherwise, nor another tensor
+ *              written), and must not overlap it otherwise, nor another output, another
+ *              tensor's gradient or coef
  *   coef       [1] FP32 on the device (moe_grad_norm's) */
 moe_status moe_grad_scale(const void* const* grads, void* const* outs, const int64_t* sizes, const int* types,
                           int n_tensors, const float* coef, void* stream);

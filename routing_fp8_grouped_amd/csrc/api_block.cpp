@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 #include <utility>
 #include <vector>
 
@@ -26,6 +27,35 @@ moe_status check_norm_shape(int T, int d) {
     if ((p) != nullptr && !aligned16(p)) return fail(MOE_ERR_INVALID_ARG, "%s is not 16-byte aligned", #p); \
   } while (0)
 
+// An operand's memory; NULL: not given.
+struct Span {
+  const char* name;
+  const void* p;
+  size_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x != 0 && y != 0 && x < y + b.bytes && y < x + a.bytes;
+}
+// No output shares memory with an input (but for `same`, whose operand it may
+// be as a whole) or with another output.
+struct Out {
+  Span span;
+  std::initializer_list<const void*> same;
+};
+moe_status check_apart(std::initializer_list<Out> outs, std::initializer_list<Span> ins) {
+  for (const Out* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span& i : ins) {
+      bool allowed = false;
+      for (const void* s : o->same) allowed = allowed || (s == i.p && s == o->span.p);
+      REQUIRE(allowed || !overlap(o->span, i), "%s must not share memory with %s", o->span.name, i.name);
+    }
+    for (const Out* b = outs.begin(); b != o; ++b)
+      REQUIRE(!overlap(o->span, b->span), "%s must not share memory with %s", o->span.name, b->span.name);
+  }
+  return MOE_OK;
+}
+
 moe_status rmsnorm_impl(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int T, int d, float eps,
                         uint16_t* sum, uint16_t* y, uint8_t* q, float* scale, float* rstd, bool pow2, void* stream) {
   moe_status s = check_norm_shape(T, d);
@@ -42,7 +72,14 @@ moe_status rmsnorm_impl(const uint16_t* x, const uint16_t* residual, const uint1
   REQUIRE_ALIGNED_OR_NULL(q);
   REQUIRE_ALIGNED4_OR_NULL(scale);
   REQUIRE_ALIGNED4_OR_NULL(rstd);
-  REQUIRE(y == nullptr || (y != sum && y != x && y != residual), "y must not be another operand's memory");
+  const size_t n = (size_t)T * d, row = (size_t)T * 4;
+  s = check_apart({{{"sum", sum, 2 * n}, {x, residual}},
+                   {{"y", y, 2 * n}, {}},
+                   {{"q", q, n}, {}},
+                   {{"scale", scale, n / 32}, {}},
+                   {{"rstd", rstd, row}, {}}},
+                  {{"x", x, 2 * n}, {"residual", residual, 2 * n}, {"weight", weight, (size_t)d * 2}});
+  if (s != MOE_OK) return s;
   return hip_status(moe::launch_rmsnorm_quant(x, residual, weight, T, d, eps, sum, y, q, scale, rstd, pow2,
                                               static_cast<hipStream_t>(stream)),
                     pow2 ? "moe_rmsnorm_quant_pow2 launch" : "moe_rmsnorm_quant launch");
@@ -87,6 +124,14 @@ moe_status layer_few_impl(const uint16_t* x, const uint16_t* wg, const float* bi
   if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need)
     return fail(MOE_ERR_WORKSPACE, "workspace %p of %zu bytes: %zu bytes, 16-byte aligned, needed", workspace,
                 workspace_bytes, need);
+  const size_t n = (size_t)T * d * 2, sel = (size_t)T * p.topk * 4, E = p.n_experts, wn = (E + 1) * f * d;
+  s = check_apart({{{"out", out, n}, {x, residual}},
+                   {{"idx", idx, sel}, {}},
+                   {{"w", w, sel}, {}},
+                   {{"workspace", workspace, need}, {}}},
+                  {{"x", x, n}, {"residual", residual, n}, {"wg", wg, E * d * 2}, {"bias", bias, E * 4},
+                   {"w13", w13, 2 * wn}, {"w13_s", w13_s, wn / 2048}, {"w2", w2, wn}, {"w2_s", w2_s, wn / 4096}});
+  if (s != MOE_OK) return s;
   return hip_status(moe::launch_layer_few(x, wg, bias, T, d, f, p.n_experts, p.n_groups, p.topk_groups, p.topk,
                                           p.route_scale, w13, w13_s, w2, w2_s, residual, idx, w, out, workspace,
                                           pow2, static_cast<hipStream_t>(stream)),
@@ -111,18 +156,33 @@ moe_status check_grads(const void* const* grads, const int64_t* sizes, const int
   return MOE_OK;
 }
 
-// No two outputs share memory (a tensor listed twice would be scaled twice).
-moe_status check_disjoint(void* const* outs, const int64_t* sizes, const int* types, int n_tensors) {
+// No output shares memory with another output (a tensor listed twice would be
+// scaled twice), with another tensor's gradient or with coef.
+moe_status check_disjoint(const void* const* grads, void* const* outs, const int64_t* sizes, const int* types,
+                          int n_tensors, const float* coef) {
   try {
     std::vector<std::pair<uintptr_t, uintptr_t>> at;
     at.reserve(n_tensors);
+    auto bytes = [&](int i) { return (uint64_t)sizes[i] * (types[i] == MOE_GRAD_FP32 ? 4 : 2); };
     for (int i = 0; i < n_tensors; ++i) {
       if (sizes[i] == 0) continue;
       const uintptr_t o = reinterpret_cast<uintptr_t>(outs[i]);
-      at.emplace_back(o, o + (uint64_t)sizes[i] * (types[i] == MOE_GRAD_FP32 ? 4 : 2));
+      at.emplace_back(o, o + bytes(i));
     }
     std::sort(at.begin(), at.end());
     for (size_t i = 1; i < at.size(); ++i) REQUIRE(at[i - 1].second <= at[i].first, "two outputs overlap");
+    // the outputs being apart, the last one that starts before `end` tells
+    auto touched = [&](uintptr_t begin, uintptr_t end) {
+      const auto it = std::lower_bound(at.begin(), at.end(), std::make_pair(end, (uintptr_t)0));
+      return it != at.begin() && (it - 1)->second > begin;
+    };
+    for (int i = 0; i < n_tensors; ++i) {
+      const uintptr_t g = reinterpret_cast<uintptr_t>(grads[i]);
+      if (sizes[i] != 0 && grads[i] != outs[i])   // in place: an output of its own, apart from the others
+        REQUIRE(!touched(g, g + bytes(i)), "an output overlaps grads[%d]", i);
+    }
+    const uintptr_t c = reinterpret_cast<uintptr_t>(coef);
+    REQUIRE(!touched(c, c + sizeof(float)), "an output overlaps coef");
   } catch (...) {
     return fail(MOE_ERR_INVALID_ARG, "n_tensors=%d: out of host memory", n_tensors);
   }
@@ -163,11 +223,17 @@ moe_status moe_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const uin
     REQUIRE_PTR4(rstd);
     REQUIRE_ALIGNED_OR_NULL(dres);
     REQUIRE_PTR(dh);
-    REQUIRE(dh != dy && dh != h, "dh must not be dy's or h's memory");
     const size_t need = rmsnorm_backward_bytes(T, d);
     if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need)
       return fail(MOE_ERR_WORKSPACE, "workspace %p of %zu bytes: %zu bytes, 16-byte aligned, needed", workspace,
                   workspace_bytes, need);
+    const size_t n = (size_t)T * d * 2;
+    s = check_apart({{{"dh", dh, n}, {dres}},
+                     {{"dweight", dweight, (size_t)d * 4}, {}},
+                     {{"workspace", workspace, need}, {}}},
+                    {{"dy", dy, n}, {"h", h, n}, {"weight", weight, (size_t)d * 2}, {"rstd", rstd, (size_t)T * 4},
+                     {"dres", dres, n}});
+    if (s != MOE_OK) return s;
   }
   return hip_status(moe::launch_rmsnorm_backward(dy, h, weight, rstd, dres, T, d, dh, dweight,
                                                  static_cast<float*>(workspace), static_cast<hipStream_t>(stream)),
@@ -175,8 +241,9 @@ moe_status moe_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const uin
 }
 
 size_t moe_layer_few_workspace_bytes(int T, int d, int f, int E, int k) {
-  clear_error();
-  if (T <= 0 || check_few(T, d, f, E, k) != MOE_OK) return 0;
+  if (T <= 0 || T > moe::kFewMaxT || d < 128 || d % 128 != 0 || d > moe::kFewMaxD || f < 128 || f % 128 != 0 ||
+      f > moe::kFewMaxF || E < 1 || E > 256 || k < 1 || k > 16 || k > E)
+    return 0;
   return moe::layer_few_workspace_bytes(T, d, f, E, k);
 }
 
@@ -215,6 +282,8 @@ moe_status moe_grad_norm(const void* const* grads, const int64_t* sizes, const i
   if (need > 0 && (workspace == nullptr || !aligned(workspace, 8) || workspace_bytes < need))
     return fail(MOE_ERR_WORKSPACE, "workspace %p of %zu bytes: %zu bytes, 8-byte aligned, needed", workspace,
                 workspace_bytes, need);
+  s = check_apart({{{"norm", norm, 4}, {}}, {{"coef", coef, 4}, {}}, {{"workspace", workspace, need}, {}}}, {});
+  if (s != MOE_OK) return s;
   return hip_status(moe::launch_grad_norm(grads, sizes, types, n_tensors, max_norm, norm, coef,
                                           static_cast<double*>(workspace), static_cast<hipStream_t>(stream)),
                     "moe_grad_norm launch");
@@ -231,13 +300,9 @@ moe_status moe_grad_scale(const void* const* grads, void* const* outs, const int
   for (int i = 0; i < n_tensors; ++i) {
     if (sizes[i] == 0) continue;
     REQUIRE(outs[i] != nullptr, "outs[%d] is NULL", i);
-    const uint64_t width = types[i] == MOE_GRAD_FP32 ? 4 : 2;
-    REQUIRE(aligned(outs[i], width), "outs[%d] is not aligned to its elements", i);
-    const uintptr_t g = reinterpret_cast<uintptr_t>(grads[i]), o = reinterpret_cast<uintptr_t>(outs[i]);
-    const uint64_t bytes = (uint64_t)sizes[i] * width;
-    REQUIRE(g == o || g + bytes <= o || o + bytes <= g, "outs[%d] overlaps grads[%d] in part", i, i);
+    REQUIRE(aligned(outs[i], types[i] == MOE_GRAD_FP32 ? 4 : 2), "outs[%d] is not aligned to its elements", i);
   }
-  s = check_disjoint(outs, sizes, types, n_tensors);
+  s = check_disjoint(grads, outs, sizes, types, n_tensors, coef);
   if (s != MOE_OK) return s;
   return hip_status(moe::launch_grad_scale(grads, outs, sizes, types, n_tensors, coef,
                                            static_cast<hipStream_t>(stream)),

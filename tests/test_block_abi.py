@@ -155,3 +155,59 @@ def test_binding_refusals():
         moe.moe_rmsnorm_quant(w, w, 1e-6, w)
     with pytest.raises(ValueError, match="GPU tensor"):
         moe.moe_rmsnorm_backward(x, x, w, w, x, w, w)
+
+
+def test_overlapping_memory_is_refused(lib):
+    """Outputs that share part of an input's or another output's memory; the same operand as a whole where the
+    header allows it is tested on the GPU."""
+    base, n = 0x100000, 4 * 256 * 2      # bytes of a BF16 operand
+    at = lambda off: P(base + off)
+    far = [P(0x1000000 * (i + 2)) for i in range(12)]
+
+    def norm(x=at(0), r=None, w=far[0], s=far[1], y=far[2], q=far[3], sc=far[4], rstd=far[5]):
+        return lib.moe_rmsnorm_quant(x, r, w, 4, 256, 1e-6, s, y, q, sc, rstd, None)
+
+    for kw, msg in [(dict(s=at(512)), "sum must not share memory with x"), (dict(s=at(-512)), "sum"),
+                    (dict(r=far[1], y=far[1]), "y must not"), (dict(r=far[6], s=P(far[6].value + n - 16)), "sum"),
+                    (dict(s=far[0]), "weight"), (dict(q=at(n - 16)), "q must not"), (dict(sc=at(n - 4)), "scale must not"),
+                    (dict(rstd=far[4]), "rstd must not share memory with scale"), (dict(q=P(far[2].value + 16)), "q must")]:
+        assert norm(**kw) == 1 and msg in last(lib), (kw, last(lib))
+
+    need = lib.moe_rmsnorm_backward_workspace_bytes(4, 256)
+
+    def bwd(dy=at(0), h=far[0], dres=None, dh=far[3], dw=far[4], ws=far[5]):
+        return lib.moe_rmsnorm_backward(dy, h, far[1], far[2], dres, 4, 256, dh, dw, ws, need, None)
+
+    for kw, msg in [(dict(dh=at(16)), "dh must not"), (dict(dres=far[6], dh=P(far[6].value + 512)), "dres"),
+                    (dict(dw=at(0)), "dweight"), (dict(ws=at(-16)), "workspace"), (dict(dw=far[5]), "workspace must not")]:
+        assert bwd(**kw) == 1 and msg in last(lib), (kw, last(lib))
+
+    need = lib.moe_layer_few_workspace_bytes(4, 256, 128, 16, 4)
+
+    def few(x=at(0), r=None, idx=far[5], w=far[6], out=far[7], ws=far[8]):
+        return lib.moe_layer_few(x, far[0], None, 4, 256, 128, _lib.RouteParams(16, 4, 2, 4, 2.5), far[1], far[2],
+                                 far[3], far[4], r, idx, w, out, ws, need, None)
+
+    for kw, msg in [(dict(out=at(512)), "out must not share memory with x"), (dict(r=at(n), out=at(512)), "out"),
+                    (dict(idx=far[6]), "w must not share memory with idx"), (dict(ws=at(-16)), "workspace"),
+                    (dict(out=far[1]), "w13"), (dict(out=P(far[8].value + need - 16)), "workspace must not")]:
+        assert few(**kw) == 1 and msg in last(lib), (kw, last(lib))
+
+    g = grads([0x10000, 0x20000], [8, 8], [0, 1])
+    scale = lambda outs, coef=A: lib.moe_grad_scale(g[0], (ctypes.c_void_p * 2)(*outs), *g[1:], coef, None)
+    for outs, coef, msg in [((0x20000, 0x30000), A, "grads[1]"), ((0x30000, 0x1001C), A, "grads[0]"),
+                            ((0x10000, 0x30000), P(0x3000C), "coef"), ((0x10000, 0x10010), A, "two outputs"),
+                            ((0x20008, 0x20000), A, "two outputs"), ((0x30000, 0x30020), P(0x30000), "coef")]:
+        assert scale(outs, coef) == 1 and msg in last(lib), (outs, last(lib))
+    need = lib.moe_grad_norm_workspace_bytes(2)
+    assert lib.moe_grad_norm(*g, 1.0, A, A, B, need, None) == 1 and "coef must not share memory with norm" in last(lib)
+    assert lib.moe_grad_norm(*g, 1.0, A, P(B.value + 64), B, need, None) == 1 and "workspace" in last(lib)
+
+
+def test_workspace_sizes_leave_the_message(lib):
+    """Asking for a size is no call that fails: the thread's message stays."""
+    assert lib.moe_rmsnorm_quant(None, None, None, -1, 128, 1e-6, *[None] * 6) == 1
+    before = last(lib)
+    assert "T=-1" in before
+    assert lib.moe_layer_few_workspace_bytes(99, 256, 128, 16, 4) == 0 and last(lib) == before
+    assert lib.moe_layer_few_workspace_bytes(4, 256, 128, 16, 4) > 0 and last(lib) == before
