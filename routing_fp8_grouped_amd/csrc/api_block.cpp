@@ -179,7 +179,7 @@ moe_status check_disjoint(const void* const* grads, void* const* outs, const int
     for (int i = 0; i < n_tensors; ++i) {
       const uintptr_t g = reinterpret_cast<uintptr_t>(grads[i]);
       if (sizes[i] != 0 && grads[i] != outs[i])   // in place: an output of its own, apart from the others
-        REQUIRE(!touched(g, g + bytes(i)), "an output overlaps grads[%d]", i);
+        REQUIRE(!touched(g, g + bytes(i)), "an output overlaps grads[%d] in part, or another tensor's", i);
     }
     const uintptr_t c = reinterpret_cast<uintptr_t>(coef);
     REQUIRE(!touched(c, c + sizeof(float)), "an output overlaps coef");
