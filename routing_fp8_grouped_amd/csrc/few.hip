@@ -24,11 +24,12 @@
 //     experts is its accumulator and the combine, in registers: expert outputs
 //     never reach memory.
 //
-// Bound by HBM reads from T = 4 on: at d 7168, f 2048, E 256, k 8 the products
-// run at 6.4 to 6.8 TB/s (a plain read of the card's memory: 7.05).  At T = 1
-// (400 MB) the launches (4.8 us for the router), the selection (9 us, of which
-// the first item's weights cover 4) and the products' starts and ends are a
-// quarter of the 77 us.
+// Bound by HBM reads from T = 4 on: at d 7168, f 2048, E 256, k 8 a call takes
+// 211 us at T = 4 (1.39 GB, 6.6 TB/s) and 677 at T = 16 (4.54 GB, 6.7 TB/s); a
+// plain read of the card's memory makes 7.05.  At T = 1 it takes 76 us for 400
+// MB, 57 at that rate: the router's kernel is 5.4 of them, the rest of the
+// difference the selection where the first weights do not cover it and the
+// starts and ends of the two products (44 and 26 us).
 #include <algorithm>
 #include <type_traits>
 
@@ -187,7 +188,10 @@ __device__ __forceinline__ float row_max(float v) {
 
 // ---- kernel 1: partial logits and the tiles of x ----
 // A workgroup takes 16 experts and one of `splits` parts of d, so that the
-// 3.7 MB of V3's router come through 128 CUs; the next kernel adds the parts.
+// 3.7 MB of V3's router come through 128 CUs (5.4 us for up to 4 tokens); the
+// next kernel adds the parts.  With more tokens every part costs that kernel
+// more loads in each workgroup: eight parts instead of two at 16 tokens took
+// 9 us off this kernel (15 -> 6) and put as many onto the next one.
 // The products run on the FP64 MFMA (16 experts by 16 tokens by 4 elements):
 // BF16 values are exact there, so the scores that the selection compares carry
 // errors of 10^-15 only, whatever the order of the sum.  (The BF16 MFMA would

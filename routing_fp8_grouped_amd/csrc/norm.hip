@@ -20,7 +20,15 @@
 //
 // Both are HBM-bound.  A row belongs to a team of threads, each holding NC
 // 16-byte chunks in registers between the sum and the second use, so every
-// operand is read once.
+// operand is read once.  At 16384 x 7168 the forward with a residual and all
+// outputs moves 1.06 GB in 182 us (5.8 TB/s), the backward with dres 0.94 GB in
+// 159 us (5.9 TB/s) and 5 us for dw; a large copy makes 4.8 TB/s, a plain read
+// 7.05.  At tens of rows a call is its launch: 3 us for 37 x 384, 5 for 64 x
+// 7168, under 7 to 8 us of the host's.
+//
+// Two chunks per thread for wide rows: one chunk (896 threads for a 7168 row)
+// took 214 us, four (256 threads) 224.  The next row's loads ahead of the
+// backward's sums gained nothing (other workgroups' loads fill that time).
 #include <algorithm>
 
 #include "common.h"
@@ -59,7 +67,7 @@ __device__ __forceinline__ V group_sum(V v, V* buf, int waves) {
   return s;
 }
 
-// Row data; STREAM: past the caches, where a call moves more than they hold.
+// Row data; STREAM: past the caches.
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 template <bool STREAM>
 __device__ __forceinline__ uint4 load16(const uint16_t* p) {
@@ -129,7 +137,7 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], float s) {
 
 // x and res are read and sum is written at the same places by the same thread,
 // the loads first, so sum may be x's or res's own memory: none is restrict.
-template <int NC, bool WAVE_ROW, bool POW2>
+template <int NC, bool WAVE_ROW, bool POW2, bool STREAM>
 __global__ __launch_bounds__(WAVE_ROW ? NORM_THREADS : 1024) void rmsnorm_quant_kernel(
     const uint16_t* x, const uint16_t* res, const uint16_t* __restrict__ w, int T, int d, float eps, uint16_t* sum,
     uint16_t* __restrict__ y, uint8_t* __restrict__ q, float* __restrict__ scale, float* __restrict__ rstd) {
@@ -147,14 +155,14 @@ __global__ __launch_bounds__(WAVE_ROW ? NORM_THREADS : 1024) void rmsnorm_quant_
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = tl + i * team;
-      if (c < chunks) h[i] = load16<false>(x + base + c * 8);
+      if (c < chunks) h[i] = load16<STREAM>(x + base + c * 8);
     }
     if (res) {
       uint4 r[NC];
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const int c = tl + i * team;
-        if (c < chunks) r[i] = load16<false>(res + base + c * 8);
+        if (c < chunks) r[i] = load16<STREAM>(res + base + c * 8);
       }
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
@@ -173,7 +181,7 @@ __global__ __launch_bounds__(WAVE_ROW ? NORM_THREADS : 1024) void rmsnorm_quant_
     for (int i = 0; i < NC; ++i) {
       const int c = tl + i * team;
       if (c < chunks) {
-        if (sum) store16<false>(sum + base + c * 8, h[i]);
+        if (sum) store16<STREAM>(sum + base + c * 8, h[i]);
         float a[8];
         unpack8(h[i], a);
 #pragma unroll
@@ -194,7 +202,7 @@ __global__ __launch_bounds__(WAVE_ROW ? NORM_THREADS : 1024) void rmsnorm_quant_
 #pragma unroll
         for (int j = 0; j < 8; ++j) a[j] = (a[j] * rs) * g[j];
         const uint4 o = pack8(a);
-        if (y) store16<false>(y + base + c * 8, o);
+        if (y) store16<STREAM>(y + base + c * 8, o);
         if (q) {
           float v[8], amax = 0.0f;
           unpack8(o, v);
@@ -330,9 +338,23 @@ __global__ __launch_bounds__(1024) void rmsnorm_dw_kernel(const float* __restric
   }
 }
 
-// Up to this width a wave owns a row (NC chunks per lane), beyond it a
-// workgroup does (2 chunks per thread).
-constexpr int kWaveRowD = 2048;
+// Up to these widths a wave owns a row, beyond them a workgroup does (2 chunks
+// per thread).  Forward: one chunk per lane; with four, up to 2048, 64 rows of
+// that width took 6.8 us against the workgroup's 4.8 and 16384 rows 65 against
+// 61.  Backward: up to four chunks per lane, since the waves share their dw
+// sums: 16384 rows of 1152 take 35 us against the workgroup's 57, of 2048 55
+// against 64 (64 rows: 6.5 against 5.9).
+constexpr int kForwardWaveD = 512;
+constexpr int kBackwardWaveD = 2048;
+
+// Calls that move more than this go past the caches; below it what they write
+// is still there for the kernel that reads it next.  Forward and the router
+// and two readers of its outputs after it, 7168 wide, us through the caches and
+// past them: 2048 rows (132 MB) 104.5 and 106.8, 4096 rows (264 MB) 149 and
+// 146, 16384 rows 420 and 413.  Backward between a writer of dy and a reader of
+// dh: 1024 rows (59 MB) 31 and 32, 2048 rows (117 MB) 51.7 and 49.1.
+constexpr size_t kForwardCached = size_t(192) << 20;
+constexpr size_t kBackwardCached = size_t(96) << 20;
 
 int group_threads(int d) { return ((d / 16) + 63) / 64 * 64; }
 
@@ -341,27 +363,29 @@ int group_threads(int d) { return ((d / 16) + 63) / 64 * 64; }
 hipError_t launch_rmsnorm_quant(const uint16_t* x, const uint16_t* res, const uint16_t* w, int T, int d, float eps,
                                 uint16_t* sum, uint16_t* y, uint8_t* q, float* scale, float* rstd, bool pow2,
                                 hipStream_t stream) {
+  const bool past_caches = (size_t)T * d * 9 > kForwardCached;
+#define MOE_NORM_ONE(NC, WR, THREADS, POW2, STREAM)                                                                 \
+  hipLaunchKernelGGL((rmsnorm_quant_kernel<NC, WR, POW2, STREAM>), grid, dim3(THREADS), 0, stream, x, res, w, T, d, \
+                     eps, sum, y, q, scale, rstd)
 #define MOE_NORM(NC, WR, THREADS, ROWS)                                                                             \
   do {                                                                                                              \
     const dim3 grid((unsigned)std::min((long)(1 << 20), ((long)T + (ROWS)-1) / (ROWS)));                            \
-    if (pow2)                                                                                                       \
-      hipLaunchKernelGGL((rmsnorm_quant_kernel<NC, WR, true>), grid, dim3(THREADS), 0, stream, x, res, w, T, d,     \
-                         eps, sum, y, q, scale, rstd);                                                              \
-    else                                                                                                            \
-      hipLaunchKernelGGL((rmsnorm_quant_kernel<NC, WR, false>), grid, dim3(THREADS), 0, stream, x, res, w, T, d,    \
-                         eps, sum, y, q, scale, rstd);                                                              \
+    if (pow2 && past_caches) MOE_NORM_ONE(NC, WR, THREADS, true, true);                                             \
+    else if (pow2) MOE_NORM_ONE(NC, WR, THREADS, true, false);                                                      \
+    else if (past_caches) MOE_NORM_ONE(NC, WR, THREADS, false, true);                                               \
+    else MOE_NORM_ONE(NC, WR, THREADS, false, false);                                                               \
   } while (0)
-  if (d <= 512) MOE_NORM(1, true, NORM_THREADS, NORM_THREADS / 64);
-  else if (d <= kWaveRowD) MOE_NORM(4, true, NORM_THREADS, NORM_THREADS / 64);
+  if (d <= kForwardWaveD) MOE_NORM(1, true, NORM_THREADS, NORM_THREADS / 64);
   else MOE_NORM(2, false, group_threads(d), 1);
 #undef MOE_NORM
+#undef MOE_NORM_ONE
   return hipGetLastError();
 }
 
 // Workgroups of the backward's first kernel: enough to fill the chip, few
 // enough that their partial rows stay a small part of the traffic.
 int rmsnorm_backward_groups(int T, int d) {
-  const int rows = d <= kWaveRowD ? NORM_THREADS / 64 : 1;
+  const int rows = d <= kBackwardWaveD ? NORM_THREADS / 64 : 1;
   return (int)std::min((long)512, ((long)T + rows - 1) / rows);
 }
 
@@ -369,7 +393,7 @@ hipError_t launch_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const 
                                    const uint16_t* dres, int T, int d, uint16_t* dh, float* dw, float* partial,
                                    hipStream_t stream) {
   const int n = T > 0 ? rmsnorm_backward_groups(T, d) : 0;   // no rows: dw = 0 alone
-  const bool stream_rows = (size_t)T * d * 8 > kCacheBytes;
+  const bool stream_rows = (size_t)T * d * 8 > kBackwardCached;
 #define MOE_NORM_BWD(NC, MAX, WR, THREADS)                                                                           \
   do {                                                                                                               \
     if (stream_rows)                                                                                                 \
@@ -381,7 +405,7 @@ hipError_t launch_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const 
   } while (0)
   if (n > 0) {
     if (d <= 512) MOE_NORM_BWD(1, NORM_THREADS, true, NORM_THREADS);
-    else if (d <= kWaveRowD) MOE_NORM_BWD(4, NORM_THREADS, true, NORM_THREADS);
+    else if (d <= kBackwardWaveD) MOE_NORM_BWD(4, NORM_THREADS, true, NORM_THREADS);
     else if (d <= 8192) MOE_NORM_BWD(2, 512, false, group_threads(d));
     else MOE_NORM_BWD(2, 1024, false, group_threads(d));
   }
