@@ -55,7 +55,7 @@ struct FewLayout {
   size_t part, xq, xs, h, hq, hsg, plan, total;
 };
 
-struct FewPlan {                        // written by the first product's workgroup 0
+struct alignas(16) FewPlan {            // written by the first product's workgroup 0
   int n_active;                         // the shared expert, then those with a token, ascending
   int pad[3];
   int expert[FW_MAX_E + 1];
@@ -100,6 +100,9 @@ struct FewArgs {
   int s_log2;       // parts of d in the logits' partial sums: 8, 4 or 2
   int e_log2;       // experts and candidates of a token, rounded up to powers of two
   int c_log2;
+  int per, keep, n_top;   // experts of a group; its best that the selection looks at, and those that rank it
+  uint32_t inv_per, inv_keep;   // 2^16 over them, rounded up
+  uint32_t inv_f8, inv_fb;      // 2^32 over f/8 and f/128, rounded up
   double* part;     // [splits, T, E] partial logits
   uint8_t* xq;      // [T, d]
   float* xs;        // [T, d/128]
@@ -108,6 +111,14 @@ struct FewArgs {
   float* hsg;       // [T (k+1), f/128]: scale times gate
   FewPlan* plan;
 };
+
+// All cache lines of the arguments at once, at a kernel's start: left to itself
+// the compiler loads each argument where it is first needed, and waits there.
+__device__ __forceinline__ void fetch_args(const FewArgs& p) {
+  const int* a = reinterpret_cast<const int*>(&p);
+  static_assert(sizeof(FewArgs) > 192 && sizeof(FewArgs) <= 256, "four lines of 64 bytes");
+  asm volatile("" ::"s"(a[0]), "s"(a[16]), "s"(a[32]), "s"(a[48]));
+}
 
 // Barrier that leaves this wave's loads in flight: waits for its LDS accesses
 // only (vmcnt untouched).
@@ -204,6 +215,7 @@ typedef double v4d __attribute__((ext_vector_type(4)));
 template <bool POW2>
 __global__ __launch_bounds__(FR_THREADS) void few_route_kernel(const FewArgs p) {
   __shared__ v4d red[FR_WAVES][64];
+  fetch_args(p);
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int router = (p.E + 15) / 16 << p.s_log2;
   if ((int)blockIdx.x >= router) {
@@ -368,9 +380,9 @@ template <typename Between>
 __device__ __forceinline__ void few_select(const FewArgs& p, SelectLds& S, FewPlan& P, bool write_out,
                                            Between between) {
   const int tid = threadIdx.x;
-  const int per = p.E / p.G, n_top = p.k / p.M, keep = min(p.k, per), cand = p.G * keep;
+  const int per = p.per, keep = p.keep, n_top = p.n_top, cand = p.G * keep;
   // i / per and i / keep for i < 256 by 16-bit reciprocals (exact: the error 255 / 65536 is below 1 / 256)
-  const uint32_t inv_per = (65536 + per - 1) / per, inv_keep = (65536 + keep - 1) / keep;
+  const uint32_t inv_per = p.inv_per, inv_keep = p.inv_keep;
   const int e_mask = (1 << p.e_log2) - 1, c_mask = (1 << p.c_log2) - 1;
   const int pairs = p.T << p.e_log2, cands = p.T << p.c_log2;
   lds_barrier();
@@ -494,6 +506,7 @@ template <int NB>
 __global__ __launch_bounds__(FW_THREADS, 1) void few_up_kernel(const FewArgs p) {
   __shared__ __attribute__((aligned(16))) SelectLds S;
   __shared__ FewPlan P;
+  fetch_args(p);
   // the waves' sums, where the selection's keys were (16 of their 32 KB)
   v4f (*const red)[FW_WAVES][64] = reinterpret_cast<v4f(*)[FW_WAVES][64]>(&S.key);
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
@@ -566,7 +579,7 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_up_kernel(const FewArgs p) 
   // the loads that it makes: n counts from -1 and stores nothing then.
   int next = early ? item + gridDim.x : item;
   for (int n = early ? 0 : -1; item < total; ++n) {
-    const int a = next / per, n8 = next - a * per;
+    const int a = (int)__umulhi((uint32_t)next, p.inv_f8), n8 = next - a * per;
     const bool more = next < total;
     const int e = __builtin_amdgcn_readfirstlane(P.expert[more ? a : 0]);
     const __amdgpu_buffer_rsrc_t wb = weights_of(e, n8, more), sb = scales_of(e, n8, more);
@@ -602,7 +615,7 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_up_kernel(const FewArgs p) 
         const float o0 = __shfl_xor(g0, 32), o1 = __shfl_xor(g1, 32);
         const float h0 = swiglu_f32(hi ? o0 : s[0], hi ? s[2] : o0);
         const float h1 = swiglu_f32(hi ? o1 : s[1], hi ? s[3] : o1);
-        const int ai = item / per, slot = P.slot[ai][r16];
+        const int ai = (int)__umulhi((uint32_t)item, p.inv_f8), slot = P.slot[ai][r16];
         if (slot != 255)
           *reinterpret_cast<float2*>(p.h + (size_t)(r16 * (p.k + 1) + slot) * p.f + (item - ai * per) * 8 +
                                      (g16 & 1) * 4 + (hi ? 2 : 0)) = make_float2(h0, h1);
@@ -685,26 +698,34 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_down_kernel(const FewArgs p
   __shared__ FewPlan P;
   __shared__ __attribute__((aligned(16))) v4f red[C][FW_WAVES][64];
   __shared__ __attribute__((aligned(16))) uint8_t stage[STAGE ? FW_STAGE_BYTES : 16];
+  fetch_args(p);
   constexpr int EARLY = 5;              // tiles of h a thread loads before the weights (9 rows of f 2048)
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int g16 = lane >> 4, r16 = lane & 15;
   const int FB = p.f / 128;
   const int tiles = p.T * (p.k + 1) * FB;
-  for (int i = tid; i < (int)(sizeof(FewPlan) / 4); i += FW_THREADS)
-    reinterpret_cast<uint32_t*>(&P)[i] = reinterpret_cast<const uint32_t*>(p.plan)[i];
+  // the plan, 16 bytes a thread (threads past its end the last again), on its
+  // way together with the tiles of h
+  constexpr int kPlan = sizeof(FewPlan) / 16;
+  static_assert(kPlan <= FW_THREADS && sizeof(FewPlan) % 16 == 0, "one load of the plan");
+  const int at = min(tid, kPlan - 1);
+  const uint4 plan = reinterpret_cast<const uint4*>(p.plan)[at];
+  pin_loads();
   HTile early[STAGE ? EARLY : 1];
   if (STAGE) {
 #pragma unroll
     for (int i = 0; i < EARLY; ++i)
       early[i].load(p.h + (size_t)min((tid >> 4) + i * (FW_THREADS / 16), tiles - 1) * 128 + (tid & 15) * 8);
   }
+  pin_loads();
+  reinterpret_cast<uint4*>(&P)[at] = plan;
   lds_barrier();
   const int steps = __builtin_amdgcn_readfirstlane(P.n_active) * FB;
+  // 256 workgroups share the d/4 units, or there is one for each
   const int units = p.d / 4;
-  const int c_begin = 4 * (int)((long)units * blockIdx.x / gridDim.x);
-  const int c_end = 4 * (int)((long)units * (blockIdx.x + 1) / gridDim.x);
-  // a step's expert: step / FB by a rounded-up reciprocal, exact for step * FB < 2^32
-  const uint32_t inv = (uint32_t)((0x100000000ull + FB - 1) / FB);
+  const int c_begin = 4 * (units >= 256 ? units * (int)blockIdx.x >> 8 : (int)blockIdx.x);
+  const int c_end = 4 * (units >= 256 ? units * ((int)blockIdx.x + 1) >> 8 : (int)blockIdx.x + 1);
+  const uint32_t inv = p.inv_fb;        // a step's expert: step / FB
   const int hstride = p.f + 16;         // staged rows, 16 bytes apart in the banks
   float* const stage_s = reinterpret_cast<float*>(stage + p.T * (p.k + 1) * hstride);
   // this lane's offsets from an expert's weights and scales
@@ -780,30 +801,40 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_down_kernel(const FewArgs p
       *reinterpret_cast<uint2*>(stage + row * hstride + (tile - row * FB) * 128 + (tid & 15) * 8) = q;
       if ((tid & 15) == 0) stage_s[tile] = s * P.gate[row];
     };
+    // One copy of the quantisation's code for the tiles loaded early, which shift
+    // down to it, and one for tiles past them.
+    int tile = tid >> 4;
+#pragma unroll 1
+    for (int i = 0; i < EARLY && i * (FW_THREADS / 16) < tiles; ++i, tile += FW_THREADS / 16) {
+      put(min(tile, tiles - 1), early[0]);   // past the last tile the last again, the same bytes
 #pragma unroll
-    for (int i = 0; i < EARLY; ++i)
-      if (i * (FW_THREADS / 16) < tiles)   // past the last tile the last again, the same bytes
-        put(min((tid >> 4) + i * (FW_THREADS / 16), tiles - 1), early[i]);
-    for (int tile = (tid >> 4) + EARLY * (FW_THREADS / 16); tile < tiles; tile += FW_THREADS / 16) {
+      for (int j = 0; j + 1 < EARLY; ++j) early[j] = early[j + 1];
+    }
+#pragma unroll 1
+    for (; tile < tiles; tile += FW_THREADS / 16) {
       HTile h;
       h.load(p.h + (size_t)tile * 128 + (tid & 15) * 8);
       put(tile, h);
     }
     lds_barrier();
   }
-  // `turns` steps per wave; steps past the end are zeros.  Leaving the last
-  // group early saves a small layer 1 us; in the other form the branch cost 4%.
+  // `turns` steps per wave (some of the last turn's are zeros), RING at a time;
+  // the rest apart: with a way out of the loop's middle the compiler would take
+  // any step's loads for the latest and wait for all of them in each turn.
   const int turns = (steps + FW_WAVES - 1) / FW_WAVES;
-  for (int u = 0; u < turns; u += RING) {
+  int left = turns;
+  for (; left >= RING; left -= RING) {
 #pragma unroll
     for (int r = 0; r < RING; ++r) {
-      if (STAGE && u + r >= turns) break;
       use(ring[r]);
       pin_loads();
       load(ring[r]);
       pin_loads();
     }
   }
+#pragma unroll
+  for (int r = 0; r + 1 < RING; ++r)
+    if (r < left) use(ring[r]);
 #pragma unroll
   for (int c = 0; c < C; ++c) red[c][wave][lane] = acc[c];
   lds_barrier();
@@ -843,9 +874,17 @@ hipError_t launch_layer_few(const uint16_t* x, const uint16_t* wg, const float* 
   // parts of d: as many as let a thread of the next kernel load all parts of its pairs by 16 loads
   const int pairs = ((T << e_log2) + FW_THREADS - 1) / FW_THREADS;
   const int s_log2 = pairs <= 2 ? 3 : pairs <= 4 ? 2 : 1;
+  // Reciprocals of f/8 and f/128: items and steps come below 257 x 4096 + 512,
+  // and times a divisor below 2^32 (or the divisor is 4096, whose reciprocal is
+  // exact), so the rounding up never reaches a quotient.  f/128 = 1 is a case of
+  // its own.  Made here: a division in a kernel is hundreds of bytes of code,
+  // and its first fetch delays the kernel's first loads (measured: 0.15 us per
+  // 128 bytes).
+  auto over = [](int n) { return (uint32_t)((0x100000000ull + n - 1) / n); };
   char* ws = static_cast<char*>(workspace);
   FewArgs p{T, d, f, E, G, M, k, (double)route_scale, x, wg, bias, w13, w13_s, w2, w2_s, residual, idx, w, out,
-            s_log2, e_log2, c_log2, reinterpret_cast<double*>(ws + L.part), reinterpret_cast<uint8_t*>(ws + L.xq),
+            s_log2, e_log2, c_log2, E / G, keep, k / M, (65536u + E / G - 1) / (E / G), (65536u + keep - 1) / keep,
+            over(f / 8), over(f / 128), reinterpret_cast<double*>(ws + L.part), reinterpret_cast<uint8_t*>(ws + L.xq),
             reinterpret_cast<float*>(ws + L.xs), reinterpret_cast<float*>(ws + L.h),
             reinterpret_cast<uint8_t*>(ws + L.hq), reinterpret_cast<float*>(ws + L.hsg),
             reinterpret_cast<FewPlan*>(ws + L.plan)};
