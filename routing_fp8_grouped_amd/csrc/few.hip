@@ -31,6 +31,7 @@
 // difference the selection where the first weights do not cover it and the
 // starts and ends of the two products (44 and 26 us).
 #include <algorithm>
+#include <cstddef>
 #include <type_traits>
 
 #include "common.h"
@@ -55,13 +56,17 @@ struct FewLayout {
   size_t part, xq, xs, h, hq, hsg, plan, total;
 };
 
-struct alignas(16) FewPlan {            // written by the first product's workgroup 0
+struct FewPlan {                        // written by the first product's first two workgroups
   int n_active;                         // the shared expert, then those with a token, ascending
-  int pad[3];
   int expert[FW_MAX_E + 1];
-  float gate[FW_T * (FW_MAX_K + 1)];    // of row t (k + 1) + slot
+  int pad[2];
   uint8_t slot[FW_MAX_E + 1][FW_T];     // slot of token t in active expert a, or 255
+  float gate[FW_T * (FW_MAX_K + 1)];    // of row t (k + 1) + slot
 };
+constexpr int kPlanLoads = sizeof(FewPlan) / 16;
+constexpr int kPlan = offsetof(FewPlan, gate) / 16;    // of them without the gates
+static_assert(kPlanLoads <= FW_THREADS && sizeof(FewPlan) % 16 == 0 && offsetof(FewPlan, gate) % 16 == 0,
+              "a thread moves 16 bytes of the plan");
 
 FewLayout few_layout(int T, int d, int f, int E, int k) {
   FewLayout L;
@@ -103,7 +108,7 @@ struct FewArgs {
   int per, keep, n_top;   // experts of a group; its best that the selection looks at, and those that rank it
   uint32_t inv_per, inv_keep;   // 2^16 over them, rounded up
   uint32_t inv_f8, inv_fb;      // 2^32 over f/8 and f/128, rounded up
-  double* part;     // [splits, T, E] partial logits
+  double* part;     // [T, E, splits] partial logits
   uint8_t* xq;      // [T, d]
   float* xs;        // [T, d/128]
   float* h;         // [T (k+1), f]
@@ -278,7 +283,7 @@ __global__ __launch_bounds__(FR_THREADS) void few_route_kernel(const FewArgs p) 
     double l = red[0][lane][i];
 #pragma unroll
     for (int v = 1; v < FR_WAVES; ++v) l += red[v][lane][i];
-    if (r16 < p.T && e < p.E) p.part[((size_t)split * p.T + r16) * p.E + e] = l;
+    if (r16 < p.T && e < p.E) p.part[(r16 * p.E + e << p.s_log2) + split] = l;
   }
 }
 
@@ -288,7 +293,7 @@ struct SelectLds {
   uint64_t best[FW_T][FW_MAX_E];         // [group][rank]: keys of each group's best, in order
   double z[FW_T][FW_MAX_E];              // biased scores
   double sig[FW_T][FW_MAX_E];            // affinities
-  double group[FW_T][64];
+  uint64_t group[FW_T][64];              // the groups' sums as keys
   double gate[FW_T][FW_MAX_K];
   uint64_t kept[FW_T];                   // groups kept
   uint32_t mask[FW_T][FW_MAX_E / 32];    // experts chosen
@@ -297,44 +302,40 @@ struct SelectLds {
 };
 
 // The partial logits of this thread's (token, expert) pairs: pair tid + 512 i
-// of the tokens' rows of 2^e_log2, in 2^s_log2 parts each, 16 loads in all.
+// of the tokens' rows of 2^e_log2, in 2^s_log2 parts each, 8 loads in all.
 // The scores are made of them before the first weights are asked for: beside
 // the chip's weight loads that took 3 us instead of 1.
 struct PartialLogits {
-  double v[16];
+  double2 v[8];
   float bias;       // of this thread's expert, the same for all its pairs
 
   __device__ __forceinline__ void load(const FewArgs& p) {
     const uint32_t e = min((int)threadIdx.x & ((1 << p.e_log2) - 1), p.E - 1);
     const uint32_t t0 = threadIdx.x >> p.e_log2, dt = FW_THREADS >> p.e_log2;
+    const uint32_t h_log2 = p.s_log2 - 1;   // a pair's parts, two a load
 #pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      const uint32_t s = q & ((1 << p.s_log2) - 1), t = min(t0 + (q >> p.s_log2) * dt, (uint32_t)p.T - 1);
-      v[q] = p.part[(s * p.T + t) * p.E + e];
+    for (int q = 0; q < 8; ++q) {
+      const uint32_t t = min(t0 + (q >> h_log2) * dt, (uint32_t)p.T - 1);
+      v[q] = reinterpret_cast<const double2*>(p.part)[(t * p.E + e << h_log2) + (q & ((1 << h_log2) - 1))];
     }
     bias = p.bias ? p.bias[e] : 0.0f;
   }
-  // The pairs' logits into z, each thread's own entries.
-  __device__ __forceinline__ void store(const FewArgs& p, double (*z)[FW_MAX_E]) {
-    double l[8];
+  // The pairs' logits, in order.
+  __device__ __forceinline__ void sums(const FewArgs& p, double (&l)[8]) const {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) l[i] = v[2 * i] + v[2 * i + 1];
+    for (int i = 0; i < 8; ++i) l[i] = v[i].x + v[i].y;
     if (p.s_log2 > 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i) l[i] = l[2 * i] + l[2 * i + 1];
     if (p.s_log2 > 2)
 #pragma unroll
       for (int i = 0; i < 2; ++i) l[i] = l[2 * i] + l[2 * i + 1];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int at = threadIdx.x + FW_THREADS * i;
-      if (at < (p.T << p.e_log2)) z[at >> p.e_log2][at & ((1 << p.e_log2) - 1)] = l[i];
-    }
   }
 };
 
 // Doubles in an unsigned order, the low byte giving way to 255 - e: keys are
-// distinct, equal scores rank by the lower index, and a score moves by at most
+// distinct, equal scores rank by the lower index (of an expert or, for a sum,
+// of a group), and a score moves by at most
 // 2^-44 of itself, far below the logits' own error.  NaN scores rank last, so
 // every index below stays in range whatever the inputs.
 __device__ __forceinline__ uint64_t score_key(double z, int e) {
@@ -348,27 +349,31 @@ __device__ __forceinline__ int key_expert(uint64_t k) { return 255 - (int)(k & 2
 // Entries of list[0..n) above k.
 __device__ __forceinline__ int count_above(const uint64_t* list, int n, uint64_t k) {
   int r = 0;
-#pragma unroll 8
+#pragma unroll 4
   for (int i = 0; i < n; ++i) r += list[i] > k ? 1 : 0;
   return r;
 }
 
-// Affinities, biased scores and keys from the logits in S.z (each thread's own
-// entries), and the cleared rest of the selection's LDS.
-__device__ __forceinline__ void few_scores(const FewArgs& p, SelectLds& S, FewPlan& P, float bias) {
+// Affinities, biased scores and keys from this thread's logits, and the cleared
+// rest of the selection's LDS.
+__device__ __forceinline__ void few_scores(const FewArgs& p, SelectLds& S, FewPlan& P, double (&l)[8], float bias) {
   const int tid = threadIdx.x, e_mask = (1 << p.e_log2) - 1, pairs = p.T << p.e_log2;
+  static_assert(sizeof(P.slot) / 16 <= FW_THREADS && offsetof(FewPlan, slot) % 16 == 0, "cleared by 16 bytes a thread");
   if (tid < FW_MAX_E / 32) S.active[tid] = 0;
   if (tid < FW_T) S.kept[tid] = 0;
   if (tid < FW_T * FW_MAX_E / 32) S.mask[0][tid] = 0;
-  for (int i = tid; i < (FW_MAX_E + 1) * FW_T / 4; i += FW_THREADS) reinterpret_cast<uint32_t*>(P.slot)[i] = ~0u;
+  if (tid < (int)sizeof(P.slot) / 16) reinterpret_cast<uint4*>(P.slot)[tid] = make_uint4(~0u, ~0u, ~0u, ~0u);
 #pragma unroll 1
-  for (int at = tid; at < pairs; at += FW_THREADS) {   // one copy of exp
+  for (int at = tid; at < pairs; at += FW_THREADS) {   // one copy of exp: the logits shift down to it
     const int t = at >> p.e_log2, e = at & e_mask;
-    if (e >= p.E) continue;
-    const double s = 1.0 / (1.0 + exp(-S.z[t][e])), z = s + (double)bias;
-    S.sig[t][e] = s;
-    S.z[t][e] = z;
-    S.key[t][e] = score_key(z, e);
+    if (e < p.E) {
+      const double s = 1.0 / (1.0 + exp(-l[0])), z = s + (double)bias;
+      S.sig[t][e] = s;
+      S.z[t][e] = z;
+      S.key[t][e] = score_key(z, e);
+    }
+#pragma unroll
+    for (int i = 0; i < 7; ++i) l[i] = l[i + 1];
   }
 }
 
@@ -400,22 +405,16 @@ __device__ __forceinline__ void few_select(const FewArgs& p, SelectLds& S, FewPl
     const int t = at >> 6, g = at & 63;
     if (g >= p.G) continue;
     double s = 0.0;
+#pragma unroll 1
     for (int r = 0; r < n_top; ++r) s += S.z[t][key_expert(S.best[t][g * keep + r])];
-    S.group[t][g] = s;
+    S.group[t][g] = score_key(s, g);
   }
   lds_barrier();
   between(std::integral_constant<int, 2>{});
   for (int at = tid; at < p.T * 64; at += FW_THREADS) {
     const int t = at >> 6, g = at & 63;
     if (g >= p.G) continue;
-    const double s = S.group[t][g];
-    int r = 0;
-#pragma unroll 8
-    for (int o = 0; o < p.G; ++o) {
-      const double os = S.group[t][o];
-      // a NaN sum ranks last, among its like by index
-      r += (os > s || (s != s && os == os) || ((os == s || (s != s && os != os)) && o < g)) ? 1 : 0;
-    }
+    const int r = count_above(S.group[t], p.G, S.group[t][g]);
     if (r < p.M) atomicOr(reinterpret_cast<unsigned long long*>(&S.kept[t]), 1ull << g);
   }
   lds_barrier();
@@ -435,11 +434,11 @@ __device__ __forceinline__ void few_select(const FewArgs& p, SelectLds& S, FewPl
     }
   }
   lds_barrier();
-  // position of expert e among a bit mask's, ascending
+  // experts of a bit mask below e
   auto place = [](const uint32_t* mask, int e) {
     int a = __popc(mask[e >> 5] & ((1u << (e & 31)) - 1u));
-#pragma unroll
-    for (int i = 0; i < FW_MAX_E / 32; ++i) a += i < (e >> 5) ? __popc(mask[i]) : 0;
+#pragma unroll 2
+    for (int i = 0; i < (e >> 5); ++i) a += __popc(mask[i]);
     return a;
   };
   // a chosen expert is one of its group's best, so the candidates hold them all
@@ -456,10 +455,7 @@ __device__ __forceinline__ void few_select(const FewArgs& p, SelectLds& S, FewPl
   }
   if (tid < p.T) P.slot[0][tid] = (uint8_t)p.k;
   if (tid == FW_THREADS - 1) {
-    int n = 1;
-#pragma unroll
-    for (int i = 0; i < FW_MAX_E / 32; ++i) n += __popc(S.active[i]);
-    P.n_active = n;
+    P.n_active = 1 + place(S.active, FW_MAX_E - 1) + (int)(S.active[FW_MAX_E / 32 - 1] >> 31);
     P.expert[0] = p.E;
   }
   lds_barrier();
@@ -476,9 +472,8 @@ __device__ __forceinline__ void few_select(const FewArgs& p, SelectLds& S, FewPl
         p.w[t * p.k + j] = w;
         p.idx[t * p.k + j] = S.chosen[t][j];
       }
-      P.gate[t * (p.k + 1) + j] = w;
+      p.plan->gate[t * (p.k + 1) + j] = w;
     }
-    lds_barrier();
   }
 }
 
@@ -505,7 +500,7 @@ __device__ __forceinline__ v8bf widen8(int lo, int hi) {
 template <int NB>
 __global__ __launch_bounds__(FW_THREADS, 1) void few_up_kernel(const FewArgs p) {
   __shared__ __attribute__((aligned(16))) SelectLds S;
-  __shared__ FewPlan P;
+  __shared__ __attribute__((aligned(16))) FewPlan P;
   fetch_args(p);
   // the waves' sums, where the selection's keys were (16 of their 32 KB)
   v4f (*const red)[FW_WAVES][64] = reinterpret_cast<v4f(*)[FW_WAVES][64]>(&S.key);
@@ -525,8 +520,9 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_up_kernel(const FewArgs p) 
     xq[j] = row_frag(p.xq + (size_t)t * p.d + kb * 128 + g16 * 32);
     xs[j] = p.xs[t * KB + kb];
   }
-  part.store(p, S.z);
-  few_scores(p, S, P, part.bias);
+  double logits[8];
+  part.sums(p, logits);
+  few_scores(p, S, P, logits, part.bias);
   pin_loads();
   // offsets of this lane's loads from an item's first gate row and its scale
   const uint32_t gate_off = (r16 & 7) * p.d + (2 * g16 + (r16 >> 3)) * 16 + wave * 128;
@@ -565,9 +561,8 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_up_kernel(const FewArgs p) 
   load_part(std::integral_constant<int, 0>{});
   few_select(p, S, P, blockIdx.x == 0,
              [&](auto i) { load_part(std::integral_constant<int, decltype(i)::value + 1>{}); });
-  if (blockIdx.x == 0)
-    for (int i = tid; i < (int)(sizeof(FewPlan) / 4); i += FW_THREADS)
-      reinterpret_cast<uint32_t*>(p.plan)[i] = reinterpret_cast<const uint32_t*>(&P)[i];
+  // the plan, but for the gates, which are workgroup 0's (the grid has 32 or more)
+  if (blockIdx.x == 1 && tid < kPlan) reinterpret_cast<uint4*>(p.plan)[tid] = reinterpret_cast<const uint4*>(&P)[tid];
   const int total = __builtin_amdgcn_readfirstlane(P.n_active) * per;
   v8bf xb[NB][4];
 #pragma unroll
@@ -695,7 +690,7 @@ struct DownStep {
 
 template <int C, int RING, bool STAGE, bool POW2>
 __global__ __launch_bounds__(FW_THREADS, 1) void few_down_kernel(const FewArgs p) {
-  __shared__ FewPlan P;
+  __shared__ __attribute__((aligned(16))) FewPlan P;
   __shared__ __attribute__((aligned(16))) v4f red[C][FW_WAVES][64];
   __shared__ __attribute__((aligned(16))) uint8_t stage[STAGE ? FW_STAGE_BYTES : 16];
   fetch_args(p);
@@ -706,9 +701,7 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_down_kernel(const FewArgs p
   const int tiles = p.T * (p.k + 1) * FB;
   // the plan, 16 bytes a thread (threads past its end the last again), on its
   // way together with the tiles of h
-  constexpr int kPlan = sizeof(FewPlan) / 16;
-  static_assert(kPlan <= FW_THREADS && sizeof(FewPlan) % 16 == 0, "one load of the plan");
-  const int at = min(tid, kPlan - 1);
+  const int at = min(tid, kPlanLoads - 1);
   const uint4 plan = reinterpret_cast<const uint4*>(p.plan)[at];
   pin_loads();
   HTile early[STAGE ? EARLY : 1];
