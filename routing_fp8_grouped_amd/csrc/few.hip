@@ -25,11 +25,13 @@
 //     never reach memory.
 //
 // Bound by HBM reads from T = 4 on: at d 7168, f 2048, E 256, k 8 a call takes
-// 211 us at T = 4 (1.39 GB, 6.6 TB/s) and 677 at T = 16 (4.54 GB, 6.7 TB/s); a
-// plain read of the card's memory makes 7.05.  At T = 1 it takes 76 us for 400
+// 212 us at T = 4 (1.39 GB, 6.6 TB/s) and 658 at T = 16 (4.54 GB, 6.9 TB/s); a
+// plain read of the card's memory makes 7.05.  At T = 1 it takes 75 us for 400
 // MB, 57 at that rate: the router's kernel is 5.4 of them, the rest of the
 // difference the selection where the first weights do not cover it and the
-// starts and ends of the two products (44 and 26 us).
+// starts and ends of the two products (44 and 25 us).  Where a batch is small
+// the kernels' code counts: its first fetch takes some 0.1 us per 128 bytes, so
+// what runs once is kept short (loops rolled, divisions on the host).
 #include <algorithm>
 #include <cstddef>
 #include <type_traits>
@@ -675,7 +677,7 @@ __global__ __launch_bounds__(256) void few_quant_kernel(const FewArgs p) {
 // STAGE: the workgroup quantises h itself, into LDS, beneath its first weight
 // loads; otherwise the tiles come from few_quant_kernel through memory, and
 // lanes whose token did not choose the expert load nothing.
-constexpr int FW_STAGE_BYTES = 48 * 1024;
+constexpr int FW_STAGE_BYTES = 38 * 1024;
 static_assert(kFewMaxD <= 256 * 32, "a workgroup's columns fit two fragments");
 
 template <int C, bool STAGE>
@@ -903,10 +905,13 @@ hipError_t launch_layer_few(const uint16_t* x, const uint16_t* wg, const float* 
   if (e != hipSuccess) return e;
   const int rows = T * (k + 1);
   // h in the last kernel's LDS, quantised by every workgroup for itself, or by a
-  // kernel of its own: V3, us a call, 76.5 against 84.9 at T = 1 (18432
-  // elements of h), 135 against 138 at T = 2, 190 against 188 at T = 3
-  const bool stage = rows * f <= 40960;
-  static_assert(40960 + 16 * FW_T * (FW_MAX_K + 1) + 40960 / 32 <= FW_STAGE_BYTES, "h, its row padding and scales");
+  // kernel of its own, us a call at the elements of h: 13.8 against 15.3 at 640,
+  // 36 against 39 at 20480 (d 2048), 76.4 against 79 at 18432 (V3, T = 1), 129
+  // against 127 at 36864 (V3, T = 2), 52 against 53 and 47.3 against 47.0 at
+  // 40960 (d 2048, f 1024 and 512)
+  constexpr int kStaged = 32768;
+  const bool stage = rows * f <= kStaged;
+  static_assert(kStaged + 16 * FW_T * (FW_MAX_K + 1) + kStaged / 32 <= FW_STAGE_BYTES, "h, its row padding and scales");
   if (!stage) {
     if (pow2) hipLaunchKernelGGL(few_quant_kernel<true>, g3, dim3(256), 0, stream, p);
     else hipLaunchKernelGGL(few_quant_kernel<false>, g3, dim3(256), 0, stream, p);

@@ -114,6 +114,14 @@ def test_v3_shape(T):
     c.check(c.run(c.res), c.res)
 
 
+@pytest.mark.parametrize("shape", [(2, 128, 3, 1, 1, 2, 32768), (3, 128, 5, 1, 1, 1, 32640), (1, 128, 2, 1, 1, 1, 8320)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_widest_intermediate(shape):
+    """The largest f, where items and steps are many: their experts come from rounded-up reciprocals."""
+    c = Case(*shape, seed=sum(shape))
+    c.check(c.run(c.res), c.res)
+
+
 @pytest.mark.parametrize("T", range(1, 17))
 def test_every_batch_size(T):
     c = Case(T, 256, 16, 4, 2, 4, 128, seed=100 + T)
