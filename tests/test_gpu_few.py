@@ -141,6 +141,23 @@ def test_ties_go_to_the_lower_index():
     assert not o["out"].any()
 
 
+@pytest.mark.parametrize("low", [float("-inf"), -3.4028234663852886e38, -1e30])
+def test_bias_that_masks_experts(low):
+    """Experts masked by a bias of minus infinity or the type's lowest value: none of them is chosen while its group has
+    others to give; a group without any ranks last, and ranks among masked ones go by the index."""
+    c = Case(9, 256, 32, 8, 2, 4, 128, seed=12)
+    c.bias[torch.arange(32, device=DEV) % 4 < 2] = low
+    c.bias[8:16] = low      # two groups wholly
+    o = c.run(c.res)
+    idx = to_np(o["idx"])
+    assert (idx % 4 >= 2).all() and not ((idx >= 8) & (idx < 16)).any()
+    c.check(o, c.res)
+    c.bias.fill_(low)       # nothing left to tell the experts apart
+    o = c.run(c.res)
+    assert to_np(o["idx"]).tolist() == [[0, 1, 2, 3]] * 9
+    c.check(o, c.res)
+
+
 def test_agrees_with_the_layer():
     """The same tokens through MoELayer: the same selection and gates, outputs within the BF16 rounding of the expert
     outputs that the layer makes and this form does not, and the codes on a midpoint."""

@@ -245,3 +245,35 @@ def test_replays_in_a_graph(d):
         for n in o:
             assert torch.equal(o[n], o2[n]), n
         assert torch.equal(dh, dh2) and torch.equal(dw, dw2)
+
+
+@pytest.mark.parametrize("T,d", [(44000, 512), (9001, 2560), (3001, 7168)])
+@pytest.mark.parametrize("form", sorted(FORMS))
+def test_large_batches_are_their_parts(form, T, d):
+    """A call that moves more than the caches hold gives each row what a small call gives it, in place too; the
+    backward's dh likewise, and its dw the sum of the parts'."""
+    g = torch.Generator(device=DEV).manual_seed(T)
+    x, r = (torch.randn(T, d, generator=g, device=DEV).to(BF16) for _ in range(2))
+    w = weight(d, d).to(DEV)
+    o, keep = buffers(T, d), r.clone()
+    o["sum_out"] = r      # in place of the residual
+    FORMS[form](x, w, EPS, residual=r, **o)
+    n = 1000
+    dh, dw = torch.empty_like(x), torch.empty(d, device=DEV)
+    ws = torch.empty(moe.moe_rmsnorm_backward_workspace_bytes(T, d), dtype=torch.uint8, device=DEV)
+    moe.moe_rmsnorm_backward(o["y"], r, w, o["rstd"], dh, dw, ws, dres=x)
+    total, mag, dw1 = torch.zeros(d, dtype=torch.float64, device=DEV), torch.zeros(d, device=DEV), torch.empty(d, device=DEV)
+    for a in range(0, T, n):
+        b = min(T, a + n)
+        p = buffers(b - a, d)
+        FORMS[form](x[a:b], w, EPS, residual=keep[a:b], **p)
+        for name in p:
+            assert torch.equal(p[name], o[name][a:b]), name
+        dh1 = torch.empty_like(p["y"])
+        moe.moe_rmsnorm_backward(p["y"], p["sum_out"], w, p["rstd"], dh1, dw1, ws, dres=x[a:b])
+        assert torch.equal(dh1, dh[a:b])
+        total += dw1
+        mag += (p["y"].float() * p["sum_out"].float() * p["rstd"][:, None]).abs().sum(0)
+    # both sides: rows one after another in FP32 (at most T over the partial sums, four waves joined), two roundings a term
+    per = -(-T // (ws.numel() // (4 * d)))
+    assert ((dw.double() - total).abs() <= 2.0 ** -24 * (2 * (per + 4 + 3) * 1.001 * mag.double() + 2 * total.abs() + mag)).all()
