@@ -566,9 +566,13 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_up_kernel(const FewArgs p) 
   // the plan, but for the gates, which are workgroup 0's (the grid has 32 or more)
   if (blockIdx.x == 1 && tid < kPlan) reinterpret_cast<uint4*>(p.plan)[tid] = reinterpret_cast<const uint4*>(&P)[tid];
   const int total = __builtin_amdgcn_readfirstlane(P.n_active) * per;
-  v8bf xb[NB][4];
+  // Activations widened once, as far as the registers go: of eight blocks four
+  // are widened at each use (all of them spilled 18 registers, and the loop's
+  // waits for those took d 8192 from XX to 4.2 TB/s).
+  constexpr int WIDE = NB < 8 ? NB : 5;
+  v8bf xb[WIDE][4];
 #pragma unroll
-  for (int j = 0; j < NB; ++j)
+  for (int j = 0; j < WIDE; ++j)
 #pragma unroll
     for (int q = 0; q < 4; ++q) xb[j][q] = widen8(xq[j][2 * q], xq[j][2 * q + 1]);
 
@@ -589,8 +593,11 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_up_kernel(const FewArgs p) 
       pin_loads();
       load(j, wb, sb);
       v4f q = v4f{0.f, 0.f, 0.f, 0.f};
+      if (j >= WIDE) asm volatile("" : "+v"(xq[j]));   // or it is widened ahead of the loop all the same
 #pragma unroll
-      for (int i = 0; i < 4; ++i) q = mfma_bf16_16x16x32(widen8(w[2 * i], w[2 * i + 1]), xb[j][i], q);
+      for (int i = 0; i < 4; ++i)
+        q = mfma_bf16_16x16x32(widen8(w[2 * i], w[2 * i + 1]),
+                               j < WIDE ? xb[j < WIDE ? j : 0][i] : widen8(xq[j][2 * i], xq[j][2 * i + 1]), q);
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[i] = fmaf(q[i], s, acc[i]);
       pin_loads();
