@@ -499,13 +499,22 @@ __device__ __forceinline__ v8bf widen8(int lo, int hi) {
   return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+// Items of a turn, whose 16 KB a block are in flight together: 64 KB for one
+// and two blocks, one item from three blocks (48 KB) on.  With 64 experts and f
+// 2048, us a call at T = 16: d 1024 140 with one item, 114 with two, 110 with
+// four; d 2048 173, 154, 156; d 2560 188, 185 (but 36.9, 38.6 at T = 4 and f
+// 512); d 4096 247, 248.
+constexpr int few_items(int NB) { return NB == 1 ? 4 : NB == 2 ? 2 : 1; }
+
 template <int NB>
 __global__ __launch_bounds__(FW_THREADS, 1) void few_up_kernel(const FewArgs p) {
   __shared__ __attribute__((aligned(16))) SelectLds S;
   __shared__ __attribute__((aligned(16))) FewPlan P;
   fetch_args(p);
-  // the waves' sums, where the selection's keys were (16 of their 32 KB)
-  v4f (*const red)[FW_WAVES][64] = reinterpret_cast<v4f(*)[FW_WAVES][64]>(&S.key);
+  // the waves' sums, where the selection's keys were
+  constexpr int D = few_items(NB);
+  v4f (*const red)[D][FW_WAVES][64] = reinterpret_cast<v4f(*)[D][FW_WAVES][64]>(&S.key);
+  static_assert(2 * sizeof(*red) <= sizeof(S.key) + sizeof(S.best) && offsetof(SelectLds, best) == sizeof(S.key));
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int g16 = lane >> 4, r16 = lane & 15;
   const int KB = p.d / 128, FB = p.f / 128, per = p.f / 8;
@@ -531,12 +540,12 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_up_kernel(const FewArgs p) 
   const uint32_t up_off = gate_off + (uint32_t)p.f * p.d;
   const uint32_t scale_off = ((g16 < 2 ? 0 : FB) * KB + wave) * 4;
   const bool last = wave + 8 * (NB - 1) < KB;   // this wave has the last block too
-  Lines b[NB];
-  float sw[NB];
-  auto load = [&](int j, __amdgpu_buffer_rsrc_t wb, __amdgpu_buffer_rsrc_t sb) {
+  Lines b[D][NB];
+  float sw[D][NB];
+  auto load = [&](int i, int j, __amdgpu_buffer_rsrc_t wb, __amdgpu_buffer_rsrc_t sb) {
     const bool there = j + 1 < NB || last;
-    b[j] = load_weight(wb, there ? gate_off + j * 1024 : kNowhere, there ? up_off + j * 1024 : kNowhere);
-    sw[j] = load_scale(sb, there ? scale_off + j * 32 : kNowhere);
+    b[i][j] = load_weight(wb, there ? gate_off + j * 1024 : kNowhere, there ? up_off + j * 1024 : kNowhere);
+    sw[i][j] = load_scale(sb, there ? scale_off + j * 32 : kNowhere);
   };
   auto weights_of = [&](int e, int n8, bool there) {
     return buffer_at(p.w13 + ((size_t)e * 2 * p.f + n8 * 8) * p.d, there);
@@ -548,70 +557,84 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_up_kernel(const FewArgs p) 
   // their loads run beneath it, three sevenths now and a seventh after each of
   // its first steps.  A CU takes some 50 KB of loads at once; with all 115 KB
   // here the later waves stood 3 us before the first barrier.
-  int item = blockIdx.x;
-  const bool early = item < per;
-  const __amdgpu_buffer_rsrc_t wb0 = weights_of(p.E, item, early), sb0 = scales_of(p.E, item, early);
+  const bool early = (int)blockIdx.x < per;
+  const __amdgpu_buffer_rsrc_t wb0 = weights_of(p.E, blockIdx.x, early), sb0 = scales_of(p.E, blockIdx.x, early);
   auto load_part = [&](auto step) {
     constexpr int from = step == 0 ? 0 : (NB * (2 + step) + 6) / 7, to = (NB * (3 + step) + 6) / 7;
     pin_loads();
 #pragma unroll
     for (int j = from; j < to; ++j) {
-      load(j, wb0, sb0);
+      load(D - 1, j, wb0, sb0);
       pin_loads();   // in the loop's order
     }
   };
+#pragma unroll
+  for (int i = 0; i + 1 < D; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) b[i][j] = Lines{}, sw[i][j] = 0.0f;
   load_part(std::integral_constant<int, 0>{});
   few_select(p, S, P, blockIdx.x == 0,
              [&](auto i) { load_part(std::integral_constant<int, decltype(i)::value + 1>{}); });
   // the plan, but for the gates, which are workgroup 0's (the grid has 32 or more)
   if (blockIdx.x == 1 && tid < kPlan) reinterpret_cast<uint4*>(p.plan)[tid] = reinterpret_cast<const uint4*>(&P)[tid];
   const int total = __builtin_amdgcn_readfirstlane(P.n_active) * per;
-  // Activations widened once, as far as the registers go: of eight blocks four
-  // are widened at each use (all of them spilled 18 registers, and the loop's
-  // waits for those took d 8192 from XX to 4.2 TB/s).
-  constexpr int WIDE = NB < 8 ? NB : 5;
-  v8bf xb[WIDE][4];
-#pragma unroll
-  for (int j = 0; j < WIDE; ++j)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) xb[j][q] = widen8(xq[j][2 * q], xq[j][2 * q + 1]);
 
-  // A workgroup whose first item was not known runs the loop once on zeros for
-  // the loads that it makes: n counts from -1 and stores nothing then.
-  int next = early ? item + gridDim.x : item;
-  for (int n = early ? 0 : -1; item < total; ++n) {
-    const int a = (int)__umulhi((uint32_t)next, p.inv_f8), n8 = next - a * per;
-    const bool more = next < total;
-    const int e = __builtin_amdgcn_readfirstlane(P.expert[more ? a : 0]);
-    const __amdgpu_buffer_rsrc_t wb = weights_of(e, n8, more), sb = scales_of(e, n8, more);
-    v4f acc = v4f{0.f, 0.f, 0.f, 0.f};
+  // This workgroup's items are blockIdx + q gridDim, q = 0, 1, ...; a turn takes
+  // D of them, q .. q + D - 1, and loads the next turn's.  Of the first turn at
+  // most the last is there, the one loaded before the selection; the others,
+  // and items past the end, are zeros that nothing is loaded for.
+  int rot = 0, half = 0;
+  for (int q = early ? 1 - D : -D; q < 0 || (int)blockIdx.x + q * (int)gridDim.x < total; q += D) {
+    asm volatile("" : "+s"(q));   // or the first turn gets a copy of the code to itself
+    __amdgpu_buffer_rsrc_t wb[D], sb[D];
+#pragma unroll
+    for (int i = 0; i < D; ++i) {
+      const int next = (int)blockIdx.x + (q + D + i) * (int)gridDim.x;
+      const bool more = next < total;
+      const int a = (int)__umulhi((uint32_t)next, p.inv_f8), n8 = next - a * per;
+      const int e = __builtin_amdgcn_readfirstlane(P.expert[more ? a : 0]);
+      wb[i] = weights_of(e, n8, more);
+      sb[i] = scales_of(e, n8, more);
+    }
+    v4f acc[D];
+#pragma unroll
+    for (int i = 0; i < D; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-      const v8i w = weight_frag(b[j]);
-      float s = sw[j] * xs[j];
-      asm volatile("" : "+v"(s));   // the product is made, and sw[j] free, before it is loaded again
-      pin_loads();
-      load(j, wb, sb);
-      v4f q = v4f{0.f, 0.f, 0.f, 0.f};
-      if (j >= WIDE) asm volatile("" : "+v"(xq[j]));   // or it is widened ahead of the loop all the same
+      // widened here for the turn's D items: widened ahead of the loop it was no
+      // faster, and eight blocks of it spilled (d 8192: 4.2 TB/s instead of 6)
+      asm volatile("" : "+v"(xq[j]));
+      v8bf x[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        q = mfma_bf16_16x16x32(widen8(w[2 * i], w[2 * i + 1]),
-                               j < WIDE ? xb[j < WIDE ? j : 0][i] : widen8(xq[j][2 * i], xq[j][2 * i + 1]), q);
+      for (int c = 0; c < 4; ++c) x[c] = widen8(xq[j][2 * c], xq[j][2 * c + 1]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = fmaf(q[i], s, acc[i]);
-      pin_loads();
+      for (int i = 0; i < D; ++i) {
+        const v8i w = weight_frag(b[i][j]);
+        float s = sw[i][j] * xs[j];
+        asm volatile("" : "+v"(s));   // the product is made, and sw free, before it is loaded again
+        pin_loads();
+        load(i, j, wb[i], sb[i]);
+        v4f t = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) t = mfma_bf16_16x16x32(widen8(w[2 * c], w[2 * c + 1]), x[c], t);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[i][c] = fmaf(t[c], s, acc[i][c]);
+        pin_loads();
+      }
     }
-    if (n >= 0) {
+    if (q + D > 0) {
       // The waves' partial sums through LDS, in two halves in turn: one barrier
-      // per item, since a half is written again only after the next item's
-      // barrier, which the wave that reads it reaches afterwards.
-      red[n & 1][wave][lane] = acc;
-      lds_barrier();
-      if (wave == (n & 7)) {
-        v4f s = red[n & 1][0][lane];
+      // per turn, since a half is written again only after the next turn's
+      // barrier, which the waves that read it reach afterwards.  A wave each
+      // for the turn's items.
 #pragma unroll
-        for (int v = 1; v < FW_WAVES; ++v) s += red[n & 1][v][lane];
+      for (int i = 0; i < D; ++i) red[half][i][wave][lane] = acc[i];
+      lds_barrier();
+      const int i = (wave - rot) & (FW_WAVES - 1), item = (int)blockIdx.x + (q + i) * (int)gridDim.x;
+      if (i < D && q + i >= 0 && item < total) {
+        v4f s = red[half][i][0][lane];
+#pragma unroll
+        for (int v = 1; v < FW_WAVES; ++v) s += red[half][i][v][lane];
         // lanes 0..31 hold G (columns 4 g16 .. +3), lanes 32..63 U of the same
         // columns: each half takes two of the four
         const bool hi = g16 >= 2;
@@ -619,14 +642,14 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_up_kernel(const FewArgs p) 
         const float o0 = __shfl_xor(g0, 32), o1 = __shfl_xor(g1, 32);
         const float h0 = swiglu_f32(hi ? o0 : s[0], hi ? s[2] : o0);
         const float h1 = swiglu_f32(hi ? o1 : s[1], hi ? s[3] : o1);
-        const int ai = (int)__umulhi((uint32_t)item, p.inv_f8), slot = P.slot[ai][r16];
+        const int a = (int)__umulhi((uint32_t)item, p.inv_f8), slot = P.slot[a][r16];
         if (slot != 255)
-          *reinterpret_cast<float2*>(p.h + (size_t)(r16 * (p.k + 1) + slot) * p.f + (item - ai * per) * 8 +
+          *reinterpret_cast<float2*>(p.h + (size_t)(r16 * (p.k + 1) + slot) * p.f + (item - a * per) * 8 +
                                      (g16 & 1) * 4 + (hi ? 2 : 0)) = make_float2(h0, h1);
       }
-      item = next;
+      half ^= 1;
+      rot += D;
     }
-    next += gridDim.x;
   }
 }
 
