@@ -55,7 +55,7 @@ constexpr int FR_MAX_SPLITS = 8;
 
 // Device workspace (byte offsets; every part 256-byte aligned).
 struct FewLayout {
-  size_t part, xq, xs, h, hq, hsg, plan, total;
+  size_t part, xq, xs, h, hq, hsg, plan, sum, ticket, total;
 };
 
 struct FewPlan {                        // written by the first product's first two workgroups
@@ -69,6 +69,18 @@ constexpr int kPlanLoads = sizeof(FewPlan) / 16;
 constexpr int kPlan = offsetof(FewPlan, gate) / 16;    // of them without the gates
 static_assert(kPlanLoads <= FW_THREADS && sizeof(FewPlan) % 16 == 0 && offsetof(FewPlan, gate) % 16 == 0,
               "a thread moves 16 bytes of the plan");
+
+// Workgroups of the last kernel that share the steps of 16 output columns: as
+// many as fill 256, with two steps or more for each wave (a token's k + 1
+// experts have that many at least).  1: the columns are shared out instead.
+// With 64 experts, k 8, f 2048, us a call shared against not, at T = 16: d 512
+// 67, 104; d 1024 81, 111; d 2048 132, 154; at T = 1 26.5, 28.7; 27.8, 30.1;
+// 35.4, 36.3.  With 320 to 512 workgroups it was 85 to 93 at d 1024, and at d
+// 2560, where 256 are not reached without (160 of them), 193 against 188.
+constexpr int FW_MAX_SPLITS = 16;
+int few_splits(int d, int f, int k) {
+  return std::max(1, std::min({FW_MAX_SPLITS, 256 / (d / 16), (k + 1) * (f / 128) / (2 * FW_WAVES)}));
+}
 
 FewLayout few_layout(int T, int d, int f, int E, int k) {
   FewLayout L;
@@ -86,6 +98,9 @@ FewLayout few_layout(int T, int d, int f, int E, int k) {
   L.hq = take(rows * f);
   L.hsg = take(rows * (f / 128) * sizeof(float));
   L.plan = take(sizeof(FewPlan));
+  const int splits = few_splits(d, f, k);
+  L.sum = take(splits > 1 ? (size_t)splits * d * FW_T * sizeof(float) : 0);
+  L.ticket = take(splits > 1 ? (size_t)(d / 16) * sizeof(int) : 0);
   L.total = at;
   return L;
 }
@@ -109,7 +124,7 @@ struct FewArgs {
   int c_log2;
   int per, keep, n_top;   // experts of a group; its best that the selection looks at, and those that rank it
   uint32_t inv_per, inv_keep;   // 2^16 over them, rounded up
-  uint32_t inv_f8, inv_fb;      // 2^32 over f/8 and f/128, rounded up
+  uint32_t inv_f8, inv_fb, inv_groups, inv_splits;   // 2^32 over f/8, f/128, d/16 and splits, rounded up
   double* part;     // [T, E, splits] partial logits
   uint8_t* xq;      // [T, d]
   float* xs;        // [T, d/128]
@@ -117,6 +132,9 @@ struct FewArgs {
   uint8_t* hq;      // [T (k+1), f]
   float* hsg;       // [T (k+1), f/128]: scale times gate
   FewPlan* plan;
+  float* sum;       // [splits, d/16, 64, 4]: the last kernel's partial sums
+  int* ticket;      // [d/16]: how many of them are there
+  int splits;
 };
 
 // All cache lines of the arguments at once, at a kernel's start: left to itself
@@ -225,6 +243,7 @@ __global__ __launch_bounds__(FR_THREADS) void few_route_kernel(const FewArgs p) 
   fetch_args(p);
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int router = (p.E + 15) / 16 << p.s_log2;
+  if (blockIdx.x == 0 && p.splits > 1 && tid < p.d / 16) p.ticket[tid] = 0;
   if ((int)blockIdx.x >= router) {
     const int tile = ((int)blockIdx.x - router) * (FR_THREADS / 16) + (tid >> 4);
     const int sub = tid & 15;
@@ -499,20 +518,19 @@ __device__ __forceinline__ v8bf widen8(int lo, int hi) {
   return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// Items of a turn, whose 16 KB a block are in flight together: 64 KB for one
-// and two blocks, one item from three blocks (48 KB) on.  With 64 experts and f
-// 2048, us a call at T = 16: d 1024 140 with one item, 114 with two, 110 with
-// four; d 2048 173, 154, 156; d 2560 188, 185 (but 36.9, 38.6 at T = 4 and f
-// 512); d 4096 247, 248.
+// Items of a turn (D), whose 16 KB a block are in flight together: 64 KB for one
+// and two blocks (NB), one item from three blocks (48 KB) on.  With 64 experts
+// and f 2048, us a call at T = 16: d 1024 140 with one item, 114 with two, 110
+// with four; d 2048 173, 154, 156; d 2560 188, 185 (but 36.9, 38.6 at T = 4 and
+// f 512); d 4096 247, 248.
 constexpr int few_items(int NB) { return NB == 1 ? 4 : NB == 2 ? 2 : 1; }
 
-template <int NB>
+template <int NB, int D>
 __global__ __launch_bounds__(FW_THREADS, 1) void few_up_kernel(const FewArgs p) {
   __shared__ __attribute__((aligned(16))) SelectLds S;
   __shared__ __attribute__((aligned(16))) FewPlan P;
   fetch_args(p);
   // the waves' sums, where the selection's keys were
-  constexpr int D = few_items(NB);
   v4f (*const red)[D][FW_WAVES][64] = reinterpret_cast<v4f(*)[D][FW_WAVES][64]>(&S.key);
   static_assert(2 * sizeof(*red) <= sizeof(S.key) + sizeof(S.best) && offsetof(SelectLds, best) == sizeof(S.key));
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
@@ -697,10 +715,11 @@ __global__ __launch_bounds__(256) void few_quant_kernel(const FewArgs p) {
 }
 
 // ---- kernel 4: out = sum over active experts of gate W2 h, + residual ----
-// Workgroup b owns an even share of the output columns, in units of 4: at most
-// 16 C of them, in C fragments (missing rows of the last read as zeros).  The
-// steps (active expert, K block; 2 C KB of weights) are dealt to the waves in
-// turn, with RING of them in flight per wave: 64 KB per CU, beyond which rings
+// A workgroup owns some output columns, up to 16 C in C fragments: an even share
+// in units of 4 (missing rows of the last fragment read as zeros), or, of narrow
+// layers, 16 whose steps several workgroups share (few_splits).
+// The steps (active expert, K block; 2 C KB of weights) are dealt to the waves
+// in turn, with RING of them in flight per wave: 64 KB per CU, beyond which rings
 // of 3 to 7 at V3 changed nothing.  A step's h serves all fragments, and one
 // barrier joins the waves' sums at the end.
 //
@@ -745,11 +764,20 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_down_kernel(const FewArgs p
   pin_loads();
   reinterpret_cast<uint4*>(&P)[at] = plan;
   lds_barrier();
-  const int steps = __builtin_amdgcn_readfirstlane(P.n_active) * FB;
-  // 256 workgroups share the d/4 units, or there is one for each
-  const int units = p.d / 4;
-  const int c_begin = 4 * (units >= 256 ? units * (int)blockIdx.x >> 8 : (int)blockIdx.x);
-  const int c_end = 4 * (units >= 256 ? units * ((int)blockIdx.x + 1) >> 8 : (int)blockIdx.x + 1);
+  const int all = __builtin_amdgcn_readfirstlane(P.n_active) * FB;
+  // Either 16 columns and a share of the steps, or all steps and a share of the
+  // d/4 units of columns, of which 256 workgroups have some each.
+  const bool shared = C == 1 && p.splits > 1;
+  const int units = p.d / 4, groups = p.d / 16;
+  const int split = shared ? (int)__umulhi(blockIdx.x, p.inv_groups) : 0, group = (int)blockIdx.x - split * groups;
+  int c_begin = 16 * group, c_end = c_begin + 16, first = 0, steps = all;
+  if (shared) {
+    first = (int)__umulhi(all * split, p.inv_splits);
+    steps = (int)__umulhi(all * (split + 1), p.inv_splits);
+  } else {
+    c_begin = 4 * (units >= 256 ? units * (int)blockIdx.x >> 8 : (int)blockIdx.x);
+    c_end = 4 * (units >= 256 ? units * ((int)blockIdx.x + 1) >> 8 : (int)blockIdx.x + 1);
+  }
   const uint32_t inv = p.inv_fb;        // a step's expert: step / FB
   const int hstride = p.f + 16;         // staged rows, 16 bytes apart in the banks
   float* const stage_s = reinterpret_cast<float*>(stage + p.T * (p.k + 1) * hstride);
@@ -768,7 +796,7 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_down_kernel(const FewArgs p
   const __amdgpu_buffer_rsrc_t hb = buffer_at(p.hq, true), gb = buffer_at(p.hsg, true);
 
   DownStep<C, STAGE> ring[RING];
-  int next = wave;                      // the step to load next
+  int next = first + wave;              // the step to load next
   auto load = [&](DownStep<C, STAGE>& st) {
     const bool there = next < steps;
     const int a = !there ? 0 : FB == 1 ? next : (int)__umulhi((uint32_t)next, inv);
@@ -846,7 +874,7 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_down_kernel(const FewArgs p
   // `turns` steps per wave (some of the last turn's are zeros), RING at a time;
   // the rest apart: with a way out of the loop's middle the compiler would take
   // any step's loads for the latest and wait for all of them in each turn.
-  const int turns = (steps + FW_WAVES - 1) / FW_WAVES;
+  const int turns = (steps - first + FW_WAVES - 1) / FW_WAVES;
   int left = turns;
   for (; left >= RING; left -= RING) {
 #pragma unroll
@@ -863,11 +891,36 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_down_kernel(const FewArgs p
 #pragma unroll
   for (int c = 0; c < C; ++c) red[c][wave][lane] = acc[c];
   lds_barrier();
-  const int col = c_begin + 16 * wave + 4 * g16;   // wave c writes fragment c
-  if (wave < C && r16 < p.T && col < c_end) {
-    v4f s = red[wave][0][lane];
+  if (wave >= C) return;
+  v4f s = red[wave][0][lane];           // wave c writes fragment c
 #pragma unroll
-    for (int v = 1; v < FW_WAVES; ++v) s += red[wave][v][lane];
+  for (int v = 1; v < FW_WAVES; ++v) s += red[wave][v][lane];
+  if (shared) {
+    // Every workgroup leaves its sum, and the last to do so, whichever it is,
+    // adds them in their order; nobody waits.  The sums are stored at device
+    // scope, past the XCD's own cache, and the wait lets the ticket be drawn
+    // only once they are there (a release fence instead writes back the whole
+    // cache: 10 to 20 us a call); the reader's fence and device-scope loads see
+    // to it that none comes from a cache of its own.
+    float* const sums = p.sum + (size_t)(group * 64 + lane) * 4;
+    const size_t stride = (size_t)groups * 256;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      __hip_atomic_store(sums + split * stride + c, s[c], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    int arrived = 0;
+    if (lane == 0) arrived = __hip_atomic_fetch_add(p.ticket + group, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (__builtin_amdgcn_readfirstlane(arrived) != p.splits - 1) return;
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    s = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int v = 0; v < p.splits; ++v)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        s[c] += __hip_atomic_load(sums + v * stride + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  const int col = c_begin + 16 * wave + 4 * g16;
+  if (r16 < p.T && col < c_end) {
     const size_t at = (size_t)r16 * p.d + col;
     if (p.residual) {
       const uint2 r = *reinterpret_cast<const uint2*>(p.residual + at);
@@ -899,20 +952,22 @@ hipError_t launch_layer_few(const uint16_t* x, const uint16_t* wg, const float* 
   // parts of d: as many as let a thread of the next kernel load all parts of its pairs by 16 loads
   const int pairs = ((T << e_log2) + FW_THREADS - 1) / FW_THREADS;
   const int s_log2 = pairs <= 2 ? 3 : pairs <= 4 ? 2 : 1;
-  // Reciprocals of f/8 and f/128: items and steps come below 257 x 4096 + 512,
-  // and times a divisor below 2^32 (or the divisor is 4096, whose reciprocal is
-  // exact), so the rounding up never reaches a quotient.  f/128 = 1 is a case of
-  // its own.  Made here: a division in a kernel is hundreds of bytes of code,
+  // Reciprocals: items and steps come below 257 x 4096 + 512, and times a divisor
+  // below 2^32 (or the divisor is 4096, whose reciprocal is exact), so the
+  // rounding up never reaches a quotient.  A divisor of 1 (f/128, splits) is a
+  // case of its own.  Made here: a division in a kernel is hundreds of bytes of code,
   // and its first fetch delays the kernel's first loads (measured: 0.15 us per
   // 128 bytes).
   auto over = [](int n) { return (uint32_t)((0x100000000ull + n - 1) / n); };
+  const int splits = few_splits(d, f, k);
   char* ws = static_cast<char*>(workspace);
   FewArgs p{T, d, f, E, G, M, k, (double)route_scale, x, wg, bias, w13, w13_s, w2, w2_s, residual, idx, w, out,
             s_log2, e_log2, c_log2, E / G, keep, k / M, (65536u + E / G - 1) / (E / G), (65536u + keep - 1) / keep,
-            over(f / 8), over(f / 128), reinterpret_cast<double*>(ws + L.part), reinterpret_cast<uint8_t*>(ws + L.xq),
+            over(f / 8), over(f / 128), over(d / 16), over(splits), reinterpret_cast<double*>(ws + L.part), reinterpret_cast<uint8_t*>(ws + L.xq),
             reinterpret_cast<float*>(ws + L.xs), reinterpret_cast<float*>(ws + L.h),
             reinterpret_cast<uint8_t*>(ws + L.hq), reinterpret_cast<float*>(ws + L.hsg),
-            reinterpret_cast<FewPlan*>(ws + L.plan)};
+            reinterpret_cast<FewPlan*>(ws + L.plan), reinterpret_cast<float*>(ws + L.sum),
+            reinterpret_cast<int*>(ws + L.ticket), splits};
   const int KB = d / 128, FB = f / 128;
   const dim3 g1(((E + 15) / 16 << s_log2) + (T * KB + FR_THREADS / 16 - 1) / (FR_THREADS / 16)), g3((T * (k + 1) * FB + 15) / 16);
   if (pow2) hipLaunchKernelGGL(few_route_kernel<true>, g1, dim3(FR_THREADS), 0, stream, p);
@@ -921,16 +976,26 @@ hipError_t launch_layer_few(const uint16_t* x, const uint16_t* wg, const float* 
   if (e != hipSuccess) return e;
   // no more workgroups than items (each active expert has f/8)
   const dim3 g2(std::min(256, std::min(E, T * k) * (f / 8) + f / 8));
+  // Several items a turn where a workgroup may have four: a layer with one each
+  // takes 14.3 us with one and 16.5 with four (tiny, T = 5), one with up to six
+  // 30.1 and 28.6 (d 1024, f 512, T = 4), with nine 33.0 and 30.2 (f 2048, T = 1).
+  const bool many = (std::min(E, T * k) + 1) * (f / 8) >= 4 * 256;
+#define MOE_FEW_UP(NB)                                                                                                \
+  do {                                                                                                                \
+    if (many) hipLaunchKernelGGL((few_up_kernel<NB, few_items(NB)>), g2, dim3(FW_THREADS), 0, stream, p);             \
+    else hipLaunchKernelGGL((few_up_kernel<NB, 1>), g2, dim3(FW_THREADS), 0, stream, p);                              \
+  } while (0)
   switch ((KB + 7) / 8) {
-    case 1: hipLaunchKernelGGL(few_up_kernel<1>, g2, dim3(FW_THREADS), 0, stream, p); break;
-    case 2: hipLaunchKernelGGL(few_up_kernel<2>, g2, dim3(FW_THREADS), 0, stream, p); break;
-    case 3: hipLaunchKernelGGL(few_up_kernel<3>, g2, dim3(FW_THREADS), 0, stream, p); break;
-    case 4: hipLaunchKernelGGL(few_up_kernel<4>, g2, dim3(FW_THREADS), 0, stream, p); break;
-    case 5: hipLaunchKernelGGL(few_up_kernel<5>, g2, dim3(FW_THREADS), 0, stream, p); break;
-    case 6: hipLaunchKernelGGL(few_up_kernel<6>, g2, dim3(FW_THREADS), 0, stream, p); break;
-    case 7: hipLaunchKernelGGL(few_up_kernel<7>, g2, dim3(FW_THREADS), 0, stream, p); break;
-    default: hipLaunchKernelGGL(few_up_kernel<8>, g2, dim3(FW_THREADS), 0, stream, p); break;
+    case 1: MOE_FEW_UP(1); break;
+    case 2: MOE_FEW_UP(2); break;
+    case 3: MOE_FEW_UP(3); break;
+    case 4: MOE_FEW_UP(4); break;
+    case 5: MOE_FEW_UP(5); break;
+    case 6: MOE_FEW_UP(6); break;
+    case 7: MOE_FEW_UP(7); break;
+    default: MOE_FEW_UP(8); break;
   }
+#undef MOE_FEW_UP
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int rows = T * (k + 1);
@@ -948,7 +1013,7 @@ hipError_t launch_layer_few(const uint16_t* x, const uint16_t* wg, const float* 
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const dim3 g4(std::min(256, d / 4));
+  const dim3 g4(splits > 1 ? d / 16 * splits : std::min(256, d / 4));
 #define MOE_FEW_DOWN(C, RING, STAGE, POW2) \
   hipLaunchKernelGGL((few_down_kernel<C, RING, STAGE, POW2>), g4, dim3(FW_THREADS), 0, stream, p)
   if (d > 256 * 16) {   // more than 16 columns a workgroup

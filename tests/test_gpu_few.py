@@ -122,6 +122,39 @@ def test_widest_intermediate(shape):
     c.check(c.run(c.res), c.res)
 
 
+@pytest.mark.parametrize("form", sorted(FORMS))
+@pytest.mark.parametrize("shape", [(16, 1536, 32, 4, 2, 4, 512), (11, 2048, 24, 4, 4, 8, 1024), (2, 512, 16, 2, 2, 8, 2048),
+                                   (16, 128, 40, 4, 2, 6, 896)], ids=lambda s: "x".join(map(str, s)))
+def test_narrow_layers(form, shape):
+    """Several items of the first product in flight; the steps of the second shared by several workgroups."""
+    c = Case(*shape, form=form, seed=sum(shape))
+    c.check(c.run(c.res), c.res)
+
+
+def test_shared_steps_repeat():
+    """Whichever workgroup comes last adds the others' sums: the bits are the same every time, eagerly, replayed, and
+    beside another call on another stream."""
+    c = Case(4, 512, 16, 2, 2, 8, 2048, seed=8)
+    want = c.run(c.res)["out"]
+    ws, o, ws2, o2 = c.workspace(), c.buffers(), c.workspace(), c.buffers()
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        for _ in range(4):
+            c.run(c.res, ws=ws, **o)
+    torch.cuda.synchronize()
+    for rep in range(20):
+        o["out"].zero_()
+        o2["out"].zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(other):
+            c.run(c.res, ws=ws2, **o2)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o["out"], want) and torch.equal(o2["out"], want), rep
+
+
 @pytest.mark.parametrize("T", range(1, 17))
 def test_every_batch_size(T):
     c = Case(T, 256, 16, 4, 2, 4, 128, seed=100 + T)
