@@ -501,8 +501,8 @@ __device__ __forceinline__ void few_select(const FewArgs& p, SelectLds& S, FewPl
 // ---- kernel 2: selection, then h = SiLU(G) U in FP32 ----
 // Item i: active expert i / (f/8), h columns 8 (i % (f/8)) .. +7.  Wave w owns
 // the K blocks w, w + 8, ... (NB = ceil(d/1024) of them): their activations
-// and scales stay in registers, and as each block's weights are consumed the
-// next item's are loaded into their place.
+// and scales stay in registers, and as each block's weights are consumed those
+// of the item D further on are loaded into their place.
 //
 // The products run as BF16 MFMAs on weights widened in registers (E4M3 values
 // are exact in BF16): the FP8 MFMA's sums of 128 products carry an error of
