@@ -95,9 +95,10 @@ size_t moe_layer_few_workspace_bytes(int T, int d, int f, int E, int k);
  *             16-byte aligned; overwritten; calls that share it must not overlap
  * The layer's arithmetic (the activations and h in 1x128 FP8 tiles, FP32
  * promotion of every K block) with two steps kept in higher precision: the
- * selection ranks FP64 scores (moe_route's FP32 ones agree except within 1e-6
- * of a tie), and the experts' outputs are summed in FP32 before the one
- * rounding of out, without being rounded to BF16 first.
+ * selection ranks FP64 scores by all their bits, equal ones by the lower index
+ * (moe_route's FP32 scores agree except within 1e-6 of a tie), and the experts'
+ * outputs are summed in FP32 before the one rounding of out, without being
+ * rounded to BF16 first.
  * T = 0 is a no-op.  Errors as moe_route and grouped_gemm_fp8_swiglu,
  * MOE_ERR_WORKSPACE, and MOE_ERR_UNSUPPORTED for T > 16, d > 8192 or f > 32768. */
 moe_status moe_layer_few(const uint16_t* x, const uint16_t* wg, const float* bias, int T, int d, int f,

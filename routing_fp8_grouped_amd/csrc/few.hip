@@ -310,9 +310,8 @@ __global__ __launch_bounds__(FR_THREADS) void few_route_kernel(const FewArgs p) 
 
 // ---- selection, by a whole workgroup, (token, expert) pairs over its threads ----
 struct SelectLds {
-  uint64_t key[FW_T][FW_MAX_E];          // score order, then lower index: larger is better
+  uint64_t key[FW_T][FW_MAX_E];          // biased scores in order: larger is better
   uint64_t best[FW_T][FW_MAX_E];         // [group][rank]: keys of each group's best, in order
-  double z[FW_T][FW_MAX_E];              // biased scores
   double sig[FW_T][FW_MAX_E];            // affinities
   uint64_t group[FW_T][64];              // the groups' sums as keys
   double gate[FW_T][FW_MAX_K];
@@ -320,6 +319,7 @@ struct SelectLds {
   uint32_t mask[FW_T][FW_MAX_E / 32];    // experts chosen
   uint32_t active[FW_MAX_E / 32];        // experts any token chose
   int16_t chosen[FW_T][FW_MAX_K];        // ascending
+  uint8_t who[FW_T][FW_MAX_E];           // the experts of `best`
 };
 
 // The partial logits of this thread's (token, expert) pairs: pair tid + 512 i
@@ -354,24 +354,32 @@ struct PartialLogits {
   }
 };
 
-// Doubles in an unsigned order, the low byte giving way to 255 - e: keys are
-// distinct, equal scores rank by the lower index (of an expert or, for a sum,
-// of a group), and a score moves by at most
-// 2^-44 of itself, far below the logits' own error.  NaN scores rank last, so
-// every index below stays in range whatever the inputs.
-__device__ __forceinline__ uint64_t score_key(double z, int e) {
+// Doubles in an unsigned order, all bits of them: scores that differ in the
+// last one rank by it.  Equal scores rank by the lower index (of an expert or,
+// for a sum, of a group).  NaN scores rank as minus infinity, so every index
+// below stays in range whatever the inputs.
+__device__ __forceinline__ uint64_t score_key(double z) {
   if (!(z == z)) z = -__builtin_huge_val();
-  uint64_t u = (uint64_t)__double_as_longlong(z + 0.0);   // -0 as +0
-  u = (u >> 63) ? ~u : u | 0x8000000000000000ull;
-  return (u & ~255ull) | (uint32_t)(255 - e);
+  const uint64_t u = (uint64_t)__double_as_longlong(z + 0.0);   // -0 as +0
+  return (u >> 63) ? ~u : u | 0x8000000000000000ull;
 }
-__device__ __forceinline__ int key_expert(uint64_t k) { return 255 - (int)(k & 255); }
+__device__ __forceinline__ double key_score(uint64_t k) {
+  return __longlong_as_double((long long)((k >> 63) ? k & 0x7FFFFFFFFFFFFFFFull : ~k));
+}
 
 // Entries of list[0..n) above k.
 __device__ __forceinline__ int count_above(const uint64_t* list, int n, uint64_t k) {
   int r = 0;
 #pragma unroll 4
   for (int i = 0; i < n; ++i) r += list[i] > k ? 1 : 0;
+  return r;
+}
+// The rank of list[own]: entries above it, and equal ones before it.  (k - 1 is
+// a key's lower neighbour: the smallest, minus infinity's, is above 0.)
+__device__ __forceinline__ int rank_of(const uint64_t* list, int n, int own, uint64_t k) {
+  int r = 0;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) r += list[i] > k - (i < own ? 1 : 0) ? 1 : 0;
   return r;
 }
 
@@ -390,8 +398,7 @@ __device__ __forceinline__ void few_scores(const FewArgs& p, SelectLds& S, FewPl
     if (e < p.E) {
       const double s = 1.0 / (1.0 + exp(-l[0])), z = s + (double)bias;
       S.sig[t][e] = s;
-      S.z[t][e] = z;
-      S.key[t][e] = score_key(z, e);
+      S.key[t][e] = score_key(z);
     }
 #pragma unroll
     for (int i = 0; i < 7; ++i) l[i] = l[i + 1];
@@ -417,8 +424,11 @@ __device__ __forceinline__ void few_select(const FewArgs& p, SelectLds& S, FewPl
     const int t = at >> p.e_log2, e = at & e_mask, g = (int)(e * inv_per >> 16);
     if (e >= p.E) continue;
     const uint64_t k = S.key[t][e];
-    const int r = count_above(&S.key[t][g * per], per, k);
-    if (r < keep) S.best[t][g * keep + r] = k;
+    const int r = rank_of(&S.key[t][g * per], per, e - g * per, k);
+    if (r < keep) {
+      S.best[t][g * keep + r] = k;
+      S.who[t][g * keep + r] = (uint8_t)e;
+    }
   }
   lds_barrier();
   between(std::integral_constant<int, 1>{});
@@ -427,15 +437,15 @@ __device__ __forceinline__ void few_select(const FewArgs& p, SelectLds& S, FewPl
     if (g >= p.G) continue;
     double s = 0.0;
 #pragma unroll 1
-    for (int r = 0; r < n_top; ++r) s += S.z[t][key_expert(S.best[t][g * keep + r])];
-    S.group[t][g] = score_key(s, g);
+    for (int r = 0; r < n_top; ++r) s += key_score(S.best[t][g * keep + r]);
+    S.group[t][g] = score_key(s);
   }
   lds_barrier();
   between(std::integral_constant<int, 2>{});
   for (int at = tid; at < p.T * 64; at += FW_THREADS) {
     const int t = at >> 6, g = at & 63;
     if (g >= p.G) continue;
-    const int r = count_above(S.group[t], p.G, S.group[t][g]);
+    const int r = rank_of(S.group[t], p.G, g, S.group[t][g]);
     if (r < p.M) atomicOr(reinterpret_cast<unsigned long long*>(&S.kept[t]), 1ull << g);
   }
   lds_barrier();
@@ -446,10 +456,12 @@ __device__ __forceinline__ void few_select(const FewArgs& p, SelectLds& S, FewPl
     if (c >= cand || !((kept >> g) & 1)) continue;
     const uint64_t k = S.best[t][c];
     int r = c - g * keep;
-    for (uint64_t m = kept & ~(1ull << g); m; m &= m - 1)
-      r += count_above(&S.best[t][(__ffsll((unsigned long long)m) - 1) * keep], keep, k);
+    for (uint64_t m = kept & ~(1ull << g); m; m &= m - 1) {
+      const int o = __ffsll((unsigned long long)m) - 1;   // all its experts come before or after this one's
+      r += count_above(&S.best[t][o * keep], keep, k - (o < g ? 1 : 0));
+    }
     if (r < p.k) {
-      const int e = key_expert(k);
+      const int e = S.who[t][c];
       atomicOr(&S.mask[t][e >> 5], 1u << (e & 31));
       atomicOr(&S.active[e >> 5], 1u << (e & 31));
     }
@@ -466,7 +478,7 @@ __device__ __forceinline__ void few_select(const FewArgs& p, SelectLds& S, FewPl
   for (int at = tid; at < cands; at += FW_THREADS) {
     const int t = at >> p.c_log2, c = at & c_mask, g = (int)(c * inv_keep >> 16);
     if (c >= cand || !((S.kept[t] >> g) & 1)) continue;
-    const int e = key_expert(S.best[t][c]);
+    const int e = S.who[t][c];
     if (!((S.mask[t][e >> 5] >> (e & 31)) & 1)) continue;
     const int j = place(S.mask[t], e), a = 1 + place(S.active, e);
     S.chosen[t][j] = (int16_t)e;

@@ -305,3 +305,22 @@ def test_refusals():
     with pytest.raises(ValueError, match="w13 must have shape"):
         c.w13 = c.w13[:16]
         c.run()
+
+
+@pytest.mark.parametrize("bias", [0.0, 0.01, -0.5])
+def test_scores_apart_by_their_last_bits(bias):
+    """Saturated affinities, logits 33 to 36: FP64 scores that differ in their last bits only.  The better expert, and
+    the better group, is chosen wherever it stands."""
+    c = Case(5, 256, 16, 4, 2, 4, 128)
+    c.x.zero_()
+    c.x[:, 0] = 1
+    c.wg.zero_()
+    c.bias.fill_(bias)
+    for logits, want in (([33.0, 34.0, 35.0, 36.0] * 4, [2, 3, 6, 7]),                      # experts of a group
+                         ([33.0] * 8 + [36.0] * 4 + [34.0] * 4, [8, 9, 10, 11]),            # groups
+                         ([34.0] * 4 + [33.0] * 8 + [36.0] * 4, [12, 13, 14, 15]),
+                         ([36.0, 33.0, 33.0, 36.0] + [33.0, 35.0, 35.0, 33.0] * 3, [0, 3, 5, 6])):
+        c.wg[:, 0] = torch.tensor(logits, device=DEV)
+        o = c.run(c.res)
+        assert to_np(o["idx"]).tolist() == [want] * 5, logits
+        c.check(o, c.res)
