@@ -552,14 +552,16 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_up_kernel(const FewArgs p) 
   PartialLogits part;
   part.load(p);
   // activations of this wave's blocks; tokens past T repeat the last, a
-  // missing last block the block KB - 1 (its weights read as zeros)
+  // missing last block the block KB - 1 (its weights read as zeros, and its
+  // scale is a zero: the block's own may be infinite)
   v8i xq[NB];
   float xs[NB];
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
     const int kb = min(wave + 8 * j, KB - 1), t = min(r16, p.T - 1);
     xq[j] = row_frag(p.xq + (size_t)t * p.d + kb * 128 + g16 * 32);
-    xs[j] = p.xs[t * KB + kb];
+    const float scale = p.xs[t * KB + kb];
+    xs[j] = wave + 8 * j < KB ? scale : 0.0f;
   }
   double logits[8];
   part.sums(p, logits);
@@ -822,7 +824,7 @@ __global__ __launch_bounds__(FW_THREADS, 1) void few_down_kernel(const FewArgs p
       st.sw[c] = load_scale(sb, so[c]);
     }
     const int slot = P.slot[a][r16];
-    st.live = slot != 255;
+    st.live = there && slot != 255;     // past the end: nothing, whatever h's scale
     const uint32_t row = r16 * (p.k + 1) + slot;
     if (STAGE) {
       st.row = st.live ? row : 0;

@@ -324,3 +324,22 @@ def test_scores_apart_by_their_last_bits(bias):
         o = c.run(c.res)
         assert to_np(o["idx"]).tolist() == [want] * 5, logits
         c.check(o, c.res)
+
+
+@pytest.mark.parametrize("form", sorted(FORMS))
+@pytest.mark.parametrize("T,d,f", [(3, 384, 128), (2, 1024, 128), (16, 384, 768)])
+def test_an_infinity_comes_through(form, T, d, f):
+    """A token with an infinity, every product of which has the same sign: its output is infinite, not NaN, where waves
+    have K blocks or steps past the end too; the other tokens keep theirs."""
+    c = Case(T, d, 8, 2, 2, 2, f, form=form, seed=21)
+    col = d - 123
+    c.wg[:, col] = c.wg[:, col].abs() + 0.01    # affinities of 1
+    c.w13[:, :, col] = 0xB8                     # -1: the infinity's code is -448, so G, U and h are +inf, h's codes -448
+    c.w2 &= 0x7F                                # positive
+    x = c.x.clone()
+    x[0, col] = 1e30                            # the same selection
+    a = c.run(c.res, x=x)
+    x[0, col] = float("inf")
+    o = c.run(c.res, x=x)
+    assert (o["out"][0] == -float("inf")).all() and torch.equal(o["idx"][0], a["idx"][0])
+    assert torch.equal(o["out"][1:], a["out"][1:]) and torch.equal(o["idx"][1:], a["idx"][1:])
