@@ -698,14 +698,17 @@ struct HTile {
   // Codes into q; returns the scale.  The quotients are correctly rounded, as
   // fp8_quant_1x128's: by Divider, for which tiles with a scale below 2^-60
   // are lifted by an exact power of two so that its reciprocal and its
-  // remainders are normal numbers.
+  // remainders are normal numbers.  Of an infinite scale the quotients are
+  // zeros, and NaN of an infinity: what times 0 makes of either.
   template <bool POW2>
   __device__ __forceinline__ float quantise(uint2& q) {
     float amax = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
-    const float s = tile_scale<POW2>(row_max(amax)), lift = s < 0x1p-60f ? 0x1p80f : 1.0f;
-    const Divider div(s * lift);
+    const float s = tile_scale<POW2>(row_max(amax));
+    const bool endless = s > 0x1p126f;    // a finite one is below 2^121
+    const float lift = s < 0x1p-60f ? 0x1p80f : endless ? 0.0f : 1.0f;
+    const Divider div(endless ? 1.0f : s * lift);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = div(v[i] * lift);
     q.x = f32x4_to_e4m3(v[0], v[1], v[2], v[3]);

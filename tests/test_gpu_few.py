@@ -343,3 +343,20 @@ def test_an_infinity_comes_through(form, T, d, f):
     o = c.run(c.res, x=x)
     assert (o["out"][0] == -float("inf")).all() and torch.equal(o["idx"][0], a["idx"][0])
     assert torch.equal(o["out"][1:], a["out"][1:]) and torch.equal(o["idx"][1:], a["idx"][1:])
+
+
+@pytest.mark.parametrize("form", sorted(FORMS))
+@pytest.mark.parametrize("T,f", [(2, 128), (16, 768)])      # h quantised in the last kernel, and by a kernel of its own
+def test_codes_of_a_tile_with_an_infinity(form, T, f):
+    """One h of the shared expert beyond FP32: its tile has an infinite scale, the infinity's code is -448 and the
+    finite elements' are zeros, as fp8_quant_1x128 makes them, so an output is an infinity of the one weight's sign."""
+    c = Case(T, 256, 8, 2, 2, 2, f, form=form)
+    c.x.fill_(1)
+    one = 77                                        # this h is (256e18)^2, the others of its tile 2^-18 of that
+    c.w13[8, :128], c.w13[8, f:f + 128] = 0x01, 0x01        # 2^-9
+    c.w13[8, one], c.w13[8, f + one] = 0x38, 0x38           # 1
+    c.w13_s[8, 0], c.w13_s[8, f // 128] = 1e18, 1e18
+    o = c.run(c.res)
+    inf = torch.tensor(float("inf"), device=DEV)
+    want = c.w2[8, :, one].view(torch.float8_e4m3fn).float() * -inf     # NaN for a weight of zero
+    assert want.isinf().any() and torch.equal(o["out"].float().nan_to_num(nan=1.0), want.nan_to_num(nan=1.0).expand(T, 256))
