@@ -138,6 +138,7 @@ size_t moe_grad_norm_workspace_bytes(int n_tensors);
  *   workspace  moe_grad_norm_workspace_bytes(n_tensors) bytes, 8-byte aligned
  *              (may be NULL when that is 0); overwritten; calls that share it
  *              must not overlap
+ * norm, coef and the workspace share no memory with each other or a gradient.
  * The host arrays are read before the call returns.  Infinities and NaN in the
  * gradients are allowed and show in norm.  The same tensors give the same
  * bits.  n_tensors = 0: norm 0, coef 1. */

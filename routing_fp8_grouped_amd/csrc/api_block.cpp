@@ -156,6 +156,10 @@ moe_status check_grads(const void* const* grads, const int64_t* sizes, const int
   return MOE_OK;
 }
 
+size_t grad_bytes(const int64_t* sizes, const int* types, int i) {
+  return (size_t)sizes[i] * (types[i] == MOE_GRAD_FP32 ? 4 : 2);
+}
+
 // No output shares memory with another output (a tensor listed twice would be
 // scaled twice), with another tensor's gradient or with coef.
 moe_status check_disjoint(const void* const* grads, void* const* outs, const int64_t* sizes, const int* types,
@@ -163,7 +167,7 @@ moe_status check_disjoint(const void* const* grads, void* const* outs, const int
   try {
     std::vector<std::pair<uintptr_t, uintptr_t>> at;
     at.reserve(n_tensors);
-    auto bytes = [&](int i) { return (uint64_t)sizes[i] * (types[i] == MOE_GRAD_FP32 ? 4 : 2); };
+    auto bytes = [&](int i) { return grad_bytes(sizes, types, i); };
     for (int i = 0; i < n_tensors; ++i) {
       if (sizes[i] == 0) continue;
       const uintptr_t o = reinterpret_cast<uintptr_t>(outs[i]);
@@ -282,8 +286,14 @@ moe_status moe_grad_norm(const void* const* grads, const int64_t* sizes, const i
   if (need > 0 && (workspace == nullptr || !aligned(workspace, 8) || workspace_bytes < need))
     return fail(MOE_ERR_WORKSPACE, "workspace %p of %zu bytes: %zu bytes, 8-byte aligned, needed", workspace,
                 workspace_bytes, need);
-  s = check_apart({{{"norm", norm, 4}, {}}, {{"coef", coef, 4}, {}}, {{"workspace", workspace, need}, {}}}, {});
+  const Span outs[] = {{"norm", norm, 4}, {"coef", coef, 4}, {"workspace", workspace, need}};
+  s = check_apart({{outs[0], {}}, {outs[1], {}}, {outs[2], {}}}, {});
   if (s != MOE_OK) return s;
+  // partial sums and results are written while other workgroups still read
+  for (const Span& o : outs)
+    for (int i = 0; i < n_tensors; ++i)
+      REQUIRE(sizes[i] == 0 || !overlap(o, {"", grads[i], grad_bytes(sizes, types, i)}),
+              "%s must not share memory with grads[%d]", o.name, i);
   return hip_status(moe::launch_grad_norm(grads, sizes, types, n_tensors, max_norm, norm, coef,
                                           static_cast<double*>(workspace), static_cast<hipStream_t>(stream)),
                     "moe_grad_norm launch");

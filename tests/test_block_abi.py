@@ -211,3 +211,25 @@ def test_workspace_sizes_leave_the_message(lib):
     assert "T=-1" in before
     assert lib.moe_layer_few_workspace_bytes(99, 256, 128, 16, 4) == 0 and last(lib) == before
     assert lib.moe_layer_few_workspace_bytes(4, 256, 128, 16, 4) > 0 and last(lib) == before
+
+
+def test_grad_norm_refuses_outputs_in_the_gradients(lib):
+    """norm, coef and the workspace are written while gradients are read: none may share memory with one of them."""
+    need = lib.moe_grad_norm_workspace_bytes(3)
+    far = [P(0x1000000 * (i + 1)) for i in range(3)]
+    g = grads([0x10000, None, 0x20000], [8, 0, 8], [0, 0, 1])       # 32 bytes, none, 16 bytes
+
+    def norm(out=far[0], coef=far[1], ws=far[2], g=g, n=need):
+        return lib.moe_grad_norm(*g, 1.0, out, coef, ws, n, None)
+
+    for kw, msg in [(dict(out=P(0x10000)), "norm must not share memory with grads[0]"),
+                    (dict(out=P(0x1001C)), "norm must not share memory with grads[0]"),
+                    (dict(coef=P(0x2000C)), "coef must not share memory with grads[2]"),
+                    (dict(ws=P(0x10018)), "workspace must not share memory with grads[0]"),
+                    (dict(ws=P(0x20008)), "workspace must not share memory with grads[2]"),
+                    (dict(ws=P(0x20000 + 16 - need)), "workspace must not share memory with grads"),
+                    (dict(ws=P(0x10020 - need), coef=P(0x20000)), "coef must not share memory with grads[2]")]:
+        assert norm(**kw) == 1 and msg in last(lib), (kw, last(lib))
+    # an outer tensor whose parts the outputs are
+    whole = grads([0x1000000], [1 << 24], [0])
+    assert norm(g=whole, ws=P(0x100), n=1 << 16) == 1 and "norm must not share memory with grads[0]" in last(lib)
