@@ -391,7 +391,12 @@ class MoELayer:
     From OVERLAP_QUANT_T tokens on, the activation quantisation runs on a
     side stream of the layer's own (default priority), forked from and joined
     back into the caller's stream within ``forward``, so the calls stay
-    ordered on that stream as seen by the caller (and capturable in a graph)."""
+    ordered on that stream as seen by the caller (and capturable in a graph).
+
+    ``idx`` and ``w`` are the selection and gates of the last pass that was
+    called (captured, in a graph): ``forward`` and ``forward_normed`` share
+    one pair of arrays, ``forward_few`` has another, so that a ``backward``
+    may follow it."""
 
     def __init__(self, T, d, E, n_groups, topk_groups, topk, f, route_scale=2.5, device="cuda",
                  dispatch=False, scales="fp32"):
@@ -404,8 +409,10 @@ class MoELayer:
         self._side = None        # stream of the overlapped activation quantisation
         rows = T * topk + T
         dev = dict(device=device)
-        self.idx = torch.empty(T, topk, dtype=torch.int32, **dev)
-        self.w = torch.empty(T, topk, dtype=torch.float32, **dev)
+        self._selection, self._few_selection = (
+            (torch.empty(T, topk, dtype=torch.int32, **dev), torch.empty(T, topk, dtype=torch.float32, **dev))
+            for _ in range(2))
+        self.idx, self.w = self._selection
         self.xq = torch.empty(T, d, dtype=torch.uint8, **dev)
         self.xs = torch.empty(T, d // 128, dtype=torch.float32, **dev)
         self.offsets = torch.empty(E + 2, dtype=torch.int32, **dev)
@@ -428,6 +435,7 @@ class MoELayer:
         ``train`` the first expert GEMM also caches [G, U] in FP8 for
         ``backward`` (FP32-scale method only)."""
         mark = mark or (lambda name: None)
+        self.idx, self.w = self._selection
         quant = fp8_quant_1x128_pow2 if self.pow2 else fp8_quant_1x128
         if self.T >= OVERLAP_QUANT_T:
             # the activation quantisation does not depend on the routing: on a
@@ -489,6 +497,7 @@ class MoELayer:
         written by the norm itself.  x, residual [T, d] BF16 (residual may be
         None), norm_weight [d] BF16.  Returns out; ``self.hsum`` holds s."""
         mark = mark or (lambda name: None)
+        self.idx, self.w = self._selection
         if getattr(self, "hsum", None) is None:
             self.hsum, self.xn = torch.empty_like(self.out), torch.empty_like(self.out)
             self.rstd = torch.empty(self.T, dtype=torch.float32, device=self.out.device)
@@ -505,8 +514,12 @@ class MoELayer:
         """The layer on x [T, d] for T <= 16 by moe_layer_few: the same
         operation as ``forward`` in three or four kernels, its selection ranked
         in FP64 and its expert outputs not rounded to BF16 before they are
-        combined.  ``residual`` [T, d] is added to the output when given."""
+        combined.  ``residual`` [T, d] is added to the output when given.
+        ``forward`` ranks FP32 scores: within 1e-6 of a tie the two may choose
+        different experts for a token.  Of what the other passes leave, only
+        ``out`` is written."""
         few = moe_layer_few_pow2 if self.pow2 else moe_layer_few
+        self.idx, self.w = self._few_selection
         few(x, wg, bias, self.n_groups, self.topk_groups, self.k, self.route_scale, weights.w13q, weights.w13s,
             weights.w2q, weights.w2s, self.idx, self.w, self.out, self.few_ws, residual=residual, stream=stream)
         return self.out
@@ -551,7 +564,7 @@ class MoELayer:
         mark = mark or (lambda name: None)
         T, k, d, f, E = self.T, self.k, self.d, self.f, self.E
         rows, G = T * k + T, E + 1
-        moe_combine_backward(dout, self.y, self.pos, self.w, T * k, self.dy, self.dw, stream,
+        moe_combine_backward(dout, self.y, self.pos, self._selection[1], T * k, self.dy, self.dw, stream,
                              dyq=self.dyq, dys=self.dys)
         mark("combine_bwd")
         grouped_gemm_fp8_down(self.dyq, self.dys, self.offsets, weights_t.w2q, weights_t.w2s, self.dh, stream)

@@ -164,3 +164,22 @@ def test_captured_clipping_keeps_its_workspace():
         n, c = onorm.grad_norm([(f.cpu() * (rep + 1)).numpy() for f in fresh], 1.0)
         assert abs(float(L.grad_norm) - n) <= 2.0 ** -23 * n
         assert torch.equal(L.dw13, fresh[0] * (rep + 1) * L.grad_coef)
+
+
+def test_backward_after_a_decode_step():
+    """A few-token pass between a training forward and its backward leaves the gradients as they were."""
+    T = 16
+    cfg, x, wg, b, res, wn, W, L = setup(T)
+    Wt = W.transposed()
+    dout = torch.randn(T, cfg.d, generator=torch.Generator(device=DEV).manual_seed(2), device=DEV).to(BF16)
+    L.forward_normed(x, wn, EPS, wg, b, W, residual=res, train=True)
+    idx, w = L.idx.clone(), L.w.clone()
+    want = [t.clone() for t in L.backward_normed(dout, wn, Wt)]
+    other = L.forward_few(x.flip(0).contiguous(), wg, b, W).clone()
+    assert not torch.equal(L.idx, idx)
+    for got, ref in zip(L.backward_normed(dout, wn, Wt), want):
+        assert torch.equal(got, ref)
+    L.forward(x, wg, b, W)
+    assert not torch.equal(L.idx, idx) and torch.equal(L.forward_few(x.flip(0).contiguous(), wg, b, W), other)
+    L.forward_normed(x, wn, EPS, wg, b, W, residual=res)
+    assert torch.equal(L.idx, idx) and torch.equal(L.w, w)

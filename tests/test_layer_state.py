@@ -1,0 +1,57 @@
+"""What MoELayer keeps from one call to the next, and the calls it refuses (CPU
+only: the calls into the library are replaced by recorders)."""
+
+import pytest
+import torch
+
+import routing_fp8_grouped_amd as moe
+
+T, D, E, F = 4, 128, 8, 128
+BF16 = torch.bfloat16
+
+
+class Recorder:
+    """Stands for every call into the library; keeps the arguments of each."""
+
+    def __init__(self, monkeypatch):
+        self.calls = []
+        for name in moe.__all__:
+            if name.islower() and not name.endswith("_bytes") and name != "moe_wgrad_columns":
+                monkeypatch.setattr(moe, name, self.stand_in(name))
+
+    def stand_in(self, name):
+        return lambda *args, **kw: self.calls.append((name, args, kw))
+
+    def args(self, name):
+        return next(a for n, a, _ in reversed(self.calls) if n == name)
+
+
+@pytest.fixture
+def recorder(monkeypatch):
+    return Recorder(monkeypatch)
+
+
+def layer():
+    return moe.MoELayer(T, D, E, 2, 2, 2, F, device="cpu")
+
+
+def operands():
+    x, wg = torch.zeros(T, D, dtype=BF16), torch.zeros(E, D, dtype=BF16)
+    W = moe.MoEWeights.empty(E + 1, D, F, device="cpu")
+    return x, wg, torch.zeros(E), W, torch.ones(D, dtype=BF16)
+
+
+def test_few_tokens_leave_the_training_selection(recorder):
+    """backward reads the gates of the training forward, not those of a few-token pass in between."""
+    L = layer()
+    x, wg, b, W, wn = operands()
+    L.forward(x, wg, b, W, train=True)
+    idx, w = recorder.args("moe_route")[7:9]
+    assert L.idx is idx and L.w is w
+    L.forward_few(x, wg, b, W)
+    few = recorder.args("moe_layer_few")[11:13]
+    assert L.idx is few[0] and L.w is few[1] and few[0] is not idx and few[1] is not w
+    L.backward(x, W)
+    assert recorder.args("moe_combine_backward")[3] is w
+    L.forward_normed(x, wn, 1e-6, wg, b, W)
+    assert L.idx is idx and L.w is w and recorder.args("moe_route")[7] is idx
