@@ -407,6 +407,7 @@ class MoELayer:
         self.n_groups, self.topk_groups, self.route_scale = n_groups, topk_groups, route_scale
         self.dispatch = dispatch
         self._side = None        # stream of the overlapped activation quantisation
+        self._counted = False    # the last pass left its experts' loads in offsets
         rows = T * topk + T
         dev = dict(device=device)
         self._selection, self._few_selection = (
@@ -472,6 +473,7 @@ class MoELayer:
             moe_permute(self.idx, self.E, self.offsets, self.pos, self.row_token, self.ws,
                         stream=stream)
             aq, as_, src = self.xq, self.xs, self.row_token
+        self._counted = True
         mark("permute")
         up = grouped_gemm_fp8_up_e8m0 if self.pow2 else grouped_gemm_fp8_up
         down = grouped_gemm_fp8_down_e8m0 if self.pow2 else grouped_gemm_fp8_down
@@ -517,11 +519,12 @@ class MoELayer:
         combined.  ``residual`` [T, d] is added to the output when given.
         ``forward`` ranks FP32 scores: within 1e-6 of a tie the two may choose
         different experts for a token.  Of what the other passes leave, only
-        ``out`` is written."""
+        ``out`` is written; the experts' loads are not counted."""
         few = moe_layer_few_pow2 if self.pow2 else moe_layer_few
         self.idx, self.w = self._few_selection
         few(x, wg, bias, self.n_groups, self.topk_groups, self.k, self.route_scale, weights.w13q, weights.w13s,
             weights.w2q, weights.w2s, self.idx, self.w, self.out, self.few_ws, residual=residual, stream=stream)
+        self._counted = False
         return self.out
 
     def _train_buffers(self):
@@ -624,6 +627,9 @@ class MoELayer:
         return self.grad_norm
 
     def update_bias(self, bias, gamma, stream=None):
-        """After forward(): one step of the balancing controller on ``bias``
-        [E] from this batch's expert loads (training-time only)."""
+        """After ``forward`` or ``forward_normed``: one step of the balancing
+        controller on ``bias`` [E] from this batch's expert loads
+        (training-time only).  Refused where the last pass counted none."""
+        if not self._counted:
+            raise RuntimeError("update_bias follows forward or forward_normed: the last pass counted no expert loads")
         moe_bias_update(self.offsets, bias, gamma, stream)

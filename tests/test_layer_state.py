@@ -55,3 +55,19 @@ def test_few_tokens_leave_the_training_selection(recorder):
     assert recorder.args("moe_combine_backward")[3] is w
     L.forward_normed(x, wn, 1e-6, wg, b, W)
     assert L.idx is idx and L.w is w and recorder.args("moe_route")[7] is idx
+
+
+def test_bias_step_needs_the_loads_of_the_last_pass(recorder):
+    """The loads are those that forward and forward_normed leave; there are none before them, and after a few-token
+    pass they would be an older batch's."""
+    L = layer()
+    x, wg, b, W, wn = operands()
+    with pytest.raises(RuntimeError, match="counted no expert loads"):
+        L.update_bias(b, 1e-3)
+    for forward in (lambda: L.forward(x, wg, b, W), lambda: L.forward_normed(x, wn, 1e-6, wg, b, W)):
+        forward()
+        L.update_bias(b, 1e-3)
+        assert recorder.args("moe_bias_update")[:2] == (L.offsets, b)
+        L.forward_few(x, wg, b, W)
+        with pytest.raises(RuntimeError, match="counted no expert loads"):
+            L.update_bias(b, 1e-3)
