@@ -408,6 +408,7 @@ class MoELayer:
         self.dispatch = dispatch
         self._side = None        # stream of the overlapped activation quantisation
         self._counted = False    # the last pass left its experts' loads in offsets
+        self._cached = None      # the method whose activations backward goes through
         rows = T * topk + T
         dev = dict(device=device)
         self._selection, self._few_selection = (
@@ -437,6 +438,7 @@ class MoELayer:
         ``backward`` (FP32-scale method only)."""
         mark = mark or (lambda name: None)
         self.idx, self.w = self._selection
+        self._cached = None
         quant = fp8_quant_1x128_pow2 if self.pow2 else fp8_quant_1x128
         if self.T >= OVERLAP_QUANT_T:
             # the activation quantisation does not depend on the routing: on a
@@ -460,11 +462,12 @@ class MoELayer:
             mark("route")
             quant(x, self.xq, self.xs, stream)
             mark("quant")
-        return self._experts(weights, stream, mark, train)
+        return self._experts(weights, stream, mark, "forward" if train else None)
 
     def _experts(self, weights, stream, mark, train, residual=None):
         """The layer after the router and the quantiser: permute, both expert
-        GEMMs, combine (with ``residual`` added)."""
+        GEMMs, combine (with ``residual`` added).  ``train`` is the calling
+        method's name where the activations are cached for its backward."""
         if self.dispatch:
             moe_permute(self.idx, self.E, self.offsets, self.pos, self.row_token, self.ws,
                         self.xq, self.xs, self.xq_perm, self.xs_perm, stream)
@@ -490,6 +493,7 @@ class MoELayer:
         mark("gemm_down")
         moe_combine(self.y, self.pos, self.w, self.T * self.k, self.out, stream, residual=residual)
         mark("combine")
+        self._cached = train
         return self.out
 
     def forward_normed(self, x, norm_weight, eps, wg, bias, weights, residual=None, stream=None, mark=None,
@@ -500,6 +504,7 @@ class MoELayer:
         None), norm_weight [d] BF16.  Returns out; ``self.hsum`` holds s."""
         mark = mark or (lambda name: None)
         self.idx, self.w = self._selection
+        self._cached = None
         if getattr(self, "hsum", None) is None:
             self.hsum, self.xn = torch.empty_like(self.out), torch.empty_like(self.out)
             self.rstd = torch.empty(self.T, dtype=torch.float32, device=self.out.device)
@@ -510,7 +515,7 @@ class MoELayer:
         moe_route(self.xn, wg, bias, self.n_groups, self.topk_groups, self.k, self.route_scale, self.idx, self.w,
                   stream, workspace=self.route_ws)
         mark("route")
-        return self._experts(weights, stream, mark, train, residual=self.hsum)
+        return self._experts(weights, stream, mark, "forward_normed" if train else None, residual=self.hsum)
 
     def forward_few(self, x, wg, bias, weights, residual=None, stream=None):
         """The layer on x [T, d] for T <= 16 by moe_layer_few: the same
@@ -558,12 +563,16 @@ class MoELayer:
         self.dw2 = torch.empty(G, d, f, dtype=torch.float32, **dev)
 
     def backward(self, dout, weights_t, stream=None, mark=None):
-        """Backward of the last ``forward(..., train=True)`` for the output
+        """Backward of the last pass, a ``forward(..., train=True)`` (any number
+        of ``forward_few`` may come between the two), for the output
         gradient dout [T, d] BF16, with ``weights_t = weights.transposed()``.
         Returns (dX [T, d] BF16, dW13 [E+1, 2f, d] FP32, dW2 [E+1, d, f] FP32,
         gate gradients [T, k] FP32).  Every backward quantisation uses
         power-of-two scales; Dgrad runs on grouped_gemm_fp8_down with the
-        transposed weights, Wgrad on the K-major 128x1 operands."""
+        transposed weights, Wgrad on the K-major 128x1 operands.  After
+        ``forward_normed`` dX is the gradient of the normed rows."""
+        if self._cached is None:
+            raise RuntimeError("backward follows a forward with train=True: the last pass cached no activations")
         mark = mark or (lambda name: None)
         T, k, d, f, E = self.T, self.k, self.d, self.f, self.E
         rows, G = T * k + T, E + 1
@@ -592,10 +601,13 @@ class MoELayer:
         return self.dx, self.dw13, self.dw2, self.dw
 
     def backward_normed(self, dout, norm_weight, weights_t, stream=None, mark=None):
-        """Backward of the last ``forward_normed(..., train=True)``.  Returns
+        """Backward of the last pass, a ``forward_normed(..., train=True)``.  Returns
         (ds [T, d] BF16, the gradient of x and of the residual alike, dweight
         [d] FP32 of the norm, dW13, dW2, gate gradients); as in ``backward``,
         the gates' gradients are not propagated into the router."""
+        if self._cached != "forward_normed":
+            raise RuntimeError("backward_normed follows a forward_normed with train=True, not "
+                               + (self._cached or "a pass that cached no activations"))
         mark = mark or (lambda name: None)
         dx, dw13, dw2, dgate = self.backward(dout, weights_t, stream, mark)
         if getattr(self, "dnorm", None) is None:

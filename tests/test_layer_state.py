@@ -71,3 +71,38 @@ def test_bias_step_needs_the_loads_of_the_last_pass(recorder):
         L.forward_few(x, wg, b, W)
         with pytest.raises(RuntimeError, match="counted no expert loads"):
             L.update_bias(b, 1e-3)
+
+
+def test_backward_needs_the_activations_of_the_last_pass(recorder):
+    """backward goes through one batch: not through a training forward's caches and a later pass' rows, nor through
+    the sums and norms of an earlier forward_normed."""
+    L = layer()
+    x, wg, b, W, wn = operands()
+
+    def normed(train):
+        L.forward_normed(x, wn, 1e-6, wg, b, W, train=train)
+
+    def refused(*methods):
+        n = len(recorder.calls)
+        for m in methods:
+            with pytest.raises(RuntimeError, match=m + " follows"):
+                L.backward(x, W) if m == "backward" else L.backward_normed(x, wn, W)
+        assert len(recorder.calls) == n
+
+    refused("backward", "backward_normed")
+    L.forward(x, wg, b, W, train=True)
+    L.backward(x, W)
+    refused("backward_normed")
+    normed(True)
+    L.backward_normed(x, wn, W)
+    L.backward_normed(x, wn, W)
+    L.backward(x, W)
+    L.forward_few(x, wg, b, W)
+    L.backward_normed(x, wn, W)
+    L.forward(x, wg, b, W, train=True)      # hsum and rstd are an older batch's
+    refused("backward_normed")
+    L.backward(x, W)
+    for untrained in (lambda: L.forward(x, wg, b, W), lambda: normed(False)):
+        normed(True)
+        untrained()
+        refused("backward", "backward_normed")
