@@ -625,6 +625,8 @@ class MoELayer:
         list of further FP32 or BF16 gradients) in place so that their joint
         L2 norm is at most ``max_norm``.  Returns the norm before, [1] FP32 on
         the device; nothing waits on the host."""
+        if getattr(self, "dw13", None) is None or getattr(self, "dw2", None) is None:
+            raise RuntimeError("clip_grads follows a backward: there are no weight gradients yet")
         grads = [self.dw13, self.dw2, *extra]
         if getattr(self, "grad_norm", None) is None:
             self.grad_norm = torch.empty(1, dtype=torch.float32, device=self.out.device)

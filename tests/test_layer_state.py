@@ -106,3 +106,18 @@ def test_backward_needs_the_activations_of_the_last_pass(recorder):
         normed(True)
         untrained()
         refused("backward", "backward_normed")
+
+
+def test_clipping_needs_gradients(recorder):
+    L = layer()
+    x, wg, b, W, _ = operands()
+    L.forward(x, wg, b, W)
+    with pytest.raises(RuntimeError, match="clip_grads follows a backward"):
+        L.clip_grads(1.0)
+    assert not any(n.startswith("moe_grad") for n, _, _ in recorder.calls)
+    L.forward(x, wg, b, W, train=True)
+    L.backward(x, W)
+    extra = torch.zeros(3)
+    L.clip_grads(1.0, extra=(t for t in [extra]))
+    for name in ("moe_grad_norm", "moe_grad_scale"):
+        assert [id(t) for t in recorder.args(name)[0]] == [id(t) for t in (L.dw13, L.dw2, extra)]
