@@ -396,7 +396,11 @@ class MoELayer:
     ``idx`` and ``w`` are the selection and gates of the last pass that was
     called (captured, in a graph): ``forward`` and ``forward_normed`` share
     one pair of arrays, ``forward_few`` has another, so that a ``backward``
-    may follow it."""
+    may follow it.
+
+    Buffers that only some methods need are made by the first call that does,
+    on its stream: memory that another stream has let go may still be in use
+    there."""
 
     def __init__(self, T, d, E, n_groups, topk_groups, topk, f, route_scale=2.5, device="cuda",
                  dispatch=False, scales="fp32"):
@@ -483,7 +487,9 @@ class MoELayer:
         if train:
             if self.pow2:
                 raise ValueError("the training forward runs the FP32-scale method")
-            self._train_buffers()
+            if getattr(self, "gu", None) is None:
+                with torch.cuda.stream(stream):
+                    self._train_buffers()
             grouped_gemm_fp8_up_train(aq, as_, src, self.offsets, weights.w13q, weights.w13s, self.h,
                                       self.hs, self.gu, self.gus, stream)
         else:
@@ -506,8 +512,9 @@ class MoELayer:
         self.idx, self.w = self._selection
         self._cached = None
         if getattr(self, "hsum", None) is None:
-            self.hsum, self.xn = torch.empty_like(self.out), torch.empty_like(self.out)
-            self.rstd = torch.empty(self.T, dtype=torch.float32, device=self.out.device)
+            with torch.cuda.stream(stream):
+                self.hsum, self.xn = torch.empty_like(self.out), torch.empty_like(self.out)
+                self.rstd = torch.empty(self.T, dtype=torch.float32, device=self.out.device)
         norm = moe_rmsnorm_quant_pow2 if self.pow2 else moe_rmsnorm_quant
         norm(x, norm_weight, eps, self.xn, residual=residual, sum_out=self.hsum, q=self.xq, scale=self.xs,
              rstd=self.rstd, stream=stream)
@@ -533,8 +540,6 @@ class MoELayer:
         return self.out
 
     def _train_buffers(self):
-        if getattr(self, "gu", None) is not None:
-            return
         T, k, d, f, E = self.T, self.k, self.d, self.f, self.E
         rows, G = T * k + T, E + 1
         dev = dict(device=self.h.device)
@@ -611,10 +616,11 @@ class MoELayer:
         mark = mark or (lambda name: None)
         dx, dw13, dw2, dgate = self.backward(dout, weights_t, stream, mark)
         if getattr(self, "dnorm", None) is None:
-            self.dnorm = torch.empty(self.d, dtype=torch.float32, device=self.out.device)
-            self.dsum = torch.empty_like(self.out)
             n = moe_rmsnorm_backward_workspace_bytes(self.T, self.d)
-            self.norm_ws = torch.empty(max(16, n), dtype=torch.uint8, device=self.out.device)
+            with torch.cuda.stream(stream):
+                self.dnorm = torch.empty(self.d, dtype=torch.float32, device=self.out.device)
+                self.dsum = torch.empty_like(self.out)
+                self.norm_ws = torch.empty(max(16, n), dtype=torch.uint8, device=self.out.device)
         moe_rmsnorm_backward(dx, self.hsum, norm_weight, self.rstd, self.dsum, self.dnorm, self.norm_ws, dres=dout,
                              stream=stream)
         mark("norm_bwd")
@@ -629,13 +635,15 @@ class MoELayer:
             raise RuntimeError("clip_grads follows a backward: there are no weight gradients yet")
         grads = [self.dw13, self.dw2, *extra]
         if getattr(self, "grad_norm", None) is None:
-            self.grad_norm = torch.empty(1, dtype=torch.float32, device=self.out.device)
-            self.grad_coef = torch.empty_like(self.grad_norm)
+            with torch.cuda.stream(stream):
+                self.grad_norm = torch.empty(1, dtype=torch.float32, device=self.out.device)
+                self.grad_coef = torch.empty_like(self.grad_norm)
             self.grad_ws = {}
         # one workspace per size, kept: a captured graph may hold any of them
         n = moe_grad_norm_workspace_bytes(len(grads))
         if n not in self.grad_ws:
-            self.grad_ws[n] = torch.empty(n, dtype=torch.uint8, device=self.out.device)
+            with torch.cuda.stream(stream):
+                self.grad_ws[n] = torch.empty(n, dtype=torch.uint8, device=self.out.device)
         moe_grad_norm(grads, max_norm, self.grad_norm, self.grad_coef, self.grad_ws[n], stream)
         moe_grad_scale(grads, self.grad_coef, stream=stream)
         return self.grad_norm

@@ -183,3 +183,31 @@ def test_backward_after_a_decode_step():
     assert not torch.equal(L.idx, idx) and torch.equal(L.forward_few(x.flip(0).contiguous(), wg, b, W), other)
     L.forward_normed(x, wn, EPS, wg, b, W, residual=res)
     assert torch.equal(L.idx, idx) and torch.equal(L.w, w)
+
+
+def test_first_calls_on_a_busy_devices_other_stream():
+    """A training step on a stream of its own while the current stream still works on memory that it has let go: the
+    buffers that the step makes are none of that memory."""
+    T = 200
+    cfg, x, wg, b, res, wn, W, L = setup(T)
+    Wt = W.transposed()
+    dout = torch.randn(T, cfg.d, generator=torch.Generator(device=DEV).manual_seed(2), device=DEV).to(BF16)
+
+    def step(L, stream=None):
+        out = L.forward_normed(x, wn, EPS, wg, b, W, residual=res, train=True, stream=stream)
+        return [out, *L.backward_normed(dout, wn, Wt, stream=stream), L.clip_grads(1.0, extra=[L.dnorm], stream=stream)]
+
+    want = [t.clone() for t in step(L)]
+    L2 = moe.MoELayer(T, cfg.d, cfg.E, cfg.G, cfg.M, cfg.k, cfg.f, cfg.route_scale)
+    sizes = [t.numel() * t.element_size() for t in vars(L).values() if isinstance(t, torch.Tensor)]
+    big, side = torch.zeros(1 << 26, device=DEV), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(100):
+        big.add_(1)
+    for n in sizes:
+        let_go = [torch.full((n,), 0xFF, dtype=torch.uint8, device=DEV) for _ in range(4)]
+        del let_go
+    got = step(L2, side)
+    side.synchronize()
+    for g, w in zip(got, want):
+        assert torch.equal(g, w)

@@ -121,3 +121,34 @@ def test_clipping_needs_gradients(recorder):
     L.clip_grads(1.0, extra=(t for t in [extra]))
     for name in ("moe_grad_norm", "moe_grad_scale"):
         assert [id(t) for t in recorder.args(name)[0]] == [id(t) for t in (L.dw13, L.dw2, extra)]
+
+
+def test_buffers_made_on_first_use_are_the_streams(recorder, monkeypatch):
+    """Whatever a call allocates, it allocates on the stream that it was given."""
+    L = layer()
+    x, wg, b, W, wn = operands()
+    current, made = [None], []
+
+    class On:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            current.append(self.stream)
+
+        def __exit__(self, *exc):
+            current.pop()
+
+    monkeypatch.setattr(torch.cuda, "stream", On)
+    for name in ("empty", "empty_like", "ones"):
+        make = getattr(torch, name)
+        monkeypatch.setattr(torch, name, lambda *a, _make=make, **kw: (made.append(current[-1]), _make(*a, **kw))[1])
+    s = object()
+    for call, some in ((lambda: L.forward_normed(x, wn, 1e-6, wg, b, W, stream=s), True),
+                       (lambda: L.forward_normed(x, wn, 1e-6, wg, b, W, stream=s, train=True), True),
+                       (lambda: L.backward_normed(x, wn, W, stream=s), True), (lambda: L.clip_grads(1.0, stream=s), True),
+                       (lambda: L.clip_grads(1.0, extra=[torch.zeros(1)] * 70, stream=s), True),
+                       (lambda: L.forward_few(x, wg, b, W, stream=s), False), (lambda: L.clip_grads(2.0, stream=s), False)):
+        made.clear()
+        call()
+        assert bool(made) == some and all(m is s for m in made)
