@@ -360,3 +360,18 @@ def test_codes_of_a_tile_with_an_infinity(form, T, f):
     inf = torch.tensor(float("inf"), device=DEV)
     want = c.w2[8, :, one].view(torch.float8_e4m3fn).float() * -inf     # NaN for a weight of zero
     assert want.isinf().any() and torch.equal(o["out"].float().nan_to_num(nan=1.0), want.nan_to_num(nan=1.0).expand(T, 256))
+
+
+# K blocks per wave that the shapes above leave out, four (d 3200 to 4096) and six (d 5248 to 6144), in whole and in
+# part; 16 whole columns to a workgroup of the second product (d 4096), its h staged and not; 16 tokens at the widths
+# of one and two fragments
+@pytest.mark.parametrize("form", sorted(FORMS))
+@pytest.mark.parametrize("shape", [(16, 4096, 8, 2, 2, 4, 256), (3, 4096, 8, 2, 2, 4, 128), (16, 4096, 8, 2, 2, 4, 512),
+                                   (5, 3328, 8, 2, 2, 4, 128), (4, 6144, 8, 2, 2, 4, 128), (4, 5376, 8, 2, 2, 4, 128),
+                                   (16, 7168, 16, 4, 2, 4, 256), (16, 7168, 16, 4, 2, 8, 384), (16, 8192, 4, 2, 1, 2, 128)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_wide_layers(form, shape):
+    c = Case(*shape, form=form, seed=sum(shape))
+    for res, bias in ((c.res, True), (None, False)):
+        rel = c.check(c.run(res, bias), res, bias)
+        log(f"{form} {shape}: rel {rel:.1e}")

@@ -169,3 +169,40 @@ def test_refusals():
     with pytest.raises(moe.MoEError, match="in part"):
         a = torch.zeros(20, device=DEV)
         moe.moe_grad_scale([a[:10]], coef, [a[4:14]])
+
+
+def test_a_list_past_the_caches():
+    """More than 256 MB of both types, tensors that start between 16-byte boundaries among them: the norm in 64 bits,
+    the scaling out of place and in place."""
+    g = torch.Generator(device=DEV).manual_seed(5)
+    ts = [torch.randn(n + 3, generator=g, device=DEV)[o:o + n].to(dt) for n, o, dt in
+          ((60_000_001, 0, FP32), (9, 1, FP32), (30_000_000, 0, BF16))]
+    whole = torch.randn(10_000_008, generator=g, device=DEV)
+    ts.append(whole[1:10_000_002])
+    assert sum(t.numel() * t.element_size() for t in ts) > 1 << 28 and ts[-1].data_ptr() % 16 == 4
+    n = float(torch.stack([t.double().square().sum() for t in ts]).sum().sqrt())
+    norm, coef = norm_of(ts, 2.5)
+    # one rounding to FP32 each (half a step), and 2^-40 for the order of 64-bit sums
+    assert abs(float(norm) - n) <= (2.0 ** -24 + 2.0 ** -40) * n
+    assert abs(float(coef) - 2.5 / n) <= (2.0 ** -24 + 2.0 ** -40) * 2.5 / n
+    want = [(t.float() * coef).to(t.dtype) for t in ts]
+    ends = whole[0].clone(), whole[10_000_002:].clone()
+    outs = [torch.full_like(t, 7) for t in ts]
+    moe.moe_grad_scale(ts, coef, outs)
+    moe.moe_grad_scale(ts, coef)
+    for t, o, w in zip(ts, outs, want):
+        assert torch.equal(o, w) and torch.equal(t, w)
+    assert torch.equal(whole[0], ends[0]) and torch.equal(whole[10_000_002:], ends[1])
+
+
+def test_a_factor_of_one_writes_nothing_in_place():
+    """Shown on NaNs whose bits a product with 1 would change: BF16 results have one NaN, FP32 products quiet ones."""
+    b = torch.tensor([0x7FA5, -1, 0x3F80, 0x7FFF] * 3000, dtype=torch.int16, device=DEV)
+    f = torch.tensor([0x7FA00001, 0x3F800000, 0x7F800001] * 3001, dtype=torch.int32, device=DEV)
+    ts = [b.clone().view(BF16), f.clone().view(FP32)]
+    one = torch.ones(1, device=DEV)
+    moe.moe_grad_scale(ts, one)
+    assert torch.equal(ts[0].view(torch.int16), b) and torch.equal(ts[1].view(torch.int32), f)
+    outs = [torch.empty_like(t) for t in ts]
+    moe.moe_grad_scale(ts, one, outs)
+    assert not torch.equal(outs[0].view(torch.int16), b)

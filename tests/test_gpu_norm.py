@@ -2,6 +2,9 @@
 against the float64 oracle: every forward output bit for bit, the backward
 within its FP32 rounding errors."""
 
+import os
+import re
+
 import numpy as np
 import pytest
 import torch
@@ -277,3 +280,16 @@ def test_large_batches_are_their_parts(form, T, d):
     # both sides: rows one after another in FP32 (at most T over the partial sums, four waves joined), two roundings a term
     per = -(-T // (ws.numel() // (4 * d)))
     assert ((dw.double() - total).abs() <= 2.0 ** -24 * (2 * (per + 4 + 3) * 1.001 * mag.double() + 2 * total.abs() + mag)).all()
+
+
+# every split of a row whose data goes past the caches, forward and backward: a wave with one chunk a lane and with
+# four, a workgroup of up to 512 threads and beyond
+@pytest.mark.parametrize("T,d", [(44000, 512), (20000, 1152), (12500, 2048), (3200, 7168), (1400, 16384)])
+@pytest.mark.parametrize("form", sorted(FORMS))
+def test_past_the_caches(form, T, d):
+    src = open(os.path.join(os.path.dirname(moe.__file__), "csrc", "norm.hip")).read()
+    forward, backward = (int(re.search(rf"{name} = size_t\((\d+)\) << 20;", src)[1]) << 20
+                         for name in ("kForwardCached", "kBackwardCached"))
+    assert 9 * T * d > forward and 8 * T * d > backward
+    assert 9 * 1000 * d < forward     # the parts' go through them
+    test_large_batches_are_their_parts(form, T, d)
