@@ -25,11 +25,12 @@
 //     never reach memory.
 //
 // Bound by HBM reads from T = 4 on: at d 7168, f 2048, E 256, k 8 a call takes
-// 212 us at T = 4 (1.39 GB, 6.6 TB/s) and 658 at T = 16 (4.54 GB, 6.9 TB/s); a
-// plain read of the card's memory makes 7.05.  At T = 1 it takes 75 us for 400
-// MB, 57 at that rate: the router's kernel is 5.4 of them, the rest of the
-// difference the selection where the first weights do not cover it and the
-// starts and ends of the two products (44 and 25 us).  Where a batch is small
+// 215 to 233 us at T = 4 (29 to 33 active experts, 1.28 to 1.45 GB, 6.1 to 6.4
+// TB/s) and 637 to 714 at T = 16 (89 to 105 of them, 3.9 to 4.6 GB, 6.3 to 6.5
+// TB/s); a plain read of the card's memory makes 7.05.  At T = 1 it takes 75 to
+// 79 us for 396 MB, 56 at that rate: the router's kernel is 5.8 of them, the rest
+// of the difference the selection where the first weights do not cover it and the
+// starts and ends of the two products (46 and 26 us).  Where a batch is small
 // the kernels' code counts: its first fetch takes some 0.1 us per 128 bytes, so
 // what runs once is kept short (loops rolled, divisions on the host).
 #include <algorithm>
@@ -736,9 +737,11 @@ __global__ __launch_bounds__(256) void few_quant_kernel(const FewArgs p) {
 // in units of 4 (missing rows of the last fragment read as zeros), or, of narrow
 // layers, 16 whose steps several workgroups share (few_splits).
 // The steps (active expert, K block; 2 C KB of weights) are dealt to the waves
-// in turn, with RING of them in flight per wave: 64 KB per CU, beyond which rings
-// of 3 to 7 at V3 changed nothing.  A step's h serves all fragments, and one
-// barrier joins the waves' sums at the end.
+// in turn, with RING of them in flight per wave: 64 KB per CU with two whole
+// fragments, where rings of 3 to 7 changed nothing at V3; 32 KB (48 with a ring
+// of 3) with one, less where the fragment is part empty (d 2560: 8 or 12 of its
+// 16 rows, 73 us at T = 16, 64 experts, f 2048, for 43 of bytes).  A step's h
+// serves all fragments, and one barrier joins the waves' sums at the end.
 //
 // STAGE: the workgroup quantises h itself, into LDS, beneath its first weight
 // loads; otherwise the tiles come from few_quant_kernel through memory, and

@@ -18,7 +18,10 @@
 //
 // Bound by HBM: 5.8 GB of FP32 gradients are squared in 0.85 ms (6.8 TB/s) and
 // scaled in 2.1 ms (11.6 GB read and written, 5.5 TB/s; a large copy makes
-// 4.8).  A few megabytes are bound by the three launches and the host's work
+// 4.8), other lists' passes in between.  The same list over and over is scaled in
+// 1.84 to 1.91 ms in place and 1.81 to 1.89 out of place, norm and scaling
+// together in 2.75 to 2.82 and 2.71 to 2.79; in place with a factor of 1 the
+// scaling takes 0.07 ms, in which its workgroups find that out.  A few megabytes are bound by the three launches and the host's work
 // per tensor: 13 MB take 5 + 2 + 5 us on the device.
 #include <algorithm>
 

@@ -6,9 +6,11 @@
 //   rstd = fl32(1 / sqrt(sum h^2 / d + eps))   sum, quotient and root in FP64
 //   y    = bf16(fl32(fl32(h * rstd) * w))
 //   s, q = the 1x128 tiles of y, as fp8_quant_1x128 makes them
-// A BF16 square is exact in FP64 and the sum's error is below 2^-50 relative,
-// so rstd, and with it every output, does not depend on how a row is split
-// over threads (up to a sum within that distance of an FP32 rounding border).
+// A BF16 square is exact in FP64, and no term goes through more than 38
+// additions (16 of its thread, 6 over the lanes, 16 over the waves), so the
+// sum's error is below 38 x 2^-53 < 2^-47 relative: rstd, and with it every
+// output, does not depend on how a row is split over threads (up to a sum within
+// that distance of an FP32 rounding border).
 // The FP64 work, one conversion and one multiply-add per element, hides behind
 // the memory traffic: 9 bytes per element with a residual.
 //
@@ -22,9 +24,10 @@
 // 16-byte chunks in registers between the sum and the second use, so every
 // operand is read once.  At 16384 x 7168 the forward with a residual and all
 // outputs moves 1.06 GB in 182 us (5.8 TB/s), the backward with dres 0.94 GB in
-// 159 us (5.9 TB/s) and 5 us for dw; a large copy makes 4.8 TB/s, a plain read
-// 7.05.  At tens of rows a call is its launch: 3 us for 37 x 384, 5 for 64 x
-// 7168, under 7 to 8 us of the host's.
+// 161 us (5.8 TB/s) and 5 us for dw; a large copy makes 4.8 TB/s, a plain read
+// 7.05.  At tens of rows a call waits on the host (7 to 8 us); the kernel alone
+// takes 3.7 us for 37 x 384 and 6.1 for 64 x 7168 (0.9 us of bytes, on 64 of
+// the 256 CUs), launched from a graph 3.1 and 5.3.
 //
 // Two chunks per thread for wide rows: one chunk (896 threads for a 7168 row)
 // took 214 us, four (256 threads) 224.  The next row's loads ahead of the
@@ -382,8 +385,13 @@ hipError_t launch_rmsnorm_quant(const uint16_t* x, const uint16_t* res, const ui
   return hipGetLastError();
 }
 
-// Workgroups of the backward's first kernel: enough to fill the chip, few
-// enough that their partial rows stay a small part of the traffic.
+// Workgroups of the backward's first kernel: enough to fill the chip.  Each
+// writes a row of dw partial sums that the second kernel reads, 4096 d bytes of
+// traffic with 512 of them.  Of rows over 2048 wide that is an eighth of the
+// operands' 8 T d at T = 4096 (49 us, 4.8 TB/s of operands at d 7168), half of
+// them at 1024 (18 us, 3.2) and as much again up to 512, where every row has its
+// own (15 us, 2.0).  At 16384 rows 256 and 1024 workgroups took 189 and 170 us against 164;
+// fewer ones for fewer rows have not been measured.
 int rmsnorm_backward_groups(int T, int d) {
   const int rows = d <= kBackwardWaveD ? NORM_THREADS / 64 : 1;
   return (int)std::min((long)512, ((long)T + rows - 1) / rows);
