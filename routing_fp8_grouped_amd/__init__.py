@@ -50,6 +50,10 @@ def _dev(t, dtype, name):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _capturing(t):
+    return t.is_cuda and torch.cuda.is_current_stream_capturing()
+
+
 def moe_route_workspace_bytes(T, E):
     return int(_lib.load().moe_route_workspace_bytes(T, E))
 
@@ -396,7 +400,9 @@ class MoELayer:
     ``idx`` and ``w`` are the selection and gates of the last pass that was
     called (captured, in a graph): ``forward`` and ``forward_normed`` share
     one pair of arrays, ``forward_few`` has another, so that a ``backward``
-    may follow it.
+    may follow it.  Calls that need what a certain pass leaves refuse where the
+    last one was another, unless such a pass has been captured: whether its
+    graph was replayed since is not known here.
 
     Buffers that only some methods need are made by the first call that does,
     on its stream: memory that another stream has let go may still be in use
@@ -411,8 +417,10 @@ class MoELayer:
         self.n_groups, self.topk_groups, self.route_scale = n_groups, topk_groups, route_scale
         self.dispatch = dispatch
         self._side = None        # stream of the overlapped activation quantisation
-        self._counted = False    # the last pass left its experts' loads in offsets
-        self._cached = None      # the method whose activations backward goes through
+        # What the last pass left for later calls: "loads" of its experts, and
+        # its method's name with train; and what captured passes leave whenever
+        # their graph is replayed, which is not seen here.
+        self._left, self._replayed = set(), set()
         rows = T * topk + T
         dev = dict(device=device)
         self._selection, self._few_selection = (
@@ -442,7 +450,7 @@ class MoELayer:
         ``backward`` (FP32-scale method only)."""
         mark = mark or (lambda name: None)
         self.idx, self.w = self._selection
-        self._cached = None
+        self._left = set()
         quant = fp8_quant_1x128_pow2 if self.pow2 else fp8_quant_1x128
         if self.T >= OVERLAP_QUANT_T:
             # the activation quantisation does not depend on the routing: on a
@@ -480,7 +488,6 @@ class MoELayer:
             moe_permute(self.idx, self.E, self.offsets, self.pos, self.row_token, self.ws,
                         stream=stream)
             aq, as_, src = self.xq, self.xs, self.row_token
-        self._counted = True
         mark("permute")
         up = grouped_gemm_fp8_up_e8m0 if self.pow2 else grouped_gemm_fp8_up
         down = grouped_gemm_fp8_down_e8m0 if self.pow2 else grouped_gemm_fp8_down
@@ -499,7 +506,9 @@ class MoELayer:
         mark("gemm_down")
         moe_combine(self.y, self.pos, self.w, self.T * self.k, self.out, stream, residual=residual)
         mark("combine")
-        self._cached = train
+        self._left = {"loads", train} - {None}
+        if _capturing(self.out):
+            self._replayed |= self._left
         return self.out
 
     def forward_normed(self, x, norm_weight, eps, wg, bias, weights, residual=None, stream=None, mark=None,
@@ -510,7 +519,7 @@ class MoELayer:
         None), norm_weight [d] BF16.  Returns out; ``self.hsum`` holds s."""
         mark = mark or (lambda name: None)
         self.idx, self.w = self._selection
-        self._cached = None
+        self._left = set()
         if getattr(self, "hsum", None) is None:
             with torch.cuda.stream(stream):
                 self.hsum, self.xn = torch.empty_like(self.out), torch.empty_like(self.out)
@@ -536,7 +545,7 @@ class MoELayer:
         self.idx, self.w = self._few_selection
         few(x, wg, bias, self.n_groups, self.topk_groups, self.k, self.route_scale, weights.w13q, weights.w13s,
             weights.w2q, weights.w2s, self.idx, self.w, self.out, self.few_ws, residual=residual, stream=stream)
-        self._counted = False
+        self._left = self._left - {"loads"}
         return self.out
 
     def _train_buffers(self):
@@ -576,7 +585,7 @@ class MoELayer:
         power-of-two scales; Dgrad runs on grouped_gemm_fp8_down with the
         transposed weights, Wgrad on the K-major 128x1 operands.  After
         ``forward_normed`` dX is the gradient of the normed rows."""
-        if self._cached is None:
+        if not {"forward", "forward_normed"} & (self._left | self._replayed):
             raise RuntimeError("backward follows a forward with train=True: the last pass cached no activations")
         mark = mark or (lambda name: None)
         T, k, d, f, E = self.T, self.k, self.d, self.f, self.E
@@ -610,9 +619,8 @@ class MoELayer:
         (ds [T, d] BF16, the gradient of x and of the residual alike, dweight
         [d] FP32 of the norm, dW13, dW2, gate gradients); as in ``backward``,
         the gates' gradients are not propagated into the router."""
-        if self._cached != "forward_normed":
-            raise RuntimeError("backward_normed follows a forward_normed with train=True, not "
-                               + (self._cached or "a pass that cached no activations"))
+        if "forward_normed" not in self._left | self._replayed:
+            raise RuntimeError("backward_normed follows a forward_normed with train=True: the last pass was none")
         mark = mark or (lambda name: None)
         dx, dw13, dw2, dgate = self.backward(dout, weights_t, stream, mark)
         if getattr(self, "dnorm", None) is None:
@@ -652,6 +660,6 @@ class MoELayer:
         """After ``forward`` or ``forward_normed``: one step of the balancing
         controller on ``bias`` [E] from this batch's expert loads
         (training-time only).  Refused where the last pass counted none."""
-        if not self._counted:
+        if "loads" not in self._left | self._replayed:
             raise RuntimeError("update_bias follows forward or forward_normed: the last pass counted no expert loads")
         moe_bias_update(self.offsets, bias, gamma, stream)

@@ -211,3 +211,27 @@ def test_first_calls_on_a_busy_devices_other_stream():
     side.synchronize()
     for g, w in zip(got, want):
         assert torch.equal(g, w)
+
+
+def test_backward_after_a_replayed_forward():
+    """The training forward in a graph, other passes of the layer between its replays, the backward eager."""
+    T = 96
+    cfg, x, wg, b, res, wn, W, L = setup(T)
+    Wt = W.transposed()
+    dout = torch.randn(T, cfg.d, generator=torch.Generator(device=DEV).manual_seed(3), device=DEV).to(BF16)
+    other = x.flip(0).contiguous()
+    L.forward_normed(x, wn, EPS, wg, b, W, residual=res, train=True)
+    want = [t.clone() for t in L.backward_normed(dout, wn, Wt)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        L.forward_normed(x, wn, EPS, wg, b, W, residual=res, train=True)
+    bias = b.clone()
+    for _ in range(3):
+        L.forward(other, wg, b, W)
+        g.replay()
+        for got, ref in zip(L.backward_normed(dout, wn, Wt), want):
+            assert torch.equal(got, ref)
+        L.update_bias(bias, 1e-3)
+    torch.cuda.synchronize()

@@ -152,3 +152,25 @@ def test_buffers_made_on_first_use_are_the_streams(recorder, monkeypatch):
         made.clear()
         call()
         assert bool(made) == some and all(m is s for m in made)
+
+
+def test_replays_of_a_captured_pass_are_not_seen(recorder, monkeypatch):
+    """A captured pass may have been replayed after any other: the calls that follow it are then not refused, those that
+    follow another pass still are."""
+    L = layer()
+    x, wg, b, W, wn = operands()
+    capturing = [True]
+    monkeypatch.setattr(moe, "_capturing", lambda t: capturing[0])
+    L.forward(x, wg, b, W, train=True)
+    capturing[0] = False
+    L.forward(x, wg, b, W)
+    L.backward(x, W)
+    L.forward_few(x, wg, b, W)
+    L.update_bias(b, 1e-3)
+    with pytest.raises(RuntimeError, match="backward_normed follows"):
+        L.backward_normed(x, wn, W)
+    capturing[0] = True
+    L.forward_normed(x, wn, 1e-6, wg, b, W, train=True)
+    capturing[0] = False
+    L.forward(x, wg, b, W)
+    L.backward_normed(x, wn, W)
