@@ -17,6 +17,10 @@ from ._lib import MoEError, RouteParams  # noqa: F401
 from .block import (moe_grad_norm, moe_grad_norm_workspace_bytes, moe_grad_scale, moe_layer_few,
                     moe_layer_few_pow2, moe_layer_few_workspace_bytes, moe_rmsnorm_backward,
                     moe_rmsnorm_backward_workspace_bytes, moe_rmsnorm_quant, moe_rmsnorm_quant_pow2)
+from .experts import (grouped_act_backward, grouped_act_backward_workspace_bytes, grouped_gemm16,
+                      grouped_gemm16_backward_workspace_bytes, grouped_gemm16_dgrad, grouped_gemm16_wgrad,
+                      grouped_gemm16_workspace_bytes, moe_collect, moe_collect_backward, moe_dispatch,
+                      moe_dispatch_backward, moe_dropout, moe_dropout_backward, moe_sort, moe_sort_workspace_bytes)
 
 __all__ = ["moe_route", "moe_route_workspace_bytes", "fp8_quant_1x128", "fp8_quant_128x128", "moe_permute_workspace_bytes",
            "moe_permute", "moe_permute_noalloc", "grouped_gemm_fp8_swiglu", "grouped_gemm_fp8_up", "grouped_gemm_fp8_down",
@@ -26,7 +30,11 @@ __all__ = ["moe_route", "moe_route_workspace_bytes", "fp8_quant_1x128", "fp8_qua
            "moe_swiglu_backward", "grouped_gemm_fp8_wgrad", "moe_rmsnorm_quant", "moe_rmsnorm_quant_pow2",
            "moe_rmsnorm_backward_workspace_bytes", "moe_rmsnorm_backward", "moe_layer_few_workspace_bytes",
            "moe_layer_few", "moe_layer_few_pow2", "moe_grad_norm_workspace_bytes",
-           "moe_grad_norm", "moe_grad_scale", "MoEWeights", "MoELayer",
+           "moe_grad_norm", "moe_grad_scale", "moe_sort_workspace_bytes", "moe_sort", "moe_dispatch",
+           "moe_dispatch_backward", "moe_collect", "moe_collect_backward", "grouped_gemm16_workspace_bytes",
+           "grouped_gemm16", "grouped_act_backward_workspace_bytes", "grouped_act_backward",
+           "grouped_gemm16_backward_workspace_bytes", "grouped_gemm16_dgrad", "grouped_gemm16_wgrad", "moe_dropout",
+           "moe_dropout_backward", "MoEWeights", "MoELayer",
            "MoEError", "RouteParams"]
 
 

@@ -12,6 +12,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "moe.h")
 BLOCK_HEADER = os.path.join(os.path.dirname(_HERE), "include", "moe_block.h")
+EXPERTS_HEADER = os.path.join(os.path.dirname(_HERE), "include", "moe_experts.h")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = range(5)
 
@@ -76,6 +77,21 @@ SIGNATURES = {
     "moe_grad_norm_workspace_bytes": (SZ, [I]),
     "moe_grad_norm": (I, [P, P, P, I, ctypes.c_float, P, P, P, SZ, P]),
     "moe_grad_scale": (I, [P, P, P, P, I, P, P]),
+    "moe_sort_workspace_bytes": (SZ, [I, I, I]),
+    "moe_sort": (I, [P, I, I, I, P, P, P, P, SZ, P]),
+    "moe_dispatch": (I, [I, P, P, P, I, I, I, I, P, P]),
+    "moe_dispatch_backward": (I, [I, P, P, P, P, P, I, I, I, I, P, P, P]),
+    "moe_collect": (I, [I, P, P, P, P, I, I, I, I, P, P]),
+    "moe_collect_backward": (I, [I, P, P, P, P, I, I, I, I, P, P, P]),
+    "grouped_gemm16_workspace_bytes": (SZ, [I, I, I, I, I]),
+    "grouped_gemm16": (I, [I, P, P, I, I, I, I, P, P, I, P, P, P, P, SZ, P]),
+    "grouped_act_backward_workspace_bytes": (SZ, [I, I, I]),
+    "grouped_act_backward": (I, [I, P, P, P, I, I, I, I, P, P, P, SZ, P]),
+    "grouped_gemm16_backward_workspace_bytes": (SZ, [I, I, I, I]),
+    "grouped_gemm16_dgrad": (I, [I, P, P, I, I, I, I, P, P, P, P, SZ, P]),
+    "grouped_gemm16_wgrad": (I, [I, P, P, P, I, I, I, I, P, P, SZ, P]),
+    "moe_dropout": (I, [I, P, P, ctypes.c_int64, ctypes.c_float, P, P, P]),
+    "moe_dropout_backward": (I, [I, P, ctypes.c_int64, ctypes.c_float, P, P, P]),
     "moe_status_string": (ctypes.c_char_p, [I]),
     "moe_last_error": (ctypes.c_char_p, []),
 }

@@ -5,7 +5,6 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
-#include <initializer_list>
 #include <utility>
 #include <vector>
 
@@ -19,40 +18,6 @@ moe_status check_norm_shape(int T, int d) {
   REQUIRE(T >= 0, "T=%d is negative", T);
   REQUIRE(d >= 128 && d % 128 == 0, "d=%d must be a positive multiple of 128", d);
   if (d > moe::kNormMaxD) return fail(MOE_ERR_UNSUPPORTED, "d=%d > %d is not implemented", d, moe::kNormMaxD);
-  return MOE_OK;
-}
-
-#define REQUIRE_ALIGNED_OR_NULL(p)                                                                          \
-  do {                                                                                                      \
-    if ((p) != nullptr && !aligned16(p)) return fail(MOE_ERR_INVALID_ARG, "%s is not 16-byte aligned", #p); \
-  } while (0)
-
-// An operand's memory; NULL: not given.
-struct Span {
-  const char* name;
-  const void* p;
-  size_t bytes;
-};
-bool overlap(const Span& a, const Span& b) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  return x != 0 && y != 0 && x < y + b.bytes && y < x + a.bytes;
-}
-// No output shares memory with an input (but for `same`, whose operand it may
-// be as a whole) or with another output.
-struct Out {
-  Span span;
-  std::initializer_list<const void*> same;
-};
-moe_status check_apart(std::initializer_list<Out> outs, std::initializer_list<Span> ins) {
-  for (const Out* o = outs.begin(); o != outs.end(); ++o) {
-    for (const Span& i : ins) {
-      bool allowed = false;
-      for (const void* s : o->same) allowed = allowed || (s == i.p && s == o->span.p);
-      REQUIRE(allowed || !overlap(o->span, i), "%s must not share memory with %s", o->span.name, i.name);
-    }
-    for (const Out* b = outs.begin(); b != o; ++b)
-      REQUIRE(!overlap(o->span, b->span), "%s must not share memory with %s", o->span.name, b->span.name);
-  }
   return MOE_OK;
 }
 

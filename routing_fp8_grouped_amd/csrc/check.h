@@ -9,6 +9,7 @@
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
+#include <initializer_list>
 
 #include "moe.h"
 
@@ -57,6 +58,40 @@ inline moe_status hip_status(hipError_t e, const char* what) {
     if ((p) != nullptr && !aligned((p), 4))                                   \
       return fail(MOE_ERR_INVALID_ARG, "%s is not 4-byte aligned", #p);       \
   } while (0)
+
+#define REQUIRE_ALIGNED_OR_NULL(p)                                                                          \
+  do {                                                                                                      \
+    if ((p) != nullptr && !aligned16(p)) return fail(MOE_ERR_INVALID_ARG, "%s is not 16-byte aligned", #p); \
+  } while (0)
+
+// An operand's memory; NULL: not given.
+struct Span {
+  const char* name;
+  const void* p;
+  size_t bytes;
+};
+inline bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x != 0 && y != 0 && x < y + b.bytes && y < x + a.bytes;
+}
+// No output shares memory with an input (but for `same`, whose operand it may
+// be as a whole) or with another output.
+struct Out {
+  Span span;
+  std::initializer_list<const void*> same;
+};
+inline moe_status check_apart(std::initializer_list<Out> outs, std::initializer_list<Span> ins) {
+  for (const Out* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span& i : ins) {
+      bool allowed = false;
+      for (const void* s : o->same) allowed = allowed || (s == i.p && s == o->span.p);
+      REQUIRE(allowed || !overlap(o->span, i), "%s must not share memory with %s", o->span.name, i.name);
+    }
+    for (const Out* b = outs.begin(); b != o; ++b)
+      REQUIRE(!overlap(o->span, b->span), "%s must not share memory with %s", o->span.name, b->span.name);
+  }
+  return MOE_OK;
+}
 
 inline moe_status check_route_params(const moe_route_params& p) {
   REQUIRE(p.n_experts >= 1 && p.n_experts <= 256, "n_experts=%d must be in [1, 256]", p.n_experts);

@@ -114,6 +114,37 @@ hipError_t launch_grad_norm(const void* const* grads, const int64_t* sizes, cons
 hipError_t launch_grad_scale(const void* const* grads, void* const* outs, const int64_t* sizes, const int* types,
                              int n_tensors, const float* coef, hipStream_t stream);
 
+// Tokens sorted by expert and back (tokens.hip).  type: moe_dtype.
+constexpr int kSortMaxK = 64, kSortMaxE = 1024;
+size_t sort_workspace_bytes(int T, int k, int E);
+hipError_t launch_sort(const int32_t* idx, int T, int k, int E, int32_t* offsets, int32_t* pos, int32_t* row_slot,
+                       int32_t* counts, hipStream_t stream);
+// rows of a token's slots = w * token row, and the rows of y times the token's
+hipError_t launch_spread(int type, const void* x, const int32_t* pos, const float* w, const void* y, int T, int k, int d,
+                         int rows, void* out, float* dots, hipStream_t stream);
+// token row = sum of w * rows + residual, and the rows times x's
+hipError_t launch_sum(int type, const void* rows_in, const int32_t* pos, const float* w, const void* x,
+                      const void* residual, int T, int k, int d, int rows, void* out, float* dots, hipStream_t stream);
+
+// Matrix products in 16 bits (gemm16.hip) and their activation's gradient
+// (act.hip).  act: moe_act; group count up to groups.h's kMaxGroups.
+size_t gemm16_workspace_bytes(int rows, int n_groups, int K, int N, int act);
+hipError_t launch_gemm16(int type, const void* a, const int32_t* offsets, int n_groups, int rows, int K, int N,
+                         const void* b, const void* bias, int act, const void* residual, void* pre, void* out,
+                         void* workspace, hipStream_t stream);
+size_t gemm16_backward_workspace_bytes(int rows, int n_groups, int K, int N);
+hipError_t launch_gemm16_dgrad(int type, const void* dz, const int32_t* offsets, int n_groups, int rows, int K, int N,
+                               const void* b, const void* residual, void* da, void* workspace, hipStream_t stream);
+hipError_t launch_gemm16_wgrad(int type, const void* dz, const void* a, const int32_t* offsets, int n_groups, int rows,
+                               int K, int N, float* db, void* workspace, hipStream_t stream);
+size_t act_backward_workspace_bytes(int rows, int n_groups, int N);
+hipError_t launch_act_backward(int type, const void* dout, const void* pre, const int32_t* offsets, int n_groups,
+                               int rows, int N, int act, void* dz, float* dbias, float* partial, hipStream_t stream);
+
+// Dropout (dropout.hip).
+hipError_t launch_dropout(int type, const void* x, const void* residual, int64_t n, float p, const int64_t* rng,
+                          void* out, hipStream_t stream);
+
 // Measured roofs (roofs.hip): FP8 MFMA issue rate and HBM read streaming.
 hipError_t launch_roof_mfma(int workgroups, int iters, float* sink, hipStream_t stream);
 hipError_t launch_roof_dma(const void* buf, size_t bytes, int K, int ahead, int workgroups, uint32_t* sink,

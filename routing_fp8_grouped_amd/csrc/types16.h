@@ -1,0 +1,108 @@
+// Element types of the operators whose operands are not quantised (BF16, FP16,
+// FP32): 16-byte chunks of them, conversions, and the launch dispatch over
+// moe_dtype.
+#pragma once
+
+#include <type_traits>
+
+#include "common.h"
+
+namespace moe {
+
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// kWidth elements make one 16-byte chunk.  Stores round to nearest even
+// (hardware conversions: infinities and NaN stay what they are).
+struct Bf16 {
+  using storage = uint16_t;
+  using frag = v8bf;
+  static constexpr int kWidth = 8;
+  static __device__ __forceinline__ float load(storage s) { return bf16_to_f32(s); }
+  static __device__ __forceinline__ storage store(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+  static __device__ __forceinline__ v4f mfma(frag a, frag b, v4f c) { return mfma_bf16_16x16x32(a, b, c); }
+};
+struct Fp16 {
+  using storage = uint16_t;
+  using frag = v8h;
+  static constexpr int kWidth = 8;
+  static __device__ __forceinline__ float load(storage s) { return (float)__builtin_bit_cast(_Float16, s); }
+  static __device__ __forceinline__ storage store(float f) {
+    asm("" : "+v"(f));   // the FP32 value is what is rounded: no mixed-precision product straight to FP16
+    return __builtin_bit_cast(uint16_t, (_Float16)f);
+  }
+  static __device__ __forceinline__ v4f mfma(frag a, frag b, v4f c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
+};
+struct Fp32 {
+  using storage = float;
+  static constexpr int kWidth = 4;
+  static __device__ __forceinline__ float load(storage s) { return s; }
+  static __device__ __forceinline__ storage store(float f) { return f; }
+};
+
+// Two values in the two halves of a word.
+template <class E>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  return (uint32_t)E::store(lo) | ((uint32_t)E::store(hi) << 16);
+}
+template <class E>
+__device__ __forceinline__ float unpack(uint32_t word, int half) {
+  return E::load((uint16_t)(word >> (16 * half)));
+}
+
+// 16 bytes at an address that is only aligned to its elements (rows of any
+// width): global memory takes them in one instruction all the same.
+template <class S>
+__device__ __forceinline__ u32x4 load_chunk(const S* p) {
+  u32x4 v;
+  __builtin_memcpy(&v, p, 16);
+  return v;
+}
+template <class S>
+__device__ __forceinline__ void store_chunk(S* p, u32x4 v) {
+  __builtin_memcpy(p, &v, 16);
+}
+
+// FP32 values of a 16-byte chunk (WHOLE) or of one element.
+template <class E, bool WHOLE>
+struct Values {
+  using S = typename E::storage;
+  using raw = std::conditional_t<WHOLE, u32x4, S>;
+  static constexpr int n = WHOLE ? E::kWidth : 1;
+  float v[n];
+
+  static __device__ __forceinline__ raw fetch(const S* p) {
+    if constexpr (WHOLE) return load_chunk(p);
+    else return *p;
+  }
+  __device__ __forceinline__ Values() {
+#pragma unroll
+    for (int i = 0; i < n; ++i) v[i] = 0.0f;
+  }
+  __device__ __forceinline__ explicit Values(raw w) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      if constexpr (!WHOLE) v[i] = E::load(w);
+      else if constexpr (E::kWidth == 8) v[i] = unpack<E>(w[i / 2], i & 1);
+      else v[i] = __uint_as_float(w[i]);
+    }
+  }
+  __device__ __forceinline__ void put(S* p) const {
+    if constexpr (WHOLE) {
+      u32x4 w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (E::kWidth == 8) w[i] = pack2<E>(v[2 * i], v[2 * i + 1]);
+        else w[i] = __float_as_uint(v[i]);
+      }
+      store_chunk(p, w);
+    } else {
+      *p = E::store(v[0]);
+    }
+  }
+};
+
+}  // namespace moe
