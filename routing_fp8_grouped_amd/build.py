@@ -23,7 +23,7 @@ LIB = os.path.join(PKG, "libmoe.so")
 SOURCES = ["api.cpp", "quant.hip", "route.hip", "permute.hip", "gemm.hip", "gemm_small.hip",
            "combine.hip", "balance.hip", "backward.hip", "wgrad.hip", "roofs.hip",
            "api_block.cpp", "norm.hip", "few.hip", "grad.hip",
-           "api_experts.cpp", "tokens.hip", "gemm16.hip", "act.hip", "dropout.hip"]
+           "api_experts.cpp", "tokens.hip", "gemm16.hip", "gemm16_slim.hip", "act.hip", "dropout.hip"]
 ARCH = os.environ.get("MOE_OFFLOAD_ARCH", "gfx950")
 
 

@@ -20,44 +20,31 @@
 // bounds, which return zeros: no branch and no padded copy.
 #include <algorithm>
 
-#include "activation.h"
-#include "groups.h"
-#include "kernels.h"
-#include "types16.h"
+#include "gemm16.h"
 
 namespace moe {
 
 namespace {
 
 constexpr int BK = 64;
-
-struct Gemm16Args {
-  const uint16_t* p;     // m-side operand
-  const uint16_t* q;     // n-side operand
-  Groups groups;
-  int M, N, K;           // M: wgrad only (the others' m are the groups' rows); K: forward and dgrad only
-  const uint16_t* bias;      // [n_groups, N] or NULL
-  const uint16_t* residual;  // or NULL
-  uint16_t* pre;             // or NULL
-  void* out;
-  int act;
-};
+constexpr int SUPER = 4;
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
-// Direct load of 16 bytes a lane from base + off to LDS address lds + 16 lane;
-// lanes at kNowhere get zeros.  As with dma16 the compiler does not track it:
-// a read of its data follows ring_barrier().
+// Direct load of 16 bytes a lane from the buffer's byte off to LDS address lds +
+// 16 lane; lanes whose off is not below the buffer's size get zeros.  As with
+// dma16 the compiler does not track it: a read of its data follows
+// ring_barrier().
 constexpr uint32_t kNowhere = 0x7FFFFFF0u;
-__device__ __forceinline__ i32x4 bounded(const void* base) {
-  const uint64_t v = reinterpret_cast<uint64_t>(base);
-  return i32x4{(int)__builtin_amdgcn_readfirstlane((uint32_t)v),
-               (int)(__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32)) & 0xFFFFu), 0x7FFFFFE0, 0x00020000};
-}
 __device__ __forceinline__ void dma16_bounded(i32x4 buffer, uint32_t off, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
-               :: "v"(off), "s"(buffer), "s"(__builtin_amdgcn_readfirstlane(lds))
+               :: "v"(off), "s"(buffer), "s"(lds)
                : "memory");
+}
+__device__ __forceinline__ i32x4 buffer_of(uint64_t base, uint32_t bytes) {
+  return i32x4{(int)__builtin_amdgcn_readfirstlane((uint32_t)base),
+               (int)(__builtin_amdgcn_readfirstlane((uint32_t)(base >> 32)) & 0xFFFFu),
+               (int)__builtin_amdgcn_readfirstlane(bytes), 0x00020000};
 }
 
 // Chunk position of a k-strided operand's k-row: the four k-rows that 16 lanes
@@ -65,257 +52,581 @@ __device__ __forceinline__ void dma16_bounded(i32x4 buffer, uint32_t off, uint32
 // eight different 32-byte places of 256 bytes.
 __device__ __forceinline__ int tr_swz(int k) { return ((k & 3) | ((k >> 1) & 4)) << 1; }
 
-// One operand's [R x 64] block of a tile.
+// One operand's [R x 64] block of a tile.  Each wave makes kLoads of its 1 KB
+// loads: load q is rows 8 q .. 8 q + 7 (k-contiguous) or kRows k-rows from
+// kRows q on.
+//
+// What lies outside: rows past the tile's last are out of the buffer's bounds
+// (zeros); k-rows past K too.  k past K in a k-contiguous row is masked.
+// Columns past the last of a k-strided operand are the next k-row's: they only
+// reach results that are not stored.
 template <int R, bool TR, int NW>
 struct Operand {
   static constexpr int kBytes = R * BK * 2;
-  static constexpr int kLoads = kBytes / 1024 / NW;   // direct loads of a wave
+  static constexpr int kLoads = kBytes / 1024 / NW;
+  static constexpr int kRows = TR ? 512 / R : 8;
   static_assert(kLoads * 1024 * NW == kBytes, "whole loads");
 
-  const uint16_t* base;     // first element of the tile, k = 0
-  size_t step;              // elements from one K block to the next
-  uint32_t off[kLoads];     // per-lane byte offsets
+  uint64_t base;           // of the next K block to load
+  uint32_t bytes, step;    // of the buffer from base on; from one block to the next
+  int64_t row_bytes;       // of a memory row
+  int cut;                 // k-strided: bytes of base past the start of its row
+  uint32_t off[kLoads];    // the lane's bytes from base on
+  uint32_t lds;            // the wave's first load within a block in LDS
+  uint32_t k_lane;         // k-contiguous: first byte of the lane's k within a block
 
-  // r0: first row of the tile in the operand (its column if k-strided); valid:
-  // rows (columns) there are; ld: elements of a memory row
-  __device__ __forceinline__ void start(const uint16_t* mem, size_t row0, int col0, int valid, size_t ld, int wave,
-                                        int lane) {
-    base = mem + row0 * ld + col0;
-    step = TR ? BK * ld : BK;
+  // mem: the tile's first row (k-row) and column; col0: that column; valid: rows
+  // there are (k-contiguous); load: the wave's first one in memory
+  __device__ __forceinline__ void start(const uint16_t* mem, int col0, int64_t valid, int64_t ld, int lds_load,
+                                        int load, int lane) {
+    base = reinterpret_cast<uint64_t>(mem);
+    row_bytes = ld * 2;
+    bytes = TR ? 0u : (uint32_t)min(valid * row_bytes, (int64_t)0x7FF00000);
+    step = TR ? (uint32_t)(BK * row_bytes) : BK * 2;
+    cut = col0 * 2;
+    lds = lds_load * 1024;
+    const int r = TR ? lane / (R / 8) : lane >> 3;
+    const int c = TR ? (lane & (R / 8 - 1)) ^ tr_swz(r) : (lane & 7) ^ op_swz(r);
+    k_lane = c * 16;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int byte = (wave * kLoads + i) * 1024 + lane * 16;
-      if (TR) {
-        const int k = byte / (R * 2), c = ((byte % (R * 2)) >> 4) ^ tr_swz(k);
-        off[i] = c * 8 < valid ? (uint32_t)(k * ld * 2) + c * 16 : kNowhere;
-      } else {
-        const int r = byte >> 7, c = ((byte >> 4) & 7) ^ op_swz(r);
-        off[i] = r < valid ? (uint32_t)(r * ld * 2) + c * 16 : kNowhere;
-      }
+      // the swizzle of load q's k-rows differs from load 0's by a constant
+      const int cc = TR ? c ^ tr_swz((lds_load + i) * kRows) : c;
+      off[i] = (uint32_t)(((load + i) * kRows + r) * row_bytes) + cc * 16;
     }
   }
-  // K block kb into `lds`; left: elements of K from this block on
-  __device__ __forceinline__ void issue(int kb, int left, uint32_t lds, int wave, int lane) const {
-    const i32x4 buffer = bounded(base + (size_t)kb * step);
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      uint32_t o = off[i];
-      if (left < BK) {
-        const int byte = (wave * kLoads + i) * 1024 + lane * 16;
-        const int k = TR ? byte / (R * 2) : (((byte >> 4) & 7) ^ op_swz(byte >> 7)) * 8;
-        if (k >= left) o = kNowhere;
-      }
-      dma16_bounded(buffer, o, lds + (wave * kLoads + i) * 1024);
-    }
+  // The next block, of which `left` elements of K are there: its buffer, then loads i of it into LDS
+  __device__ __forceinline__ i32x4 block(int left) const {
+    return buffer_of(base, TR ? (uint32_t)(min(left, BK) * row_bytes - cut) : bytes);
   }
-  // MFMA fragment of rows r0 .. r0+15, k in [32 s, 32 s + 32)
-  template <class F>
-  static __device__ __forceinline__ F frag(const unsigned char* lds, int r0, int s, int lane) {
+  __device__ __forceinline__ void advance() {
+    base += step;
+    if (!TR) bytes -= step;
+  }
+  __device__ __forceinline__ void load(int i, i32x4 buffer, int left, uint32_t at) const {
+    uint32_t o = off[i];
+    if (!TR) o = (int)k_lane < left * 2 ? o : kNowhere;
+    dma16_bounded(buffer, o, __builtin_amdgcn_readfirstlane(at + lds + i * 1024));
+  }
+  // Where this lane reads its part of a fragment of the wave whose first one is
+  // number i0: fragment i0 + i is at an offset (or, k-strided, an exclusive or).
+  static __device__ __forceinline__ uint32_t lane_at(int i0, int lane) {
     const int g = lane >> 4, i = lane & 15;
+    if (TR) {
+      const int k = g * 8 + (i >> 2);
+      return (k * (R * 2) + (tr_swz(k) << 4) + ((i & 2) << 3) + ((i & 1) << 3)) ^ (i0 << 5);
+    }
+    return i0 * 2048 + i * 128 + ((g ^ op_swz(i)) << 4);
+  }
+  // MFMA fragment of rows 16 (i0 + i) .. + 15, k in [32 s, 32 s + 32); at: the
+  // LDS address of the block + lane_at(i0)
+  template <class F>
+  static __device__ __forceinline__ F frag(uint32_t at, int i, int s) {
+    typedef __attribute__((address_space(3))) char lds_char;
     if constexpr (TR) {
       typedef short v4s __attribute__((ext_vector_type(4)));
-      typedef __attribute__((address_space(3))) v4s lds_v4s;
-      const int k = s * 32 + g * 8 + (i >> 2);
-      const int c = (r0 >> 3) + ((i >> 1) & 1), h = (i & 1) * 8;
-      const uint32_t at = lds_addr(lds);
-      const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (lds_v4s*)(uintptr_t)(at + k * (R * 2) + ((c ^ tr_swz(k)) << 4) + h));
-      const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (lds_v4s*)(uintptr_t)(at + (k + 4) * (R * 2) + ((c ^ tr_swz(k + 4)) << 4) + h));
       typedef short v8s __attribute__((ext_vector_type(8)));
+      typedef __attribute__((address_space(3))) v4s lds_v4s;
+      lds_char* x = (lds_char*)(uintptr_t)(at ^ (uint32_t)(i << 5));
+      const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(x + s * 32 * R * 2));
+      const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(x + (s * 32 + 4) * R * 2));
       return __builtin_bit_cast(F, v8s{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
     } else {
-      const int r = r0 + i;
-      return *reinterpret_cast<const F*>(lds + r * 128 + (((s * 4 + g) ^ op_swz(r)) << 4));
+      typedef __attribute__((address_space(3))) F lds_f;
+      return *(lds_f*)((lds_char*)(uintptr_t)(at ^ (uint32_t)(s << 6)) + i * 2048);
     }
   }
 };
 
-enum Kind { kForward = 0, kForwardGlu = 1, kDgrad = 2, kWgrad = 3 };
+// kDgradPart, kWgradPart: the sum over a part of k, FP32, into the workspace.
+enum Kind { kForward = 0, kForwardGlu = 1, kDgrad = 2, kWgrad = 3, kDgradPart = 4, kWgradPart = 5 };
 
-// Eight neighbouring columns of a lane from two sub-tiles' accumulators: lanes
-// 16 apart trade halves.  They belong to column 16 (g & 1) + 8 (g >> 1) of the
-// pair's 32, g = lane / 16.
-__device__ __forceinline__ void columns8(const v4f a, const v4f b, float (&f)[8]) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(a[e]), __float_as_uint(b[e]), false, false);
-    f[e] = __uint_as_float(x[0]);
-    f[4 + e] = __uint_as_float(x[1]);
-  }
+// Waits until at most n of the wave's vector memory operations are outstanding
+// and its LDS operations are done, then for the other waves.  n is uniform and
+// one of a few.
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));
 }
-
-__device__ __forceinline__ float activate(int act, float z) {
-  switch (act) {
-    case kActRelu: return act_value<kActRelu>(z);
-    case kActSilu: return act_value<kActSilu>(z);
-    case kActGelu: return act_value<kActGelu>(z);
-    default: return z;
-  }
-}
+__device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory"); }
 
 template <class E, int KIND, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM * WN * 64, 1) void gemm16_kernel(Gemm16Args p) {
   constexpr int NW = WM * WN, MS = BM / WM / 16, NS = BN / WN / 16;
-  constexpr bool GLU = KIND == kForwardGlu;
+  constexpr bool GLU = KIND == kForwardGlu, WGRAD = KIND == kWgrad || KIND == kWgradPart;
+  constexpr bool DGRAD = KIND == kDgrad || KIND == kDgradPart, PART = KIND == kDgradPart || KIND == kWgradPart;
+  constexpr bool F32 = WGRAD || PART;   // out is FP32, stored from registers
   using F = typename E::frag;
-  using P = Operand<BM, KIND == kWgrad, NW>;
-  using Q = Operand<BN, KIND == kDgrad || KIND == kWgrad, NW>;
-  constexpr int STG = P::kBytes + Q::kBytes;
-  __shared__ __attribute__((aligned(1024))) unsigned char sm[2 * STG];
-  __shared__ int first[KIND == kWgrad ? 1 : kMaxGroups + 1];
+  using P = Operand<BM, WGRAD, NW>;
+  using Q = Operand<BN, DGRAD || WGRAD, NW>;
+  constexpr int LOADS = P::kLoads + Q::kLoads;
+  __shared__ __attribute__((aligned(1024))) unsigned char sm[2 * (P::kBytes + Q::kBytes)];   // two blocks of P, two of Q
+  __shared__ int first[WGRAD ? 1 : kMaxGroups + 1];
 
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int wm = wave / WN, wn = wave % WN;
   const int g16 = lane >> 4, r16 = lane & 15;
   const int cols = GLU ? p.N / 2 : p.N;            // columns of out
   constexpr int TN = GLU ? BN / 2 : BN;            // columns of out in a tile
   const int nt = (cols + TN - 1) / TN, mt = (p.M + BM - 1) / BM;
+  const uint32_t ps = lds_addr(sm), qs = ps + 2 * P::kBytes;
+  const uint32_t p_at = ps + P::lane_at(wm * MS, lane), q_at = qs + Q::lane_at(GLU ? wn * (NS / 2) : wn * NS, lane);
   int total;
-  if constexpr (KIND == kWgrad) {
+  if constexpr (WGRAD) {
     total = p.groups.n * mt * nt;
   } else {
     list_tiles(p.groups, BM, first);
     total = first[p.groups.n] * nt;
   }
-  for (int L = blockIdx.x; L < total; L += gridDim.x) {
-    // ---- the tile ----
-    int g, m0, mv, n0;
-    int kext;
-    size_t row0;
-    if constexpr (KIND == kWgrad) {
-      g = L / (mt * nt);
-      const int rem = L - g * mt * nt;
-      m0 = rem / nt * BM;
-      n0 = rem % nt * BN;
-      mv = min(BM, p.M - m0);
-      row0 = p.groups.at(g);
-      kext = p.groups.count(g);
+  const int tiles = total;
+  if (PART) total *= p.parts;
+
+  // ---- tiles ----
+  struct Tile {
+    int g, m0, mv, n0, k, part;   // group, first row, rows there are, first column of out, length of the sum, its part
+  };
+  P pl;
+  Q ql;
+  int pleft = 0, qleft = 0;   // of K, from each operand's next block to load on
+  // Tile `local` of a group of `rows` row tiles: super-blocks of SUPER row tiles,
+  // in them columns of tiles
+  auto place = [&](int local, int rows, int& m, int& n) {
+    const int sb = local / (SUPER * nt), rem = local - sb * SUPER * nt, msb = min(SUPER, rows - sb * SUPER);
+    n = rem / msb;
+    m = sb * SUPER + rem - n * msb;
+  };
+  auto open = [&](int L) {
+    Tile t;
+    t.part = PART ? L / tiles : 0;
+    if (PART) L -= t.part * tiles;
+    // the part's first k and its length, whole blocks
+    auto cut = [&](int k) {
+      if (!PART) {
+        t.k = k;
+        return 0;
+      }
+      const int64_t kb = (k + BK - 1) / BK;
+      const int k0 = (int)(kb * t.part / p.parts) * BK;
+      t.k = min(k, (int)(kb * (t.part + 1) / p.parts) * BK) - k0;
+      return k0;
+    };
+    const int pload = wave * P::kLoads, qload = wave * Q::kLoads;
+    if constexpr (WGRAD) {
+      t.g = L / (mt * nt);
+      int m, n;
+      place(L - t.g * mt * nt, mt, m, n);
+      t.m0 = m * BM;
+      t.n0 = n * BN;
+      t.mv = min(BM, p.M - t.m0);
+      const size_t row0 = (size_t)p.groups.at(t.g) + cut(p.groups.count(t.g));
+      pl.start(p.p + row0 * p.M + t.m0, t.m0, 0, p.M, pload, pload, lane);
+      ql.start(p.q + row0 * p.N + t.n0, t.n0, 0, p.N, qload, qload, lane);
     } else {
-      const int tm = L / nt;
-      g = tile_group(first, p.groups.n, tm);
-      const int at = p.groups.at(g);
-      m0 = at + (tm - first[g]) * BM;
-      n0 = (L - tm * nt) * TN;
-      mv = min(BM, p.groups.at(g + 1) - m0);
-      row0 = 0;
-      kext = p.K;
-    }
-    P pl;
-    Q ql;
-    if constexpr (KIND == kWgrad) {
-      pl.start(p.p, row0, m0, mv, p.M, wave, lane);
-      ql.start(p.q, row0, n0, p.N - n0, p.N, wave, lane);
-    } else {
-      pl.start(p.p, m0, 0, mv, p.K, wave, lane);
-      const uint16_t* b = p.q + (size_t)g * p.N * p.K;
-      if constexpr (KIND == kDgrad) ql.start(b, 0, n0, p.N - n0, p.N, wave, lane);
-      else if constexpr (!GLU) ql.start(b, n0, 0, p.N - n0, p.K, wave, lane);
+      t.g = tile_group(first, p.groups.n, L / nt);
+      const int f0 = __builtin_amdgcn_readfirstlane(first[t.g]), f1 = __builtin_amdgcn_readfirstlane(first[t.g + 1]);
+      int m, n;
+      place(L - f0 * nt, f1 - f0, m, n);
+      t.m0 = __builtin_amdgcn_readfirstlane(p.groups.at(t.g)) + m * BM;
+      t.n0 = n * TN;
+      t.mv = __builtin_amdgcn_readfirstlane(min(BM, p.groups.at(t.g + 1) - t.m0));
+      const int k0 = cut(p.K);
+      pl.start(p.p + (size_t)t.m0 * p.K + k0, 0, t.mv, p.K, pload, pload, lane);
+      pl.bytes -= k0 * 2;
+      const uint16_t* b = p.q + (size_t)t.g * p.N * p.K;
+      if constexpr (DGRAD) ql.start(b + (size_t)k0 * p.N + t.n0, t.n0, 0, p.N, qload, qload, lane);
+      else if constexpr (!GLU) ql.start(b + (size_t)t.n0 * p.K, 0, p.N - t.n0, p.K, qload, qload, lane);
       else {
         // the first half of the tile's rows are gate rows, the second the same
         // columns' up rows; each wave loads rows of one half
         const int h = wave >= NW / 2;
-        ql.start(b, n0 + (size_t)h * (cols - BN / 2), 0, min(BN, cols - n0 + h * (BN / 2)), p.K, wave, lane);
+        ql.start(b + (size_t)(t.n0 + h * cols) * p.K, 0, cols - t.n0, p.K, qload, qload - h * (BN / 16), lane);
       }
     }
+    pleft = qleft = t.k;
+    return t;
+  };
+  auto refill_p = [&](int kb) {
+    const i32x4 buffer = pl.block(pleft);
+#pragma unroll
+    for (int i = 0; i < P::kLoads; ++i) pl.load(i, buffer, pleft, ps + (kb & 1) * P::kBytes);
+    pl.advance();
+    pleft -= BK;
+  };
+  auto refill_q = [&](int kb) {
+    const i32x4 buffer = ql.block(qleft);
+#pragma unroll
+    for (int i = 0; i < Q::kLoads; ++i) ql.load(i, buffer, qleft, qs + (kb & 1) * Q::kBytes);
+    ql.advance();
+    qleft -= BK;
+  };
+  // What is loaded of the next tile while this one's results are stored: two
+  // blocks, or one where the other's place holds results on their way.
+  constexpr int EARLY = F32 ? 2 : 1;
+  constexpr int STORES = F32 ? MS * NS : 0;   // of a tile, each wave
+  auto early = [&](const Tile& t) {
+#pragma unroll
+    for (int kb = 0; kb < EARLY; ++kb)
+      if (kb * BK < t.k) {
+        refill_p(kb);
+        refill_q(kb);
+      }
+  };
+
+  // Workgroup b runs on XCD b % 8 and takes tiles of its XCD's contiguous eighth
+  // of the list, so that workgroups behind one L2 share operands.
+  const int xcd = blockIdx.x & 7, hi = (int)((long)total * (xcd + 1) / 8), step_L = gridDim.x >> 3;
+  int L = (int)((long)total * xcd / 8) + (blockIdx.x >> 3);
+  if (L >= hi) return;
+  Tile cur = open(L);
+  early(cur);
+  bool stored = false;   // a tile's stores follow its early loads
+  while (true) {
+    const int KB = (cur.k + BK - 1) / BK;
     v4f acc[MS][NS];
 #pragma unroll
     for (int ms = 0; ms < MS; ++ms)
 #pragma unroll
       for (int ns = 0; ns < NS; ++ns) acc[ms][ns] = v4f{0.f, 0.f, 0.f, 0.f};
-    const int KB = (kext + BK - 1) / BK;
-    __syncthreads();   // the last tile's reads are done
-    auto issue = [&](int kb) {
-      const uint32_t s = lds_addr(sm + (kb & 1) * STG);
-      pl.issue(kb, kext - kb * BK, s, wave, lane);
-      ql.issue(kb, kext - kb * BK, s + P::kBytes, wave, lane);
+
+    // A wave holds its m-side fragments of a step of 32 k and streams the n-side
+    // ones, AHEAD of their use; the next step's m-side fragments replace these
+    // behind their last use.  So the m-side place of a block is free at the
+    // beginning of its second step, the n-side place at its end: a barrier each,
+    // and it is refilled.  Loads are never all waited for at once, and the L2,
+    // which gives at most some 12 TB/s here (23 bytes a clock and CU), is kept
+    // busy: with one refill a block the tile of 256 x 256 was 5% slower.
+    constexpr int AHEAD = NS > 3 ? 3 : NS - 1, SLOTS = AHEAD + 1;
+    static_assert(NS % SLOTS == 0, "a fragment has the same slot in every step");
+    F pf[MS], qf[SLOTS];
+    auto readq = [&](int kb, int s, int ns) {
+      const int i = GLU ? (ns < NS / 2 ? 0 : BN / 32) + ns % (NS / 2) : ns;
+      qf[ns % SLOTS] = Q::template frag<F>(q_at + (kb & 1) * Q::kBytes, i, s);
     };
-    if (KB > 0) issue(0);
-    for (int kb = 0; kb < KB; ++kb) {
-      ring_barrier();
-      if (kb + 1 < KB) issue(kb + 1);
-      const unsigned char* ps = sm + (kb & 1) * STG;
-      const unsigned char* qs = ps + P::kBytes;
+    auto readp = [&](int kb, int s, int ms) { pf[ms] = P::template frag<F>(p_at + (kb & 1) * P::kBytes, ms, s); };
+    auto free_p = [&](int kb) {
+      __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+      barrier();
+      if (kb + 2 < KB) refill_p(kb);
+    };
+    // the next block has landed: all but what was issued after it (its own n-side
+    // refill comes first; then stores, if they stand between)
+    auto next_landed = [&](int kb) {
+      const bool after_stores = STORES > 0 && kb == 0 && stored;
+      if (kb + 2 < KB) {
+        if (after_stores) wait_vm<P::kLoads + STORES>();
+        else wait_vm<P::kLoads>();
+      } else {
+        if (after_stores) wait_vm<STORES>();
+        else wait_vm<0>();
+      }
+      barrier();
+    };
+    auto step = [&](int kb, int s, bool more) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        F pf[MS];
+      for (int ns = 0; ns < NS; ++ns) {
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        if (s == 1 && ns == 0) free_p(kb);
+        if (s == 1 && ns == NS - AHEAD && more) next_landed(kb);
+        if (ns + AHEAD < NS) readq(kb, s, ns + AHEAD);
+        else if (more) readq(kb + s, s ^ 1, ns + AHEAD - NS);
+        if (s == 1 && ns == NS - 1 && kb + 2 < KB) refill_q(kb);
 #pragma unroll
-        for (int ms = 0; ms < MS; ++ms) pf[ms] = P::template frag<F>(ps, wm * MS * 16 + ms * 16, s, lane);
+        for (int ms = 0; ms < MS; ++ms) {
+          acc[ms][ns] = E::mfma(qf[ns % SLOTS], pf[ms], acc[ms][ns]);
+          if (ns + 1 == NS && more) {
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+            readp(kb + s, s ^ 1, ms);
+          }
+        }
+      }
+    };
+    if (KB > 0) {
+      // block 0
+      if (!F32 || !stored) {
+        if (EARLY > 1 && KB > 1) wait_vm<LOADS>();
+        else wait_vm<0>();
+      } else {
+        if (KB > 1) wait_vm<LOADS + STORES>();
+        else wait_vm<STORES>();
+      }
+      barrier();
+      if (EARLY == 1 && KB > 1) {
+        refill_p(1);
+        refill_q(1);
+      }
+      if (wm * MS * 16 < cur.mv) {
 #pragma unroll
-        for (int ns = 0; ns < NS; ++ns) {
-          const int r = GLU ? (ns < NS / 2 ? 0 : BN / 2) + wn * (NS / 2) * 16 + (ns % (NS / 2)) * 16 : (wn * NS + ns) * 16;
-          const F qf = Q::template frag<F>(qs, r, s, lane);
+        for (int ns = 0; ns < AHEAD; ++ns) readq(0, 0, ns);
 #pragma unroll
-          for (int ms = 0; ms < MS; ++ms) acc[ms][ns] = E::mfma(qf, pf[ms], acc[ms][ns]);
+        for (int ms = 0; ms < MS; ++ms) readp(0, 0, ms);
+        for (int kb = 0; kb < KB - 1; ++kb) {
+          step(kb, 0, true);
+          step(kb, 1, true);
+        }
+        step(KB - 1, 0, true);
+        step(KB - 1, 1, false);
+      } else {
+        // none of the wave's rows is there: its loads and barriers only
+        for (int kb = 0; kb < KB; ++kb) {
+          free_p(kb);
+          if (kb + 1 < KB) {
+            next_landed(kb);
+            if (kb + 2 < KB) refill_q(kb);
+          }
         }
       }
     }
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    barrier();   // every wave has read the last block
+    const Tile done = cur;
+    L += step_L;
+    const bool more_tiles = L < hi;
+    if (more_tiles) {
+      cur = open(L);
+      early(cur);
+    }
+
     // ---- epilogue: lane (g16, r16) holds row ms*16 + r16, columns ns*16 + 4*g16 .. +3 ----
-    const int lc = (g16 & 1) * 16 + (g16 >> 1) * 8;
-    if constexpr (KIND == kWgrad) {
-      float* out = static_cast<float*>(p.out) + (size_t)g * p.M * p.N;
+    if constexpr (F32) {
+      // From registers, every wave the same number of stores (rows and columns
+      // past the end are out of the buffer's bounds, which drops them), so that
+      // the next tile's waits can count over them.
+      const size_t row0 = WGRAD ? ((size_t)done.part * p.groups.n + done.g) * p.M : (size_t)done.part * p.groups.rows;
+      const uint64_t base = reinterpret_cast<uint64_t>(static_cast<float*>(p.out) + (row0 + done.m0) * p.N);
+      const __amdgpu_buffer_rsrc_t buffer = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<void*>(uniform_ptr(reinterpret_cast<const void*>(base))), 0,
+          __builtin_amdgcn_readfirstlane((uint32_t)min((int64_t)done.mv * p.N * 4, (int64_t)0x7FFFFFE0)), 0x00020000);
+      // A store is eight rows of 128 bytes: lanes eight apart trade sub-tiles, so
+      // that a row's two 64-byte parts come together.  (Rows of 64 bytes a store:
+      // 3.5 TB/s of gradients instead of 5.)
+      auto put = [&](int r, int c, const float (&v)[4]) {
+        const u32x4 w{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+        constexpr int kNonTemporal = 2;
+        __builtin_amdgcn_raw_buffer_store_b128(w, buffer, c < p.N ? (uint32_t)(r * (int64_t)p.N + c) * 4 : kNowhere, 0,
+                                               kNonTemporal);
+      };
 #pragma unroll
       for (int ms = 0; ms < MS; ++ms) {
-        const int m = m0 + wm * MS * 16 + ms * 16 + r16;
+        const int r = wm * MS * 16 + ms * 16 + (r16 & 7);
 #pragma unroll
-        for (int ns = 0; ns < NS; ++ns) {
-          const int n = n0 + (wn * NS + ns) * 16 + 4 * g16;
-          if (m < p.M && n < p.N) *reinterpret_cast<v4f*>(out + (size_t)m * p.N + n) = acc[ms][ns];
+        for (int ns = 0; ns < NS; ns += 2) {
+          const int c = done.n0 + (wn * NS + ns + (r16 >> 3)) * 16 + 4 * g16;
+          float lo[4], hi8[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            constexpr int ROW_ROR8 = 0x128;
+            const int x = __float_as_int(acc[ms][ns][e]), y = __float_as_int(acc[ms][ns + 1][e]);
+            lo[e] = __int_as_float(__builtin_amdgcn_update_dpp(x, y, ROW_ROR8, 0xF, 0xC, false));
+            hi8[e] = __int_as_float(__builtin_amdgcn_update_dpp(y, x, ROW_ROR8, 0xF, 0x3, false));
+          }
+          put(r, c, lo);
+          put(r + 8, c, hi8);
         }
       }
+      stored = true;
     } else {
-      uint16_t* out = static_cast<uint16_t*>(p.out);
-      constexpr int NP = GLU ? NS / 2 : NS;
+      // Sixteen rows at a time go through the wave's part of the second block's
+      // place, so that what follows is one short loop over whole chunks of rows:
+      // code that runs once a tile is fetched at some 0.1 us per 128 bytes, and an
+      // activation spelled out for every register took 70 us a tile.  What is
+      // loaded here (bias, residual) is loaded a pass ahead.
+      using V8 = Values<E, true>;
+      constexpr int CH = GLU ? NS : 2 * NS;   // 16-byte chunks of a row of out
+      constexpr int IT = 16 * CH / 64;
+      static_assert(IT * 64 == 16 * CH && 64 % CH == 0, "a lane keeps its columns");
+      constexpr int kPart = 16 * NS * 64;      // bytes of sixteen rows of the wave's columns
+      static_assert(NW * kPart <= P::kBytes + Q::kBytes && P::kBytes % kPart == 0, "parts fit");
+      const int er = lane / CH, ec = lane % CH;
+      const int n = done.n0 + (wn * CH + ec) * 8;
+      const bool nok = n < cols;
+      u32x4 bg{}, bu{}, rv[IT];
+      auto fetch = [&](int pass, int i) {
+        const int r = min(wm * MS * 16 + pass * 16 + er + i * (64 / CH), done.mv - 1);
+        if (p.residual) rv[i] = load_chunk(p.residual + ((size_t)done.m0 + r) * cols + (nok ? n : 0));
+      };
+      if (p.bias) {
+        const uint16_t* bp = p.bias + (size_t)done.g * p.N + (nok ? n : 0);
+        bg = load_chunk(bp);
+        if (GLU) bu = load_chunk(bp + cols);
+      }
 #pragma unroll
-      for (int ns = 0; ns < NP; ns += 2) {
-        const int n = n0 + (wn * NP + ns) * 16 + lc;
-        Values<E, true> bg, bu;
-        if (p.bias && n < cols) {
-          bg = Values<E, true>(load_chunk(p.bias + (size_t)g * p.N + n));
-          if (GLU) bu = Values<E, true>(load_chunk(p.bias + (size_t)g * p.N + cols + n));
-        }
+      for (int i = 0; i < IT; ++i) fetch(0, i);
+      const int at = wave * kPart;
+      unsigned char* ep = sm + (at < P::kBytes ? P::kBytes + at : 2 * P::kBytes + Q::kBytes + at - P::kBytes);
+      auto chunk16 = [&](int r, int c) { return *reinterpret_cast<const v4f*>(ep + r * (NS * 64) + ((c ^ (r & 7)) << 4)); };
+      if (wm * MS * 16 < done.mv)
+#pragma unroll 1
+      for (int pass = 0; pass < MS; ++pass) {
 #pragma unroll
-        for (int ms = 0; ms < MS; ++ms) {
-          const int r = wm * MS * 16 + ms * 16 + r16;
-          const size_t m = m0 + r;
-          Values<E, true> z, u;
-          columns8(acc[ms][ns], acc[ms][ns + 1], z.v);
-          if constexpr (GLU) columns8(acc[ms][NP + ns], acc[ms][NP + ns + 1], u.v);
-          if (r >= mv || n >= cols) continue;
+        for (int ms = 0; ms < MS; ++ms)
+          if (pass == ms)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) z.v[e] += bg.v[e];
-          if (GLU)
+            for (int ns = 0; ns < NS; ++ns)
+              *reinterpret_cast<v4f*>(ep + r16 * (NS * 64) + (((ns * 4 + g16) ^ (r16 & 7)) << 4)) = acc[ms][ns];
+        __builtin_amdgcn_wave_barrier();   // the wave's LDS operations are in order
 #pragma unroll
-            for (int e = 0; e < 8; ++e) u.v[e] += bu.v[e];
-          if (p.pre) {
+        for (int i = 0; i < IT; ++i) {
+          const int r = er + i * (64 / CH), tr = wm * MS * 16 + pass * 16 + r;
+          const bool ok = tr < done.mv && nok;
+          const size_t m = (size_t)done.m0 + tr;
+          auto z8 = [&](int c) {
+            V8 z;
+            const v4f a = chunk16(r, c), b = chunk16(r, c + 1);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z.v[e] = a[e], z.v[4 + e] = b[e];
+            return z;
+          };
+          auto add = [](V8& z, const V8& v) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z.v[e] += v.v[e];
+          };
+          V8 z = z8(2 * ec), u;
+          add(z, V8(bg));
+          if (GLU) {
+            u = z8(2 * (CH + ec));
+            add(u, V8(bu));
+          }
+          if (p.pre && ok) {
             z.put(p.pre + m * p.N + n);
             if (GLU) u.put(p.pre + m * p.N + cols + n);
           }
+          if constexpr (GLU) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) z.v[e] = GLU ? swiglu_f32(z.v[e], u.v[e]) : activate(p.act, z.v[e]);
-          if (p.residual) {
-            const Values<E, true> res(load_chunk(p.residual + m * cols + n));
-#pragma unroll
-            for (int e = 0; e < 8; ++e) z.v[e] += res.v[e];
+            for (int e = 0; e < 8; ++e) z.v[e] = glu_value(z.v[e], u.v[e]);
+          } else if constexpr (KIND == kForward) {
+            activate(p.act, z.v);
           }
-          z.put(out + m * cols + n);
+          if (p.residual) add(z, V8(rv[i]));
+          fetch(min(pass + 1, MS - 1), i);
+          if (ok) z.put(static_cast<uint16_t*>(p.out) + m * cols + n);
         }
       }
+    }
+    if (!more_tiles) return;
+  }
+}
+
+// out = the sum of the parts in order (+ residual, to the type), or FP32 (TO32).
+// Rows from the last group's end on are left.
+template <class E, bool TO32>
+__global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ parts, int n, size_t size, Groups groups,
+                                                   int cols, const uint16_t* residual, void* out) {
+  const size_t end = TO32 ? size : (size_t)groups.at(groups.n) * cols;
+  for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 8; i < end; i += (size_t)gridDim.x * 256 * 8) {
+    v4f a = *reinterpret_cast<const v4f*>(parts + i), b = *reinterpret_cast<const v4f*>(parts + i + 4);
+    for (int s = 1; s < n; ++s) {
+      a += *reinterpret_cast<const v4f*>(parts + s * size + i);
+      b += *reinterpret_cast<const v4f*>(parts + s * size + i + 4);
+    }
+    if constexpr (TO32) {
+      *reinterpret_cast<v4f*>(static_cast<float*>(out) + i) = a;
+      *reinterpret_cast<v4f*>(static_cast<float*>(out) + i + 4) = b;
+    } else {
+      Values<E, true> v;
+      if (residual) v = Values<E, true>(load_chunk(residual + i));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v.v[e] += a[e], v.v[4 + e] += b[e];
+      v.put(static_cast<uint16_t*>(out) + i);
     }
   }
 }
 
-template <int KIND>
-hipError_t launch(int type, const Gemm16Args& p, long tiles_bound, hipStream_t stream) {
-  const unsigned grid = (unsigned)std::min(tiles_bound, 512L);
-  if (type == 0) hipLaunchKernelGGL((gemm16_kernel<Bf16, KIND, 128, 128, 2, 2>), dim3(grid), dim3(256), 0, stream, p);
-  else hipLaunchKernelGGL((gemm16_kernel<Fp16, KIND, 128, 128, 2, 2>), dim3(grid), dim3(256), 0, stream, p);
-  return hipGetLastError();
+// Tiles of a product with `m` rows (over all groups) and n columns, about: half
+// a row tile more for every group that has rows.
+long tiles_of(long m, int groups, int n, int bm, int bn) {
+  const long live = std::min<long>(groups, m);
+  const long rows = live <= 1 ? (m + bm - 1) / bm : (2 * m / bm + live + 1) / 2;
+  return rows * ((n + bn - 1) / bn);
 }
 
-long tiles(long rows, int n_groups, int cols, int tn) { return (rows / 128 + n_groups) * ((cols + tn - 1) / tn); }
+constexpr int kCus = 256;
+
+// 256 x 256 tiles, one to a CU, or 128 x 128, two: whichever takes less time by
+// rounds of tiles.  Measured per block of 64 k with every CU busy: 1.6 us a
+// round of 256 x 256 tiles, 1.0 a round of 512 of 128 x 128 (8192 cubed: 0.81
+// against 1.0 ms).
+bool big_tiles(long t256, long t128) {
+  return 8 * ((t256 + kCus - 1) / kCus) <= 5 * ((t128 + 2 * kCus - 1) / (2 * kCus));
+}
+
+template <int KIND, class E>
+void launch_kind(const Gemm16Args& p, bool big, long tiles_bound, hipStream_t stream) {
+  const long wgs = (tiles_bound + 7) / 8 * 8;
+  if constexpr (KIND != kDgradPart && KIND != kWgradPart)
+    if (big) {
+      hipLaunchKernelGGL((gemm16_kernel<E, KIND, 256, 256, 4, 2>), dim3((unsigned)std::min(wgs, (long)kCus)), dim3(512), 0,
+                         stream, p);
+      return;
+    }
+  hipLaunchKernelGGL((gemm16_kernel<E, KIND, 128, 128, 2, 2>), dim3((unsigned)std::min(wgs, 2L * kCus)), dim3(256), 0,
+                     stream, p);
+}
+
+template <int KIND>
+void launch(int type, const Gemm16Args& p, bool big, long tiles_bound, hipStream_t stream) {
+  if (type == 0) launch_kind<KIND, Bf16>(p, big, tiles_bound, stream);
+  else launch_kind<KIND, Fp16>(p, big, tiles_bound, stream);
+}
+
+// Products over rows: tiles of both sizes, their bound for the launch.
+struct RowTiles {
+  bool big;
+  long bound;
+  RowTiles(int rows, int n_groups, int cols, bool glu) {
+    const int c256 = glu ? 128 : 256, c128 = glu ? 64 : 128;
+    big = big_tiles(tiles_of(rows, n_groups, cols, 256, c256), tiles_of(rows, n_groups, cols, 128, c128));
+    const int bm = big ? 256 : 128, bn = big ? c256 : c128;
+    bound = ((long)rows / bm + n_groups) * ((cols + bn - 1) / bn);
+  }
+};
+
+// Parts of k for the gradients' products, whose tiles may be too few for the
+// chip: the number with the least time in us by what was measured: a block of 64
+// k takes 0.65 with at most one 128 x 128 tile to a CU and 1.0 a round of two;
+// joining takes 3 for its launch and the parts' bytes, written and read, at 4
+// TB/s.  (16384 rows to 2048 x 2048: one part 194 us, two 149, four 160; 8192 rows
+// to 256 x 256: 70, 42, 26, 19 and 18.5 with 1 to 16.)
+int parts_of(long t128, int k, double elements) {
+  int best = 1;
+  double least = 0;
+  for (int p = 1; p <= 16; p *= 2) {
+    const long blocks = (k / BK + p - 1) / p, wgs = t128 * p;
+    if (p > 1 && blocks < 2) break;
+    const double rounds = wgs <= kCus ? 0.65 : (double)((wgs + 2 * kCus - 1) / (2 * kCus));
+    const double t = blocks * rounds + (p > 1 ? 3.0 + elements * 8 * p / 4e6 : 0.0);
+    if (p == 1 || t < least) {
+      least = t;
+      best = p;
+    }
+  }
+  return best;
+}
+int dgrad_parts(int rows, int n_groups, int K, int N) {
+  return parts_of(tiles_of(rows, n_groups, K, 128, 128), N, (double)rows * K);
+}
+int wgrad_parts(int rows, int n_groups, int K, int N) {
+  return parts_of((long)n_groups * ((N + 127) / 128) * ((K + 127) / 128), rows / n_groups, (double)n_groups * N * K);
+}
+
+template <bool TO32>
+void join(int type, const float* parts, int n, size_t size, const Groups& groups, int cols, const void* residual,
+          void* out, hipStream_t stream) {
+  const unsigned grid = (unsigned)std::min<size_t>((size / 8 + 255) / 256, 2048);
+  const uint16_t* res = static_cast<const uint16_t*>(residual);
+  if (type == 0) hipLaunchKernelGGL((join_kernel<Bf16, TO32>), dim3(grid), dim3(256), 0, stream, parts, n, size, groups, cols, res, out);
+  else hipLaunchKernelGGL((join_kernel<Fp16, TO32>), dim3(grid), dim3(256), 0, stream, parts, n, size, groups, cols, res, out);
+}
 
 }  // namespace
+
+size_t gemm16_workspace_bytes(int, int, int, int, int) { return 0; }
+
+size_t gemm16_backward_workspace_bytes(int rows, int n_groups, int K, int N) {
+  const int d = dgrad_parts(rows, n_groups, K, N), w = wgrad_parts(rows, n_groups, K, N);
+  return std::max(d > 1 ? (size_t)d * rows * K * 4 : 0, w > 1 ? (size_t)w * n_groups * N * K * 4 : 0);
+}
 
 hipError_t launch_gemm16(int type, const void* a, const int32_t* offsets, int n_groups, int rows, int K, int N,
                          const void* b, const void* bias, int act, const void* residual, void* pre, void* out,
@@ -332,13 +643,15 @@ hipError_t launch_gemm16(int type, const void* a, const int32_t* offsets, int n_
   p.pre = static_cast<uint16_t*>(pre);
   p.out = out;
   p.act = act;
-  if (act == kActSwiglu) return launch<kForwardGlu>(type, p, tiles(rows, n_groups, N / 2, 64), stream);
-  return launch<kForward>(type, p, tiles(rows, n_groups, N, 128), stream);
+  if (gemm16_slim(p)) return launch_gemm16_slim(type, p, stream);
+  const RowTiles t(rows, n_groups, act == kActSwiglu ? N / 2 : N, act == kActSwiglu);
+  if (act == kActSwiglu) launch<kForwardGlu>(type, p, t.big, t.bound, stream);
+  else launch<kForward>(type, p, t.big, t.bound, stream);
+  return hipGetLastError();
 }
 
 hipError_t launch_gemm16_dgrad(int type, const void* dz, const int32_t* offsets, int n_groups, int rows, int K, int N,
                                const void* b, const void* residual, void* da, void* workspace, hipStream_t stream) {
-  (void)workspace;
   Gemm16Args p{};
   p.p = static_cast<const uint16_t*>(dz);
   p.q = static_cast<const uint16_t*>(b);
@@ -347,12 +660,20 @@ hipError_t launch_gemm16_dgrad(int type, const void* dz, const int32_t* offsets,
   p.K = N;
   p.residual = static_cast<const uint16_t*>(residual);
   p.out = da;
-  return launch<kDgrad>(type, p, tiles(rows, n_groups, K, 128), stream);
+  p.parts = dgrad_parts(rows, n_groups, K, N);
+  const RowTiles t(rows, n_groups, K, false);
+  if (p.parts > 1) {
+    p.out = workspace;
+    launch<kDgradPart>(type, p, false, ((long)rows / 128 + n_groups) * ((K + 127) / 128) * p.parts, stream);
+    join<false>(type, static_cast<const float*>(workspace), p.parts, (size_t)rows * K, p.groups, K, residual, da, stream);
+  } else {
+    launch<kDgrad>(type, p, t.big, t.bound, stream);
+  }
+  return hipGetLastError();
 }
 
 hipError_t launch_gemm16_wgrad(int type, const void* dz, const void* a, const int32_t* offsets, int n_groups, int rows,
                                int K, int N, float* db, void* workspace, hipStream_t stream) {
-  (void)workspace;
   Gemm16Args p{};
   p.p = static_cast<const uint16_t*>(dz);
   p.q = static_cast<const uint16_t*>(a);
@@ -360,10 +681,21 @@ hipError_t launch_gemm16_wgrad(int type, const void* dz, const void* a, const in
   p.M = N;
   p.N = K;
   p.out = db;
-  return launch<kWgrad>(type, p, (long)n_groups * ((N + 127) / 128) * ((K + 127) / 128), stream);
+  p.parts = rows > 0 ? wgrad_parts(rows, n_groups, K, N) : 1;
+  const long t256 = (long)n_groups * ((N + 255) / 256) * ((K + 255) / 256);
+  const long t128 = (long)n_groups * ((N + 127) / 128) * ((K + 127) / 128);
+  if (p.parts > 1) {
+    p.out = workspace;
+    launch<kWgradPart>(type, p, false, t128 * p.parts, stream);
+    join<true>(type, static_cast<const float*>(workspace), p.parts, (size_t)n_groups * N * K, p.groups, K, nullptr, db,
+               stream);
+  } else {
+    // groups differ in rows, so in time: many tiles even it out (8192 rows in 33
+    // groups to 512 x 512: 30 us with the 132 large tiles, 17 with the small)
+    const bool big = big_tiles(t256, t128) && (n_groups == 1 || t256 >= 8 * kCus);
+    launch<kWgrad>(type, p, big, big ? t256 : t128, stream);
+  }
+  return hipGetLastError();
 }
-
-size_t gemm16_workspace_bytes(int, int, int, int, int) { return 0; }
-size_t gemm16_backward_workspace_bytes(int, int, int, int) { return 0; }
 
 }  // namespace moe

@@ -1,0 +1,234 @@
+// The forward product of include/moe_experts.h for few rows: out = act(a b^T +
+// bias) + residual where a tile kernel would leave most of the chip idle.
+//
+// A workgroup makes a slim tile (16 MB rows, 16 NB weight rows) alone: its eight
+// waves split K, stream their parts of both operands from memory straight into
+// MFMA fragments (no LDS, no barrier on the way) and join their sums in LDS at
+// the end.  With one row and N = 4096 every CU has a workgroup, and all of its
+// waves stream: a read of the weights and little else.
+#include <algorithm>
+#include <cmath>
+
+#include "gemm16.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 512, kWaves = kThreads / 64;
+constexpr int kNonTemporal = 2;
+constexpr uint32_t kNowhere = 0x7FFFFFF0u;   // out of every buffer's bounds: loads zeros
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* base) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(uniform_ptr(base)), 0, 0x7FFFFFE0, 0x00020000);
+}
+
+// R x 64 elements of an operand: R / 8 loads of eight whole lines each (eight
+// neighbouring lanes a row).  Fragments want one row a lane; loading them in
+// that layout would touch 64 lines an instruction.
+template <int R, int AUX>
+struct Lines {
+  u32x4 v[R / 8];
+  // off: byte offset of this lane's row in each eight rows; k: first element; end: of the wave's part of K
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t buffer, const uint32_t (&off)[R / 8], int k, int end,
+                                       int lane) {
+    const int at = k + (lane & 7) * 8;
+    const bool ok = at < end;
+#pragma unroll
+    for (int i = 0; i < R / 8; ++i)
+      v[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(buffer, ok ? off[i] + at * 2 : kNowhere, 0, AUX));
+  }
+  __device__ __forceinline__ void store(unsigned char* lds, int lane) const {
+#pragma unroll
+    for (int i = 0; i < R / 8; ++i) {
+      const int r = i * 8 + (lane >> 3);
+      *reinterpret_cast<u32x4*>(lds + r * 128 + (((lane & 7) ^ op_swz(r)) << 4)) = v[i];
+    }
+  }
+};
+
+template <class F>
+__device__ __forceinline__ F fragment(const unsigned char* lds, int r, int c) {
+  return *reinterpret_cast<const F*>(lds + r * 128 + ((c ^ op_swz(r)) << 4));
+}
+
+template <class E, bool GLU, int MB, int NB, int S, int PR>
+__global__ __launch_bounds__(kThreads, 2) void slim_kernel(Gemm16Args p) {
+  using F = typename E::frag;
+  constexpr int TM = 16 * MB, TN = GLU ? 8 * NB : 16 * NB;   // rows and columns of out in a tile
+  constexpr int kStage = (MB + NB) * 2048 > MB * NB * 1024 ? (MB + NB) * 2048 : MB * NB * 1024;
+  __shared__ __attribute__((aligned(16))) unsigned char stage[kWaves][kStage];
+  __shared__ int first[kMaxGroups + 1];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, g16 = lane >> 4, r16 = lane & 15;
+  const int cols = GLU ? p.N / 2 : p.N, nt = (cols + TN - 1) / TN;
+  list_tiles(p.groups, TM, first);
+  const int tm = blockIdx.x / nt, n0 = (blockIdx.x - tm * nt) * TN;
+  if (tm >= first[p.groups.n]) return;
+  const int g = tile_group(first, p.groups.n, tm);
+  const int m0 = p.groups.at(g) + (tm - first[g]) * TM, mv = min(TM, p.groups.at(g + 1) - m0);
+
+  // this wave's part of K, whole lines
+  const int each = (p.K + kWaves * 64 - 1) / (kWaves * 64) * 64;
+  const int k0 = min(p.K, wave * each), end = min(p.K, k0 + each);
+  const __amdgpu_buffer_rsrc_t pb = buffer_at(p.p + (size_t)m0 * p.K), qb = buffer_at(p.q + ((size_t)g * p.N + n0) * p.K);
+  uint32_t po[PR / 8], qo[2 * NB];
+#pragma unroll
+  for (int i = 0; i < PR / 8; ++i) {
+    const int r = i * 8 + (lane >> 3);
+    po[i] = r < mv ? (uint32_t)r * p.K * 2 : kNowhere;
+  }
+#pragma unroll
+  for (int i = 0; i < 2 * NB; ++i) {
+    // GLU: fragment rows 0..7 are gate rows, 8..15 the same columns' up rows
+    const int r = GLU ? (i >> 1) * 8 + (lane >> 3) : i * 8 + (lane >> 3);
+    qo[i] = n0 + r < cols ? (uint32_t)(r + (GLU && (i & 1) ? cols : 0)) * p.K * 2 : kNowhere;
+  }
+  v4f acc[MB][NB];
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  // S blocks of 64 k in flight in registers.  A block that has arrived goes
+  // through the wave's own LDS into fragments, and its registers take the block
+  // S ahead (past the end: nothing).  No other wave is waited for.
+  unsigned char* lp = stage[wave];
+  unsigned char* lq = lp + MB * 2048;
+  Lines<PR, 0> pl[S];
+  Lines<16 * NB, MB == 1 ? kNonTemporal : 0> ql[S];
+#pragma unroll
+  for (int b = 0; b < S; ++b) {
+    ql[b].load(qb, qo, k0 + b * 64, end, lane);
+    pl[b].load(pb, po, k0 + b * 64, end, lane);
+  }
+  for (int k = k0; k < end; k += 64 * S) {
+#pragma unroll
+    for (int b = 0; b < S; ++b) {
+      ql[b].store(lq, lane);
+      pl[b].store(lp, lane);
+      ql[b].load(qb, qo, k + (S + b) * 64, end, lane);
+      pl[b].load(pb, po, k + (S + b) * 64, end, lane);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        F pf[MB], qf[NB];
+#pragma unroll
+        for (int i = 0; i < MB; ++i) pf[i] = fragment<F>(lp, (i * 16 + r16) & (PR - 1), s * 4 + g16);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) qf[j] = fragment<F>(lq, j * 16 + r16, s * 4 + g16);
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+          for (int j = 0; j < NB; ++j) acc[i][j] = E::mfma(qf[j], pf[i], acc[i][j]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  __syncthreads();   // the stages become the sums' place
+  v4f (*part)[MB * NB][64] = reinterpret_cast<v4f (*)[MB * NB][64]>(&stage[0][0]);
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) part[wave][i * NB + j][lane] = acc[i][j];
+  __syncthreads();
+  uint16_t* out = static_cast<uint16_t*>(p.out);
+  for (int f = wave; f < MB * NB; f += kWaves) {
+    const int i = f / NB, j = f % NB;
+    v4f z = part[0][f][lane];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) z += part[w][f][lane];
+    // row r, four columns of z from zn on (lanes of g16 >= 2: up columns), of out from n on
+    const int r = i * 16 + r16;
+    const int n = n0 + (GLU ? j * 8 + (g16 & 1) * 4 : j * 16 + g16 * 4), zn = n + (GLU && g16 >= 2 ? cols : 0);
+    const bool ok = r < mv && n < cols;
+    const size_t m = m0 + r;
+    if (ok) {
+      if (p.bias) {
+        const u32x2 v = *reinterpret_cast<const u32x2*>(p.bias + (size_t)g * p.N + zn);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[e] += unpack<E>(v[e / 2], e & 1);
+      }
+      if (p.pre)
+        *reinterpret_cast<u32x2*>(p.pre + m * p.N + zn) = u32x2{pack2<E>(z[0], z[1]), pack2<E>(z[2], z[3])};
+    }
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = GLU ? glu_value(z[e], __shfl_xor(z[e], 32)) : z[e];
+    if (!GLU) activate(p.act, v);
+    if (ok && !(GLU && g16 >= 2)) {
+      if (p.residual) {
+        const u32x2 t = *reinterpret_cast<const u32x2*>(p.residual + m * cols + n);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += unpack<E>(t[e / 2], e & 1);
+      }
+      *reinterpret_cast<u32x2*>(out + m * cols + n) = u32x2{pack2<E>(v[0], v[1]), pack2<E>(v[2], v[3])};
+    }
+  }
+}
+
+template <class E, int MB, int NB, int S, int PR = 16 * MB>
+void run(const Gemm16Args& p, hipStream_t stream) {
+  const bool glu = p.act == kActSwiglu;
+  const int cols = glu ? p.N / 2 : p.N, tn = (glu ? 8 : 16) * NB;
+  const unsigned grid = (unsigned)((p.groups.rows / (16 * MB) + p.groups.n) * ((cols + tn - 1) / tn));
+  if (glu) hipLaunchKernelGGL((slim_kernel<E, true, MB, NB, S, PR>), dim3(grid), dim3(kThreads), 0, stream, p);
+  else hipLaunchKernelGGL((slim_kernel<E, false, MB, NB, S, PR>), dim3(grid), dim3(kThreads), 0, stream, p);
+}
+
+// Workgroups of tiles of 16 MB rows and 16 NB weight rows, about: a row tile
+// more for every group that has rows.
+long slim_tiles(const Gemm16Args& p, int mb, int nb) {
+  const int cols = p.act == kActSwiglu ? p.N / 2 : p.N, tn = (p.act == kActSwiglu ? 8 : 16) * nb;
+  const long rows = p.groups.rows, live = std::min<long>(p.groups.n, rows);
+  const long m = live <= 1 ? (rows + 16 * mb - 1) / (16 * mb) : rows / (16 * mb) + live;
+  return m * ((cols + tn - 1) / tn);
+}
+
+// Row tiles are counted with one more for every group that has rows, so rows
+// per group decide between streaming a group's weights past few rows (MB = 1)
+// and larger tiles.
+long average_rows(const Gemm16Args& p) { return (p.groups.rows + p.groups.n - 1) / p.groups.n; }
+
+template <class E>
+void launch_slim(const Gemm16Args& p, hipStream_t stream) {
+  const long avg = average_rows(p);
+  if (avg <= 8) return run<E, 1, 1, 2, 8>(p, stream);
+  if (avg <= 16) return run<E, 1, 1, 2>(p, stream);
+  // Each tile's cost: rounds of 256 workgroups by a round's time relative to a
+  // 2 x 2 tile's (a smaller tile loads its operands more often, a larger one
+  // leaves CUs idle).  128 rows, K 7168, N 4096 take 44, 32, 27 and 37 us as 2 x 1,
+  // 2 x 2, 2 x 4 and 4 x 4; 333 x 1000 x 1016 11.5, 8.6, 8.0 and 11.1.
+  struct { int mb, nb; float time; } const tiles[] = {{2, 1, 0.9f}, {2, 2, 1.0f}, {2, 4, 1.3f}, {4, 2, 1.3f}, {4, 4, 1.75f}};
+  int best = 0;
+  float least = INFINITY;
+  for (int i = 0; i < 5; ++i) {
+    const float cost = (float)((slim_tiles(p, tiles[i].mb, tiles[i].nb) + 255) / 256) * tiles[i].time;
+    if (cost < least) {
+      least = cost;
+      best = i;
+    }
+  }
+  if (best == 0) run<E, 2, 1, 2>(p, stream);
+  else if (best == 1) run<E, 2, 2, 1>(p, stream);
+  else if (best == 2) run<E, 2, 4, 1>(p, stream);
+  else if (best == 3) run<E, 4, 2, 1>(p, stream);
+  else run<E, 4, 4, 1>(p, stream);
+}
+
+}  // namespace
+
+// Up to two rounds of 4 x 4 tiles (512 rows, K 4096, N 4096: 39 us against 55 of
+// the tile kernel; 1024 rows, four rounds: 73 against 54), and few rows a group
+// at any size (128 rows in 64 groups, K 7168, N 4096: 425 against 540; 512 rows in
+// 33 groups, K 1024, N 2048: 53 against 30).
+bool gemm16_slim(const Gemm16Args& p) {
+  if ((size_t)p.N * p.K * 2 > 0x7F000000u) return false;   // a group's matrix within one buffer's bounds
+  return average_rows(p) <= (p.groups.n == 1 ? 16 : 6) || slim_tiles(p, 4, 4) <= 512;
+}
+
+hipError_t launch_gemm16_slim(int type, const Gemm16Args& p, hipStream_t stream) {
+  if (type == 0) launch_slim<Bf16>(p, stream);
+  else launch_slim<Fp16>(p, stream);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -173,6 +173,23 @@ def test_larger(rows, K, N, sizes):
     p.check_backward()
 
 
+# products with enough tiles for the kernel's large ones, their rows, columns and K cut off anywhere; sums split into parts
+@pytest.mark.parametrize("ty", TYPES)
+@pytest.mark.parametrize("rows,K,N,sizes", [(4000, 72, 4040, None), (3990, 200, 4048, [300, 0, 3500, 64, 101, 20])])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_large_tiles_forward(ty, rows, K, N, sizes, act):
+    N = 2 * N if act == "swiglu" else N
+    Product(TYPES[ty], rows, K, N, sizes, bias=True, residual=N // 2 if act == "swiglu" else N).check_forward(act)
+
+
+@pytest.mark.parametrize("ty", TYPES)
+@pytest.mark.parametrize("rows,K,N,sizes", [(4000, 4040, 72, None), (3990, 4048, 136, [300, 0, 3500, 64, 101, 20]),
+                                            (72, 4040, 4000, None), (1, 4096, 4088, None), (5000, 264, 520, None),
+                                            (3000, 136, 2056, None), (2000, 1032, 4104, [1500, 0, 490, 10])])
+def test_large_tiles_and_parts_backward(ty, rows, K, N, sizes):
+    Product(TYPES[ty], rows, K, N, sizes).check_backward()
+
+
 @pytest.mark.parametrize("rows,sizes", [(3, [1, 1, 1]), (400, [130, 140, 130]), (40, [13, 14, 13])])
 def test_nan_and_infinities_stay_in_their_rows(rows, sizes):
     """Rows, groups and memory behind the last row that hold NaN and infinities reach no other row's results."""
