@@ -141,9 +141,8 @@ struct Operand {
 // kDgradPart, kWgradPart: the sum over a part of k, FP32, into the workspace.
 enum Kind { kForward = 0, kForwardGlu = 1, kDgrad = 2, kWgrad = 3, kDgradPart = 4, kWgradPart = 5 };
 
-// Waits until at most n of the wave's vector memory operations are outstanding
-// and its LDS operations are done, then for the other waves.  n is uniform and
-// one of a few.
+// Waits until at most N of the wave's vector memory operations are outstanding
+// (they end in their order) and all of its LDS operations are done.
 template <int N>
 __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));
@@ -155,17 +154,15 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void gemm16_kernel(Gemm16Args p) {
   constexpr int NW = WM * WN, MS = BM / WM / 16, NS = BN / WN / 16;
   constexpr bool GLU = KIND == kForwardGlu, WGRAD = KIND == kWgrad || KIND == kWgradPart;
   constexpr bool DGRAD = KIND == kDgrad || KIND == kDgradPart, PART = KIND == kDgradPart || KIND == kWgradPart;
-  constexpr bool F32 = WGRAD || PART;   // out is FP32, stored from registers
+  constexpr bool F32 = WGRAD || PART;   // out is FP32
   using F = typename E::frag;
   using P = Operand<BM, WGRAD, NW>;
   using Q = Operand<BN, DGRAD || WGRAD, NW>;
-  constexpr int LOADS = P::kLoads + Q::kLoads;
   __shared__ __attribute__((aligned(1024))) unsigned char sm[2 * (P::kBytes + Q::kBytes)];   // two blocks of P, two of Q
   __shared__ int first[WGRAD ? 1 : kMaxGroups + 1];
 
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int wm = wave / WN, wn = wave % WN;
-  const int g16 = lane >> 4, r16 = lane & 15;
   const int cols = GLU ? p.N / 2 : p.N;            // columns of out
   constexpr int TN = GLU ? BN / 2 : BN;            // columns of out in a tile
   const int nt = (cols + TN - 1) / TN, mt = (p.M + BM - 1) / BM;
@@ -259,17 +256,13 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void gemm16_kernel(Gemm16Args p) {
     ql.advance();
     qleft -= BK;
   };
-  // What is loaded of the next tile while this one's results are stored: two
-  // blocks, or one where the other's place holds results on their way.
-  constexpr int EARLY = F32 ? 2 : 1;
-  constexpr int STORES = F32 ? MS * NS : 0;   // of a tile, each wave
+  // The first block is loaded while the tile before it is stored.
+  constexpr int STORES = F32 ? MS * NS : 0;   // of a tile, each wave, behind that load
   auto early = [&](const Tile& t) {
-#pragma unroll
-    for (int kb = 0; kb < EARLY; ++kb)
-      if (kb * BK < t.k) {
-        refill_p(kb);
-        refill_q(kb);
-      }
+    if (t.k > 0) {
+      refill_p(0);
+      refill_q(0);
+    }
   };
 
   // Workgroup b runs on XCD b % 8 and takes tiles of its XCD's contiguous eighth
@@ -308,17 +301,10 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void gemm16_kernel(Gemm16Args p) {
       barrier();
       if (kb + 2 < KB) refill_p(kb);
     };
-    // the next block has landed: all but what was issued after it (its own n-side
-    // refill comes first; then stores, if they stand between)
+    // the next block has landed: all but the m-side refill that was issued after it
     auto next_landed = [&](int kb) {
-      const bool after_stores = STORES > 0 && kb == 0 && stored;
-      if (kb + 2 < KB) {
-        if (after_stores) wait_vm<P::kLoads + STORES>();
-        else wait_vm<P::kLoads>();
-      } else {
-        if (after_stores) wait_vm<STORES>();
-        else wait_vm<0>();
-      }
+      if (kb + 2 < KB) wait_vm<P::kLoads>();
+      else wait_vm<0>();
       barrier();
     };
     auto step = [&](int kb, int s, bool more) {
@@ -343,16 +329,10 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void gemm16_kernel(Gemm16Args p) {
       }
     };
     if (KB > 0) {
-      // block 0
-      if (!F32 || !stored) {
-        if (EARLY > 1 && KB > 1) wait_vm<LOADS>();
-        else wait_vm<0>();
-      } else {
-        if (KB > 1) wait_vm<LOADS + STORES>();
-        else wait_vm<STORES>();
-      }
+      if (F32 && stored) wait_vm<STORES>();   // block 0
+      else wait_vm<0>();
       barrier();
-      if (EARLY == 1 && KB > 1) {
+      if (KB > 1) {
         refill_p(1);
         refill_q(1);
       }
@@ -389,56 +369,61 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void gemm16_kernel(Gemm16Args p) {
     }
 
     // ---- epilogue: lane (g16, r16) holds row ms*16 + r16, columns ns*16 + 4*g16 .. +3 ----
+    // Sixteen rows at a time go through the wave's part of the second block's
+    // place, whose rows are then read in whole chunks.  Its addresses are made
+    // anew for every tile (`el` hides that they are the same): kept in registers
+    // over the sums they would be spilled, and reloading them would wait for the
+    // stores before.
+    int el = lane;
+    asm volatile("" : "+v"(el));
+    const int er16 = el & 15, eg16 = el >> 4;
+    constexpr int kPart = 16 * NS * 64;
+    static_assert(NW * kPart <= P::kBytes + Q::kBytes && P::kBytes % kPart == 0, "parts fit");
+    const int part_at = wave * kPart;
+    unsigned char* ep = sm + (part_at < P::kBytes ? P::kBytes + part_at : P::kBytes + Q::kBytes + part_at);
+    auto stage = [&](const v4f (&row)[NS]) {
+#pragma unroll
+      for (int ns = 0; ns < NS; ++ns)
+        *reinterpret_cast<v4f*>(ep + er16 * (NS * 64) + (((ns * 4 + eg16) ^ (er16 & 7)) << 4)) = row[ns];
+    };
+    auto staged = [&](int r, int c) { return *reinterpret_cast<const v4f*>(ep + r * (NS * 64) + ((c ^ (r & 7)) << 4)); };
     if constexpr (F32) {
-      // From registers, every wave the same number of stores (rows and columns
-      // past the end are out of the buffer's bounds, which drops them), so that
-      // the next tile's waits can count over them.
+      // Every wave makes the same number of stores (rows and columns past the end
+      // are out of the buffer's bounds, which drops them), so that the wait for the
+      // next tile's first block can leave them in flight.  Rows of 512 bytes a
+      // store, past the caches: 1.9 GB of gradients (8192 rows in 32 groups, 7168 x
+      // 2048) take 665 us against 745 with 128-byte rows from registers and 770
+      // through the caches.
       const size_t row0 = WGRAD ? ((size_t)done.part * p.groups.n + done.g) * p.M : (size_t)done.part * p.groups.rows;
       const uint64_t base = reinterpret_cast<uint64_t>(static_cast<float*>(p.out) + (row0 + done.m0) * p.N);
       const __amdgpu_buffer_rsrc_t buffer = __builtin_amdgcn_make_buffer_rsrc(
           const_cast<void*>(uniform_ptr(reinterpret_cast<const void*>(base))), 0,
           __builtin_amdgcn_readfirstlane((uint32_t)min((int64_t)done.mv * p.N * 4, (int64_t)0x7FFFFFE0)), 0x00020000);
-      // A store is eight rows of 128 bytes: lanes eight apart trade sub-tiles, so
-      // that a row's two 64-byte parts come together.  (Rows of 64 bytes a store:
-      // 3.5 TB/s of gradients instead of 5.)
-      auto put = [&](int r, int c, const float (&v)[4]) {
-        const u32x4 w{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
-        constexpr int kNonTemporal = 2;
-        __builtin_amdgcn_raw_buffer_store_b128(w, buffer, c < p.N ? (uint32_t)(r * (int64_t)p.N + c) * 4 : kNowhere, 0,
-                                               kNonTemporal);
-      };
+      constexpr int CH = NS * 4, IT = 16 * CH / 64;   // 16-byte chunks of a row; a lane's of sixteen rows
+      constexpr int kNonTemporal = 2;
 #pragma unroll
-      for (int ms = 0; ms < MS; ++ms) {
-        const int r = wm * MS * 16 + ms * 16 + (r16 & 7);
+      for (int pass = 0; pass < MS; ++pass) {
+        stage(acc[pass]);
+        __builtin_amdgcn_wave_barrier();   // the wave's LDS operations are in order
 #pragma unroll
-        for (int ns = 0; ns < NS; ns += 2) {
-          const int c = done.n0 + (wn * NS + ns + (r16 >> 3)) * 16 + 4 * g16;
-          float lo[4], hi8[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            constexpr int ROW_ROR8 = 0x128;
-            const int x = __float_as_int(acc[ms][ns][e]), y = __float_as_int(acc[ms][ns + 1][e]);
-            lo[e] = __int_as_float(__builtin_amdgcn_update_dpp(x, y, ROW_ROR8, 0xF, 0xC, false));
-            hi8[e] = __int_as_float(__builtin_amdgcn_update_dpp(y, x, ROW_ROR8, 0xF, 0x3, false));
-          }
-          put(r, c, lo);
-          put(r + 8, c, hi8);
+        for (int i = 0; i < IT; ++i) {
+          const int r = (i * 64 + el) / CH, c = el % CH, n = done.n0 + wn * NS * 16 + c * 4;
+          const uint32_t at = (uint32_t)((wm * MS * 16 + pass * 16 + r) * (int64_t)p.N + n) * 4;
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, staged(r, c)), buffer, n < p.N ? at : kNowhere,
+                                                 0, kNonTemporal);
         }
       }
       stored = true;
     } else {
-      // Sixteen rows at a time go through the wave's part of the second block's
-      // place, so that what follows is one short loop over whole chunks of rows:
-      // code that runs once a tile is fetched at some 0.1 us per 128 bytes, and an
-      // activation spelled out for every register took 70 us a tile.  What is
-      // loaded here (bias, residual) is loaded a pass ahead.
+      // What follows is one short loop: code that runs once a tile is fetched at
+      // some 0.1 us per 128 bytes, and an activation spelled out for every register
+      // of a tile was 140 KB of it.  What is loaded here (bias, residual) is loaded a pass
+      // ahead.
       using V8 = Values<E, true>;
       constexpr int CH = GLU ? NS : 2 * NS;   // 16-byte chunks of a row of out
       constexpr int IT = 16 * CH / 64;
       static_assert(IT * 64 == 16 * CH && 64 % CH == 0, "a lane keeps its columns");
-      constexpr int kPart = 16 * NS * 64;      // bytes of sixteen rows of the wave's columns
-      static_assert(NW * kPart <= P::kBytes + Q::kBytes && P::kBytes % kPart == 0, "parts fit");
-      const int er = lane / CH, ec = lane % CH;
+      const int er = el / CH, ec = el % CH;
       const int n = done.n0 + (wn * CH + ec) * 8;
       const bool nok = n < cols;
       u32x4 bg{}, bu{}, rv[IT];
@@ -453,19 +438,13 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void gemm16_kernel(Gemm16Args p) {
       }
 #pragma unroll
       for (int i = 0; i < IT; ++i) fetch(0, i);
-      const int at = wave * kPart;
-      unsigned char* ep = sm + (at < P::kBytes ? P::kBytes + at : 2 * P::kBytes + Q::kBytes + at - P::kBytes);
-      auto chunk16 = [&](int r, int c) { return *reinterpret_cast<const v4f*>(ep + r * (NS * 64) + ((c ^ (r & 7)) << 4)); };
       if (wm * MS * 16 < done.mv)
 #pragma unroll 1
       for (int pass = 0; pass < MS; ++pass) {
 #pragma unroll
         for (int ms = 0; ms < MS; ++ms)
-          if (pass == ms)
-#pragma unroll
-            for (int ns = 0; ns < NS; ++ns)
-              *reinterpret_cast<v4f*>(ep + r16 * (NS * 64) + (((ns * 4 + g16) ^ (r16 & 7)) << 4)) = acc[ms][ns];
-        __builtin_amdgcn_wave_barrier();   // the wave's LDS operations are in order
+          if (pass == ms) stage(acc[ms]);
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
           const int r = er + i * (64 / CH), tr = wm * MS * 16 + pass * 16 + r;
@@ -473,7 +452,7 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void gemm16_kernel(Gemm16Args p) {
           const size_t m = (size_t)done.m0 + tr;
           auto z8 = [&](int c) {
             V8 z;
-            const v4f a = chunk16(r, c), b = chunk16(r, c + 1);
+            const v4f a = staged(r, c), b = staged(r, c + 1);
 #pragma unroll
             for (int e = 0; e < 4; ++e) z.v[e] = a[e], z.v[4 + e] = b[e];
             return z;
