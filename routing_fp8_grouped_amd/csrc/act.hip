@@ -18,6 +18,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / 64, kCols = 512;
+constexpr int U = 4;   // rows in flight a wave
 
 // Rows of a chunk: 64, fewer while the launch would not fill the chip.
 int chunk_rows(int rows, int N) {
@@ -51,30 +52,42 @@ __global__ __launch_bounds__(kThreads) void act_backward_kernel(ActArgs p) {
   const int col = blockIdx.y * kCols + lane * 8;
   Val sg, su;
   if (col < width) {
-#pragma unroll 4
-    for (int r = r0 + wave; r < r1; r += kWaves) {
-      const Val d(load_chunk(p.dout + (size_t)r * width + col));
-      Val z, u;
-      if (ACT != kActNone) z = Val(load_chunk(p.pre + (size_t)r * p.N + col));
-      if (GLU) u = Val(load_chunk(p.pre + (size_t)r * p.N + width + col));
-      Val og, ou;
+    // U rows' loads before the first is used; rows past the chunk's end repeat its last one and are dropped
+    for (int r = r0 + wave; r < r1; r += U * kWaves) {
+      u32x4 dr[U], zr[U], ur[U];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if constexpr (GLU) {
-          const float e = sigmoid_f32(z.v[i]);
-          og.v[i] = d.v[i] * u.v[i] * (e * fmaf(z.v[i], 1.0f - e, 1.0f));
-          ou.v[i] = d.v[i] * (z.v[i] * e);
-          su.v[i] += ou.v[i];
-        } else if constexpr (ACT == kActRelu) {
-          og.v[i] = z.v[i] > 0.0f ? d.v[i] : 0.0f;
-        } else {
-          og.v[i] = d.v[i] * act_slope<ACT>(z.v[i]);
-        }
-        sg.v[i] += og.v[i];
+      for (int k = 0; k < U; ++k) {
+        const size_t m = min(r + k * kWaves, r1 - 1);
+        dr[k] = load_chunk(p.dout + m * width + col);
+        if (ACT != kActNone) zr[k] = load_chunk(p.pre + m * p.N + col);
+        if (GLU) ur[k] = load_chunk(p.pre + m * p.N + width + col);
       }
-      if (p.dz) {
-        og.put(p.dz + (size_t)r * p.N + col);
-        if (GLU) ou.put(p.dz + (size_t)r * p.N + width + col);
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int m = r + k * kWaves;
+        if (m >= r1) break;
+        const Val d(dr[k]);
+        Val og, ou, z, u;
+        if (ACT != kActNone) z = Val(zr[k]);
+        if (GLU) u = Val(ur[k]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if constexpr (GLU) {
+            const float e = sigmoid_f32(z.v[i]), v = z.v[i] * e;
+            og.v[i] = d.v[i] * u.v[i] * fmaf(v, 1.0f - e, e);
+            ou.v[i] = d.v[i] * v;
+            su.v[i] += ou.v[i];
+          } else if constexpr (ACT == kActRelu) {
+            og.v[i] = z.v[i] > 0.0f ? d.v[i] : 0.0f;
+          } else {
+            og.v[i] = d.v[i] * act_slope<ACT>(z.v[i]);
+          }
+          sg.v[i] += og.v[i];
+        }
+        if (p.dz) {
+          og.put(p.dz + (size_t)m * p.N + col);
+          if (GLU) ou.put(p.dz + (size_t)m * p.N + width + col);
+        }
       }
     }
   }

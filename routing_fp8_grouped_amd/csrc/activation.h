@@ -7,9 +7,12 @@ namespace moe {
 
 enum Act { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActSwiglu = 4 };
 
+// e^z by the hardware's 2^x; results below 2^-126 are 0.
+__device__ __forceinline__ float exp_f32(float z) { return __builtin_amdgcn_exp2f(1.44269504088896341f * z); }
+
 // By the hardware's 2^x and reciprocal (an ulp each): within (4 + |z|) 2^-23 of
 // the exact value, where what it goes into is rounded to 16 bits.
-__device__ __forceinline__ float sigmoid_f32(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
+__device__ __forceinline__ float sigmoid_f32(float z) { return __builtin_amdgcn_rcpf(1.0f + exp_f32(-z)); }
 
 // Phi(z), the normal distribution's: for t = |z|, Phi(-t) = e^(-t^2/2) g(t) with
 // g(t) = e^(t^2/2) erfc(t / sqrt 2) / 2 smooth and falling, so a polynomial of
@@ -29,7 +32,7 @@ __device__ __forceinline__ float normal_cdf(float z) {
   p = fmaf(p, u, 8.5762918e-2f);
   p = fmaf(p, u, 9.23784599e-2f);
   p = fmaf(p, u, -2.7762424e-5f);
-  const float q = p * __expf(-0.5f * t * t);
+  const float q = p * exp_f32(-0.5f * t * t);
   return z < 0.0f ? q : 1.0f - q;
 }
 
@@ -52,7 +55,7 @@ __device__ __forceinline__ float act_slope(float z) {
     const float e = sigmoid_f32(z);
     return e * fmaf(z, 1.0f - e, 1.0f);
   } else if constexpr (ACT == kActGelu) {
-    return fmaf(z, 0.39894228040143268f * __expf(-0.5f * z * z), normal_cdf(z));
+    return fmaf(z, 0.39894228040143268f * exp_f32(-0.5f * z * z), normal_cdf(z));
   } else return 1.0f;
 }
 

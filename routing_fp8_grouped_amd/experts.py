@@ -56,53 +56,53 @@ def moe_sort(idx, n_experts, offsets, pos, row_slot, workspace=None, stream=None
           _size(workspace), _stream(stream, dev))
 
 
-def _copy(name, token, token_name, rows, rows_name, pos, specs):
-    """Checks what the four copies share; returns (type, T, k, d, rows, device)."""
-    _dims(pos, 2, "pos")
-    _dims(token, 2, token_name)
-    _dims(rows, 2, rows_name)
+def _sizes(token, token_name, rows, rows_name, pos):
+    """(T, k, d, number of rows, type, device) of a copy between the two orders."""
+    if pos.dim() != 2 or token.dim() != 2 or rows.dim() != 2:
+        raise ValueError(f"pos, {token_name} and {rows_name} must have two dimensions, got {tuple(pos.shape)}, "
+                         f"{tuple(token.shape)} and {tuple(rows.shape)}")
     T, k = pos.shape
     n, d = rows.shape
-    dev = _device(pos, "pos")
-    _check(dev, ((pos, "pos", _I32, None), (token, token_name, token.dtype, (T, d)),
-                 (rows, rows_name, token.dtype, None)) + specs(T, k, n, d, token.dtype))
-    return _type(token, token_name), T, k, d, n, dev
+    return T, k, d, n, token.dtype, _device(pos, "pos")
 
 
 def moe_dispatch(x, pos, rows, w=None, stream=None):
     """Tokens to their rows: rows[pos[t, j]] = w[t, j] * x[t] (ones without ``w``).  x [T, d] and rows [n, d] bfloat16,
     float16 or float32, pos [T, k] int32 (negative: dropped), w [T, k] float32.  Other rows are left as they were."""
-    ty, T, k, d, n, dev = _copy("moe_dispatch", x, "x", rows, "rows", pos,
-                                lambda T, k, n, d, dt: ((w, "w", _FP32, (T, k)),))
-    _call("moe_dispatch", ty, _ptr(x), _ptr(pos), _ptr(w), T, k, d, n, _ptr(rows), _stream(stream, dev))
+    T, k, d, n, dt, dev = _sizes(x, "x", rows, "rows", pos)
+    _check(dev, ((pos, "pos", _I32, None), (x, "x", dt, (T, d)), (rows, "rows", dt, None), (w, "w", _FP32, (T, k))))
+    _call("moe_dispatch", _type(x, "x"), _ptr(x), _ptr(pos), _ptr(w), T, k, d, n, _ptr(rows), _stream(stream, dev))
 
 
 def moe_dispatch_backward(drows, pos, dx, w=None, x=None, dw=None, residual=None, stream=None):
     """dx[t] = sum_j w[t, j] * drows[pos[t, j]] (+ residual[t], whose memory dx may be); with the forward's ``x`` also
     dw [T, k] float32, the gradient of ``w``."""
-    ty, T, k, d, n, dev = _copy("moe_dispatch_backward", dx, "dx", drows, "drows", pos,
-                                lambda T, k, n, d, dt: ((w, "w", _FP32, (T, k)), (x, "x", dt, (T, d)),
-                                                        (dw, "dw", _FP32, (T, k)),
-                                                        (residual, "residual", dt, (T, d))))
-    _call("moe_dispatch_backward", ty, _ptr(drows), _ptr(pos), _ptr(w), _ptr(x), _ptr(residual), T, k, d, n, _ptr(dx),
-          _ptr(dw), _stream(stream, dev))
+    T, k, d, n, dt, dev = _sizes(dx, "dx", drows, "drows", pos)
+    token = (T, d)
+    _check(dev, ((pos, "pos", _I32, None), (dx, "dx", dt, token), (drows, "drows", dt, None), (w, "w", _FP32, (T, k)),
+                 (x, "x", dt, token), (dw, "dw", _FP32, (T, k)), (residual, "residual", dt, token)))
+    _call("moe_dispatch_backward", _type(dx, "dx"), _ptr(drows), _ptr(pos), _ptr(w), _ptr(x), _ptr(residual), T, k, d, n,
+          _ptr(dx), _ptr(dw), _stream(stream, dev))
 
 
 def moe_collect(y, pos, out, w=None, residual=None, stream=None):
     """Rows back to their tokens: out[t] = sum_j w[t, j] * y[pos[t, j]] (+ residual[t], whose memory out may be)."""
-    ty, T, k, d, n, dev = _copy("moe_collect", out, "out", y, "y", pos,
-                                lambda T, k, n, d, dt: ((w, "w", _FP32, (T, k)), (residual, "residual", dt, (T, d))))
-    _call("moe_collect", ty, _ptr(y), _ptr(pos), _ptr(w), _ptr(residual), T, k, d, n, _ptr(out), _stream(stream, dev))
+    T, k, d, n, dt, dev = _sizes(out, "out", y, "y", pos)
+    token = (T, d)
+    _check(dev, ((pos, "pos", _I32, None), (out, "out", dt, token), (y, "y", dt, None), (w, "w", _FP32, (T, k)),
+                 (residual, "residual", dt, token)))
+    _call("moe_collect", _type(out, "out"), _ptr(y), _ptr(pos), _ptr(w), _ptr(residual), T, k, d, n, _ptr(out),
+          _stream(stream, dev))
 
 
 def moe_collect_backward(dout, pos, dy, w=None, y=None, dw=None, stream=None):
     """dy[pos[t, j]] = w[t, j] * dout[t] (other rows are left; dy may be y's memory); with the forward's ``y`` also dw
     [T, k] float32, the gradient of ``w``."""
-    ty, T, k, d, n, dev = _copy("moe_collect_backward", dout, "dout", dy, "dy", pos,
-                                lambda T, k, n, d, dt: ((w, "w", _FP32, (T, k)), (y, "y", dt, (n, d)),
-                                                        (dw, "dw", _FP32, (T, k))))
-    _call("moe_collect_backward", ty, _ptr(dout), _ptr(pos), _ptr(w), _ptr(y), T, k, d, n, _ptr(dy), _ptr(dw),
-          _stream(stream, dev))
+    T, k, d, n, dt, dev = _sizes(dout, "dout", dy, "dy", pos)
+    _check(dev, ((pos, "pos", _I32, None), (dout, "dout", dt, (T, d)), (dy, "dy", dt, None), (w, "w", _FP32, (T, k)),
+                 (y, "y", dt, (n, d)), (dw, "dw", _FP32, (T, k))))
+    _call("moe_collect_backward", _type(dout, "dout"), _ptr(dout), _ptr(pos), _ptr(w), _ptr(y), T, k, d, n, _ptr(dy),
+          _ptr(dw), _stream(stream, dev))
 
 
 # ---- matrix products in 16 bits ----
