@@ -52,6 +52,7 @@ __device__ __forceinline__ F fragment(const unsigned char* lds, int r, int c) {
   return *reinterpret_cast<const F*>(lds + r * 128 + ((c ^ op_swz(r)) << 4));
 }
 
+// PR: rows of a that are loaded, 16 MB or, where no tile has more, 8.
 template <class E, bool GLU, int MB, int NB, int S, int PR>
 __global__ __launch_bounds__(kThreads, 2) void slim_kernel(Gemm16Args p) {
   using F = typename E::frag;
@@ -191,7 +192,7 @@ long average_rows(const Gemm16Args& p) { return (p.groups.rows + p.groups.n - 1)
 template <class E>
 void launch_slim(const Gemm16Args& p, hipStream_t stream) {
   const long avg = average_rows(p);
-  if (avg <= 8) return run<E, 1, 1, 2, 8>(p, stream);
+  if (p.groups.rows <= 8) return run<E, 1, 1, 2, 8>(p, stream);   // no tile has more
   if (avg <= 16) return run<E, 1, 1, 2>(p, stream);
   // Each tile's cost: rounds of 256 workgroups by a round's time relative to a
   // 2 x 2 tile's (a smaller tile loads its operands more often, a larger one

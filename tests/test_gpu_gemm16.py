@@ -149,6 +149,13 @@ def test_forward_grouped(ty, act, sizes, behind):
         Product(TYPES[ty], rows, 200, 304, sizes, bias=True).check_forward(act)
 
 
+# few rows a group on average, but more than 8 or 16 in one of them
+@pytest.mark.parametrize("sizes", [[0] * 5 + [12] + [1] * 4, [3] * 7 + [17, 0], [9] + [0] * 11, [0, 40] + [0] * 30 + [2]], ids=str)
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_forward_few_uneven(sizes, act):
+    Product(torch.bfloat16, sum(sizes) + 1, 520, 272, sizes, bias=True).check_forward(act)
+
+
 @pytest.mark.parametrize("ty", TYPES)
 @pytest.mark.parametrize("rows,K,N", SHAPES)
 def test_backward(ty, rows, K, N):
@@ -185,9 +192,38 @@ def test_large_tiles_forward(ty, rows, K, N, sizes, act):
 @pytest.mark.parametrize("ty", TYPES)
 @pytest.mark.parametrize("rows,K,N,sizes", [(4000, 4040, 72, None), (3990, 4048, 136, [300, 0, 3500, 64, 101, 20]),
                                             (72, 4040, 4000, None), (1, 4096, 4088, None), (5000, 264, 520, None),
-                                            (3000, 136, 2056, None), (2000, 1032, 4104, [1500, 0, 490, 10])])
+                                            (3000, 136, 2056, None), (2000, 1032, 4104, [1500, 0, 490, 10]),
+                                            (300, 1496, 1504, [0, 5, 64, 65, 0, 130, 36]), (40, 5376, 5120, None),
+                                            (200, 5120, 5384, None)])
 def test_large_tiles_and_parts_backward(ty, rows, K, N, sizes):
     Product(TYPES[ty], rows, K, N, sizes).check_backward()
+
+
+def test_operands_beyond_4_gib():
+    """Rows on both sides of 2^32 bytes, of the operands and of the results."""
+    rows, K, N = 280000, 8192, 16
+    at = torch.tensor([0, 1, 262143, 262144, 262145, rows - 1], device=DEV)     # 2^32 bytes are 262144 rows
+    a, b = torch.zeros(rows, K, dtype=torch.bfloat16, device=DEV), torch.randn(1, N, K, device=DEV).bfloat16()
+    a[at] = torch.randn(len(at), K, device=DEV).bfloat16()
+    out = torch.empty(rows, N, dtype=torch.bfloat16, device=DEV)
+    moe.grouped_gemm16(a, b, out)
+    z, mag = ox.gemm(np64(a[at]), np64(b), None, None)
+    assert np.all(np.abs(np64(out[at]) - z) <= rounded(torch.bfloat16, z, steps(K) * U * mag))
+    rest = torch.ones(rows, dtype=torch.bool, device=DEV)
+    rest[at] = False
+    assert not out[rest].any()
+    ws = lambda: torch.empty(max(16, moe.grouped_gemm16_backward_workspace_bytes(rows, 1, K, N)), dtype=torch.uint8, device=DEV)
+    db = torch.empty(1, N, K, device=DEV)
+    dz = torch.randn(rows, N, device=DEV).bfloat16()
+    moe.grouped_gemm16_wgrad(dz, a, db, ws())
+    ref, mag = ox.wgrad(np64(dz[at]), np64(a[at]), None, 1)
+    assert np.all(np.abs(np64(db) - ref) <= steps(rows) * U * mag + U * np.abs(ref))
+    moe.grouped_gemm16_dgrad(dz, b, a, ws())
+    ref, mag = ox.dgrad(np64(dz[at]), np64(b), None)
+    assert np.all(np.abs(np64(a[at]) - ref) <= rounded(torch.bfloat16, ref, steps(N) * U * mag))
+    before = a[at]
+    moe.grouped_act_backward(a, a, "relu", a)
+    assert torch.equal(a[at], before.clamp_min(0))
 
 
 @pytest.mark.parametrize("rows,sizes", [(3, [1, 1, 1]), (400, [130, 140, 130]), (40, [13, 14, 13])])

@@ -58,7 +58,7 @@ def indices(kind, T, k, E, seed):
 # one workgroup up to 4096 slots, blocks of 1024 and more beyond; experts of one pass and of several
 @pytest.mark.parametrize("kind", ["all", "dropped", "one", "none"])
 @pytest.mark.parametrize("T,k,E", [(1, 1, 1), (1, 8, 256), (5, 3, 7), (64, 8, 256), (512, 8, 33), (513, 8, 256),
-                                   (1000, 7, 1024), (4097, 64, 5), (16384, 8, 256), (300001, 1, 300), (3, 2, 2)])
+                                   (1000, 7, 1024), (4097, 64, 5), (16384, 8, 256), (300001, 1, 300), (3, 2, 2), (512, 8, 1024), (64, 3, 1023)])
 def test_sort(kind, T, k, E):
     idx = indices(kind, T, k, E, T + k)
     for got, ref in zip(run_sort(idx, E), ox.sort(idx, E)):
@@ -207,6 +207,22 @@ def test_without_rows():
     e = torch.empty(0, k, dtype=I32, device=DEV)
     moe.moe_dispatch(empty, e, none)
     moe.moe_collect(none, e, empty)
+
+
+def test_rows_beyond_4_gib():
+    T, k, d = 300000, 2, 4096
+    pos = torch.randperm(T * k, device=DEV).int().view(T, k)
+    pos[-1] = -1
+    x, w = torch.randn(T, d, device=DEV).half(), torch.rand(T, k, device=DEV)
+    rows = torch.zeros(T * k, d, dtype=torch.float16, device=DEV)
+    moe.moe_dispatch(x, pos, rows, w=w)
+    at = torch.cat([torch.arange(0, T - 1, 997, device=DEV), torch.arange(T - 9, T - 1, device=DEV)])
+    for j in range(k):
+        assert torch.equal(rows[pos[at, j].long()], (x[at].float() * w[at, j, None]).half())
+    out = torch.empty_like(x)
+    moe.moe_collect(rows, pos, out)
+    total = sum(rows[pos[at, j].long()].float() for j in range(k))
+    assert torch.equal(out[at], total.half()) and not out[-1].any()
 
 
 def test_gradients_are_differences():
