@@ -33,8 +33,11 @@ __device__ __forceinline__ void activate(int act, float (&z)[N]) {
   else if (act == kActGelu) each([](float v) { return act_value<kActGelu>(v); });
 }
 
-// The forward's product by gemm16_slim.hip, where it is the faster one.
+// The forward's product by gemm16_slim.hip: where it is faster than the tile
+// kernel, in particular with few rows (a group); its time in us, about.
+bool gemm16_few_rows(const Gemm16Args& p);
 bool gemm16_slim(const Gemm16Args& p);
+double gemm16_slim_time(const Gemm16Args& p);
 hipError_t launch_gemm16_slim(int type, const Gemm16Args& p, hipStream_t stream);
 
 }  // namespace moe

@@ -16,6 +16,11 @@
 // source side of the direct load) so that a read's lanes fall on different
 // banks.
 //
+// What bounds it is the feeding of the matrix units: 8192 cubed takes 795 us
+// (1380 TFLOP/s; the library's product reaches 1580 to 1610), 596 of them MFMA
+// alone and 666 without the loads from memory; 16384 rows, K 7168, SwiGLU of N 4096
+// 725 (1330 TFLOP/s).
+//
 // Places past the end of K or of the rows are loads outside the buffer's
 // bounds, which return zeros: no branch and no padded copy.
 #include <algorithm>
@@ -27,7 +32,7 @@ namespace moe {
 namespace {
 
 constexpr int BK = 64;
-constexpr int SUPER = 4;
+constexpr int SUPER = 4;   // row tiles of a super-block; 1 and 8 are slower
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
@@ -138,8 +143,8 @@ struct Operand {
   }
 };
 
-// kDgradPart, kWgradPart: the sum over a part of k, FP32, into the workspace.
-enum Kind { kForward = 0, kForwardGlu = 1, kDgrad = 2, kWgrad = 3, kDgradPart = 4, kWgradPart = 5 };
+// k...Part: the sums over a part of k, FP32, into the workspace.
+enum Kind { kForward, kForwardGlu, kDgrad, kWgrad, kDgradPart, kWgradPart, kForwardPart };
 
 // Waits until at most N of the wave's vector memory operations are outstanding
 // (they end in their order) and all of its LDS operations are done.
@@ -153,7 +158,7 @@ template <class E, int KIND, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM * WN * 64, 1) void gemm16_kernel(Gemm16Args p) {
   constexpr int NW = WM * WN, MS = BM / WM / 16, NS = BN / WN / 16;
   constexpr bool GLU = KIND == kForwardGlu, WGRAD = KIND == kWgrad || KIND == kWgradPart;
-  constexpr bool DGRAD = KIND == kDgrad || KIND == kDgradPart, PART = KIND == kDgradPart || KIND == kWgradPart;
+  constexpr bool DGRAD = KIND == kDgrad || KIND == kDgradPart, PART = KIND >= kDgradPart;
   constexpr bool F32 = WGRAD || PART;   // out is FP32
   using F = typename E::frag;
   using P = Operand<BM, WGRAD, NW>;
@@ -231,8 +236,10 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void gemm16_kernel(Gemm16Args p) {
       pl.bytes -= k0 * 2;
       const uint16_t* b = p.q + (size_t)t.g * p.N * p.K;
       if constexpr (DGRAD) ql.start(b + (size_t)k0 * p.N + t.n0, t.n0, 0, p.N, qload, qload, lane);
-      else if constexpr (!GLU) ql.start(b + (size_t)t.n0 * p.K, 0, p.N - t.n0, p.K, qload, qload, lane);
-      else {
+      else if constexpr (!GLU) {
+        ql.start(b + (size_t)t.n0 * p.K + k0, 0, p.N - t.n0, p.K, qload, qload, lane);
+        ql.bytes -= k0 * 2;
+      } else {
         // the first half of the tile's rows are gate rows, the second the same
         // columns' up rows; each wave loads rows of one half
         const int h = wave >= NW / 2;
@@ -512,6 +519,55 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ par
   }
 }
 
+// The forward's epilogue on the parts' sums, eight columns of out a thread.
+template <class E>
+__global__ __launch_bounds__(256) void join_forward_kernel(const float* __restrict__ parts, int n, Gemm16Args p) {
+  using V8 = Values<E, true>;
+  const bool glu = p.act == kActSwiglu;
+  const int cols = glu ? p.N / 2 : p.N;
+  const size_t end = (size_t)p.groups.at(p.groups.n) * (cols / 8), size = (size_t)p.groups.rows * p.N;
+  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < end; i += (size_t)gridDim.x * 256) {
+    const int m = (int)(i / (cols / 8)), c = (int)(i - (size_t)m * (cols / 8)) * 8;
+    int g = 0;
+    if (p.bias && p.groups.offsets) {   // the last group that starts at or before the row
+      int hi = p.groups.n - 1;
+      while (g < hi) {
+        const int mid = (g + hi + 1) >> 1;
+        if (p.groups.at(mid) <= m) g = mid; else hi = mid - 1;
+      }
+    }
+    auto z8 = [&](int col) {
+      const float* at = parts + (size_t)m * p.N + col;
+      v4f a = *reinterpret_cast<const v4f*>(at), b = *reinterpret_cast<const v4f*>(at + 4);
+      for (int s = 1; s < n; ++s) {
+        a += *reinterpret_cast<const v4f*>(at + s * size);
+        b += *reinterpret_cast<const v4f*>(at + s * size + 4);
+      }
+      V8 z;
+      if (p.bias) z = V8(load_chunk(p.bias + (size_t)g * p.N + col));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z.v[e] += a[e], z.v[4 + e] += b[e];
+      if (p.pre) z.put(p.pre + (size_t)m * p.N + col);
+      return z;
+    };
+    V8 z = z8(c);
+    if (glu) {
+      const V8 u = z8(cols + c);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z.v[e] = glu_value(z.v[e], u.v[e]);
+    } else {
+      activate(p.act, z.v);
+    }
+    const size_t at = (size_t)m * cols + c;
+    if (p.residual) {
+      const V8 r(load_chunk(p.residual + at));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z.v[e] += r.v[e];
+    }
+    z.put(static_cast<uint16_t*>(p.out) + at);
+  }
+}
+
 // Tiles of a product with `m` rows (over all groups) and n columns, about: half
 // a row tile more for every group that has rows.
 long tiles_of(long m, int groups, int n, int bm, int bn) {
@@ -533,7 +589,7 @@ bool big_tiles(long t256, long t128) {
 template <int KIND, class E>
 void launch_kind(const Gemm16Args& p, bool big, long tiles_bound, hipStream_t stream) {
   const long wgs = (tiles_bound + 7) / 8 * 8;
-  if constexpr (KIND != kDgradPart && KIND != kWgradPart)
+  if constexpr (KIND < kDgradPart)
     if (big) {
       hipLaunchKernelGGL((gemm16_kernel<E, KIND, 256, 256, 4, 2>), dim3((unsigned)std::min(wgs, (long)kCus)), dim3(512), 0,
                          stream, p);
@@ -561,13 +617,13 @@ struct RowTiles {
   }
 };
 
-// Parts of k for the gradients' products, whose tiles may be too few for the
-// chip: the number with the least time in us by what was measured: a block of 64
-// k takes 0.65 with at most one 128 x 128 tile to a CU and 1.0 a round of two;
-// joining takes 3 for its launch and the parts' bytes, written and read, at 4
-// TB/s.  (16384 rows to 2048 x 2048: one part 194 us, two 149, four 160; 8192 rows
-// to 256 x 256: 70, 42, 26, 19 and 18.5 with 1 to 16.)
-int parts_of(long t128, int k, double elements) {
+// Parts of k for products whose tiles may be too few for the chip: the number
+// with the least time in us by what was measured: a block of 64 k takes 0.65 with
+// at most one 128 x 128 tile to a CU and 1.0 a round of two; joining takes 3 for
+// its launch and the parts' bytes, written and read, at 4 TB/s.  (16384 rows to
+// 2048 x 2048: one part 194 us, two 149, four 160; 8192 rows to 256 x 256: 70, 42,
+// 26, 19 and 18.5 with 1 to 16.)
+int parts_of(long t128, int k, double elements, double* time = nullptr) {
   int best = 1;
   double least = 0;
   for (int p = 1; p <= 16; p *= 2) {
@@ -580,7 +636,18 @@ int parts_of(long t128, int k, double elements) {
       best = p;
     }
   }
+  if (time) *time = least;
   return best;
+}
+// The forward's: where neither the slim tiles nor whole sums are faster (4151
+// rows, K 3560, N 240: 50 us by slim tiles, two rounds of which the second has four
+// workgroups, 26 in four parts).
+int forward_parts(const Gemm16Args& p) {
+  const long t128 = tiles_of(p.groups.rows, p.groups.n, p.N, 128, 128);
+  if (t128 >= kCus || gemm16_few_rows(p)) return 1;
+  double time;
+  const int parts = parts_of(t128, p.K, (double)p.groups.rows * p.N, &time);
+  return gemm16_slim(p) && gemm16_slim_time(p) <= time + 2.0 ? 1 : parts;
 }
 int dgrad_parts(int rows, int n_groups, int K, int N) {
   return parts_of(tiles_of(rows, n_groups, K, 128, 128), N, (double)rows * K);
@@ -600,7 +667,15 @@ void join(int type, const float* parts, int n, size_t size, const Groups& groups
 
 }  // namespace
 
-size_t gemm16_workspace_bytes(int, int, int, int, int) { return 0; }
+size_t gemm16_workspace_bytes(int rows, int n_groups, int K, int N, int act) {
+  Gemm16Args p{};
+  p.groups = Groups{nullptr, n_groups, rows};
+  p.N = N;
+  p.K = K;
+  p.act = act;
+  const int parts = forward_parts(p);
+  return parts > 1 ? (size_t)parts * rows * N * 4 : 0;
+}
 
 size_t gemm16_backward_workspace_bytes(int rows, int n_groups, int K, int N) {
   const int d = dgrad_parts(rows, n_groups, K, N), w = wgrad_parts(rows, n_groups, K, N);
@@ -610,7 +685,6 @@ size_t gemm16_backward_workspace_bytes(int rows, int n_groups, int K, int N) {
 hipError_t launch_gemm16(int type, const void* a, const int32_t* offsets, int n_groups, int rows, int K, int N,
                          const void* b, const void* bias, int act, const void* residual, void* pre, void* out,
                          void* workspace, hipStream_t stream) {
-  (void)workspace;
   Gemm16Args p{};
   p.p = static_cast<const uint16_t*>(a);
   p.q = static_cast<const uint16_t*>(b);
@@ -622,6 +696,18 @@ hipError_t launch_gemm16(int type, const void* a, const int32_t* offsets, int n_
   p.pre = static_cast<uint16_t*>(pre);
   p.out = out;
   p.act = act;
+  p.parts = forward_parts(p);
+  if (p.parts > 1) {
+    Gemm16Args sums = p;
+    sums.out = workspace;
+    launch<kForwardPart>(type, sums, false, ((long)rows / 128 + n_groups) * ((N + 127) / 128) * p.parts, stream);
+    const size_t chunks = (size_t)rows * (act == kActSwiglu ? N / 2 : N) / 8;
+    const dim3 grid((unsigned)std::min<size_t>((chunks + 255) / 256, 4096));
+    const float* parts = static_cast<const float*>(workspace);
+    if (type == 0) hipLaunchKernelGGL(join_forward_kernel<Bf16>, grid, dim3(256), 0, stream, parts, p.parts, p);
+    else hipLaunchKernelGGL(join_forward_kernel<Fp16>, grid, dim3(256), 0, stream, parts, p.parts, p);
+    return hipGetLastError();
+  }
   if (gemm16_slim(p)) return launch_gemm16_slim(type, p, stream);
   const RowTiles t(rows, n_groups, act == kActSwiglu ? N / 2 : N, act == kActSwiglu);
   if (act == kActSwiglu) launch<kForwardGlu>(type, p, t.big, t.bound, stream);

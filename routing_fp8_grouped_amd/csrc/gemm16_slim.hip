@@ -2,10 +2,12 @@
 // bias) + residual where a tile kernel would leave most of the chip idle.
 //
 // A workgroup makes a slim tile (16 MB rows, 16 NB weight rows) alone: its eight
-// waves split K, stream their parts of both operands from memory straight into
-// MFMA fragments (no LDS, no barrier on the way) and join their sums in LDS at
-// the end.  With one row and N = 4096 every CU has a workgroup, and all of its
-// waves stream: a read of the weights and little else.
+// waves split K, and each brings its parts of both operands from memory in whole
+// lines, turns them into MFMA fragments through LDS of its own (no barrier on the
+// way) and joins its sums with the others' in LDS at the end.  With one row and
+// N = 4096 every CU has a workgroup, and all of its waves stream: a read of the
+// weights and little else.  One row, K 7168, SwiGLU of N 4096: 11 us, the launch
+// among them, 5.3 TB/s; 128 rows in 64 groups of these: 418 us for up to 3.3 GB.
 #include <algorithm>
 #include <cmath>
 
@@ -189,18 +191,14 @@ long slim_tiles(const Gemm16Args& p, int mb, int nb) {
 // and larger tiles.
 long average_rows(const Gemm16Args& p) { return (p.groups.rows + p.groups.n - 1) / p.groups.n; }
 
-template <class E>
-void launch_slim(const Gemm16Args& p, hipStream_t stream) {
-  const long avg = average_rows(p);
-  if (p.groups.rows <= 8) return run<E, 1, 1, 2, 8>(p, stream);   // no tile has more
-  if (avg <= 16) return run<E, 1, 1, 2>(p, stream);
-  // Each tile's cost: rounds of 256 workgroups by a round's time relative to a
-  // 2 x 2 tile's (a smaller tile loads its operands more often, a larger one
-  // leaves CUs idle).  128 rows, K 7168, N 4096 take 44, 32, 27 and 37 us as 2 x 1,
-  // 2 x 2, 2 x 4 and 4 x 4; 333 x 1000 x 1016 11.5, 8.6, 8.0 and 11.1.
+// The tile for more than 16 rows, by cost: rounds of 256 workgroups by a round's
+// time relative to a 2 x 2 tile's (a smaller tile loads its operands more often, a
+// larger one leaves CUs idle).  128 rows, K 7168, N 4096 take 44, 32, 27 and 37 us as
+// 2 x 1, 2 x 2, 2 x 4 and 4 x 4; 333 x 1000 x 1016 11.5, 8.6, 8.0 and 11.1.
+int best_tile(const Gemm16Args& p, float& least) {
   struct { int mb, nb; float time; } const tiles[] = {{2, 1, 0.9f}, {2, 2, 1.0f}, {2, 4, 1.3f}, {4, 2, 1.3f}, {4, 4, 1.75f}};
   int best = 0;
-  float least = INFINITY;
+  least = INFINITY;
   for (int i = 0; i < 5; ++i) {
     const float cost = (float)((slim_tiles(p, tiles[i].mb, tiles[i].nb) + 255) / 256) * tiles[i].time;
     if (cost < least) {
@@ -208,6 +206,15 @@ void launch_slim(const Gemm16Args& p, hipStream_t stream) {
       best = i;
     }
   }
+  return best;
+}
+
+template <class E>
+void launch_slim(const Gemm16Args& p, hipStream_t stream) {
+  if (p.groups.rows <= 8) return run<E, 1, 1, 2, 8>(p, stream);   // no tile has more
+  if (average_rows(p) <= 16) return run<E, 1, 1, 2>(p, stream);
+  float cost;
+  const int best = best_tile(p, cost);
   if (best == 0) run<E, 2, 1, 2>(p, stream);
   else if (best == 1) run<E, 2, 2, 1>(p, stream);
   else if (best == 2) run<E, 2, 4, 1>(p, stream);
@@ -221,9 +228,19 @@ void launch_slim(const Gemm16Args& p, hipStream_t stream) {
 // the tile kernel; 1024 rows, four rounds: 73 against 54), and few rows a group
 // at any size (128 rows in 64 groups, K 7168, N 4096: 425 against 540; 512 rows in
 // 33 groups, K 1024, N 2048: 53 against 30).
+bool gemm16_few_rows(const Gemm16Args& p) { return average_rows(p) <= (p.groups.n == 1 ? 16 : 6); }
+
 bool gemm16_slim(const Gemm16Args& p) {
   if ((size_t)p.N * p.K * 2 > 0x7F000000u) return false;   // a group's matrix within one buffer's bounds
-  return average_rows(p) <= (p.groups.n == 1 ? 16 : 6) || slim_tiles(p, 4, 4) <= 512;
+  return gemm16_few_rows(p) || slim_tiles(p, 4, 4) <= 512;
+}
+
+// A round of 4 x 4 tiles takes 0.26 us per 64 k (512 rows, K and N 4096, two
+// rounds: 39 us with the launch).
+double gemm16_slim_time(const Gemm16Args& p) {
+  float cost;
+  best_tile(p, cost);
+  return p.K / 64.0 * 0.15 * cost;
 }
 
 hipError_t launch_gemm16_slim(int type, const Gemm16Args& p, hipStream_t stream) {

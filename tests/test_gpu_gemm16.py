@@ -199,6 +199,19 @@ def test_large_tiles_and_parts_backward(ty, rows, K, N, sizes):
     Product(TYPES[ty], rows, K, N, sizes).check_backward()
 
 
+# Few and narrow tiles over a long k; the last four sum it in parts
+@pytest.mark.parametrize("ty", TYPES)
+@pytest.mark.parametrize("act", ["gelu", "swiglu"])
+@pytest.mark.parametrize("rows,K,N,sizes", [(6000, 3000, 144, None), (5000, 4000, 272, [0, 1900, 0, 3000, 1, 60, 0]),
+                                            (4151, 3560, 240, None), (256, 5120, 5120, None),
+                                            (4151, 3560, 240, [0, 4000, 151]),
+                                            (1200, 4104, 1040, [700, 0, 1, 400])])
+def test_forward_long_sums(ty, act, rows, K, N, sizes):
+    if (rows, K) in ((4151, 3560), (256, 5120), (1200, 4104)):
+        assert moe.grouped_gemm16_workspace_bytes(rows, len(sizes or [0]), K, N, act) > 0
+    Product(TYPES[ty], rows, K, N, sizes, bias=True, residual=N // 2 if act == "swiglu" else N).check_forward(act)
+
+
 def test_operands_beyond_4_gib():
     """Rows on both sides of 2^32 bytes, of the operands and of the results."""
     rows, K, N = 280000, 8192, 16
