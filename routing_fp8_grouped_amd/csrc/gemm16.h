@@ -33,10 +33,8 @@ __device__ __forceinline__ void activate(int act, float (&z)[N]) {
   else if (act == kActGelu) each([](float v) { return act_value<kActGelu>(v); });
 }
 
-// The forward's product by gemm16_slim.hip: where it is faster than the tile
-// kernel, in particular with few rows (a group); its time in us, about.
-bool gemm16_few_rows(const Gemm16Args& p);
-bool gemm16_slim(const Gemm16Args& p);
+// The forward's product by gemm16_slim.hip, and about how many us it takes
+// besides its launch (infinity where it cannot).
 double gemm16_slim_time(const Gemm16Args& p);
 hipError_t launch_gemm16_slim(int type, const Gemm16Args& p, hipStream_t stream);
 

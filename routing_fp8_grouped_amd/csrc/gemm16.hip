@@ -24,6 +24,7 @@
 // Places past the end of K or of the rows are loads outside the buffer's
 // bounds, which return zeros: no branch and no padded copy.
 #include <algorithm>
+#include <cmath>
 
 #include "gemm16.h"
 
@@ -569,10 +570,10 @@ __global__ __launch_bounds__(256) void join_forward_kernel(const float* __restri
 }
 
 // Tiles of a product with `m` rows (over all groups) and n columns, about: half
-// a row tile more for every group that has rows.
+// a row tile more for every group that has rows, and at least one.
 long tiles_of(long m, int groups, int n, int bm, int bn) {
   const long live = std::min<long>(groups, m);
-  const long rows = live <= 1 ? (m + bm - 1) / bm : (2 * m / bm + live + 1) / 2;
+  const long rows = live <= 1 ? (m + bm - 1) / bm : std::max(live, (2 * m / bm + live + 1) / 2);
   return rows * ((n + bn - 1) / bn);
 }
 
@@ -619,18 +620,18 @@ struct RowTiles {
 
 // Parts of k for products whose tiles may be too few for the chip: the number
 // with the least time in us by what was measured: a block of 64 k takes 0.65 with
-// at most one 128 x 128 tile to a CU and 1.0 a round of two; joining takes 3 for
-// its launch and the parts' bytes, written and read, at 4 TB/s.  (16384 rows to
-// 2048 x 2048: one part 194 us, two 149, four 160; 8192 rows to 256 x 256: 70, 42,
-// 26, 19 and 18.5 with 1 to 16.)
+// at most one 128 x 128 tile to a CU and 1.0 a round of two; joining takes 2.5 for
+// its launch and the parts' bytes, written and read, at 6 TB/s.  (2048 x 2048 from
+// a sum over 16384: one part 194 us, two 149, four 160; 256 x 256 over 8192: 70, 42,
+// 26, 19 and 18.5 with 1 to 16; 6867 x 128 over 4088: 45, 28, 23, 25 and 35.)
 int parts_of(long t128, int k, double elements, double* time = nullptr) {
   int best = 1;
   double least = 0;
   for (int p = 1; p <= 16; p *= 2) {
-    const long blocks = (k / BK + p - 1) / p, wgs = t128 * p;
+    const long blocks = ((k + BK - 1) / BK + p - 1) / p, wgs = t128 * p;
     if (p > 1 && blocks < 2) break;
     const double rounds = wgs <= kCus ? 0.65 : (double)((wgs + 2 * kCus - 1) / (2 * kCus));
-    const double t = blocks * rounds + (p > 1 ? 3.0 + elements * 8 * p / 4e6 : 0.0);
+    const double t = blocks * rounds + (p > 1 ? 2.5 + elements * 8 * p / 6e6 : 0.0);
     if (p == 1 || t < least) {
       least = t;
       best = p;
@@ -639,15 +640,20 @@ int parts_of(long t128, int k, double elements, double* time = nullptr) {
   if (time) *time = least;
   return best;
 }
-// The forward's: where neither the slim tiles nor whole sums are faster (4151
-// rows, K 3560, N 240: 50 us by slim tiles, two rounds of which the second has four
-// workgroups, 26 in four parts).
+// The forward's: 0 where slim tiles take less time, 16 rows and fewer among them.
+// Both read the groups' weights, the slim tiles faster (128 rows in 64 groups, K
+// 7168, N 4096: 418 against 540 us).  Of 120 random products 114 take at most 8%
+// longer than the fastest of slim tiles and 1 to 16 parts (at sums of at most 30
+// GFLOP), the others 25%.
 int forward_parts(const Gemm16Args& p) {
+  double slim = gemm16_slim_time(p), tile;
   const long t128 = tiles_of(p.groups.rows, p.groups.n, p.N, 128, 128);
-  if (t128 >= kCus || gemm16_few_rows(p)) return 1;
-  double time;
-  const int parts = parts_of(t128, p.K, (double)p.groups.rows * p.N, &time);
-  return gemm16_slim(p) && gemm16_slim_time(p) <= time + 2.0 ? 1 : parts;
+  const int parts = parts_of(t128, p.K, (double)p.groups.rows * p.N, &tile);
+  if (p.groups.rows <= 16 && !std::isinf(slim)) return 0;
+  const double weights = 2.0 * std::min(p.groups.n, p.groups.rows) * p.N * p.K;
+  slim = std::max(slim, weights / 7.5e6);
+  tile = std::max(tile, weights / 5.5e6) + 0.7;
+  return slim <= tile ? 0 : parts;
 }
 int dgrad_parts(int rows, int n_groups, int K, int N) {
   return parts_of(tiles_of(rows, n_groups, K, 128, 128), N, (double)rows * K);
@@ -708,7 +714,7 @@ hipError_t launch_gemm16(int type, const void* a, const int32_t* offsets, int n_
     else hipLaunchKernelGGL(join_forward_kernel<Fp16>, grid, dim3(256), 0, stream, parts, p.parts, p);
     return hipGetLastError();
   }
-  if (gemm16_slim(p)) return launch_gemm16_slim(type, p, stream);
+  if (p.parts == 0) return launch_gemm16_slim(type, p, stream);
   const RowTiles t(rows, n_groups, act == kActSwiglu ? N / 2 : N, act == kActSwiglu);
   if (act == kActSwiglu) launch<kForwardGlu>(type, p, t.big, t.bound, stream);
   else launch<kForward>(type, p, t.big, t.bound, stream);

@@ -172,7 +172,9 @@ template <class E, int MB, int NB, int S, int PR = 16 * MB>
 void run(const Gemm16Args& p, hipStream_t stream) {
   const bool glu = p.act == kActSwiglu;
   const int cols = glu ? p.N / 2 : p.N, tn = (glu ? 8 : 16) * NB;
-  const unsigned grid = (unsigned)((p.groups.rows / (16 * MB) + p.groups.n) * ((cols + tn - 1) / tn));
+  // every row tile has a row
+  const long row_tiles = std::min<long>(p.groups.rows, p.groups.rows / (16 * MB) + p.groups.n);
+  const unsigned grid = (unsigned)(row_tiles * ((cols + tn - 1) / tn));
   if (glu) hipLaunchKernelGGL((slim_kernel<E, true, MB, NB, S, PR>), dim3(grid), dim3(kThreads), 0, stream, p);
   else hipLaunchKernelGGL((slim_kernel<E, false, MB, NB, S, PR>), dim3(grid), dim3(kThreads), 0, stream, p);
 }
@@ -186,23 +188,29 @@ long slim_tiles(const Gemm16Args& p, int mb, int nb) {
   return m * ((cols + tn - 1) / tn);
 }
 
-// Row tiles are counted with one more for every group that has rows, so rows
-// per group decide between streaming a group's weights past few rows (MB = 1)
-// and larger tiles.
 long average_rows(const Gemm16Args& p) { return (p.groups.rows + p.groups.n - 1) / p.groups.n; }
 
-// The tile for more than 16 rows, by cost: rounds of 256 workgroups by a round's
-// time relative to a 2 x 2 tile's (a smaller tile loads its operands more often, a
-// larger one leaves CUs idle).  128 rows, K 7168, N 4096 take 44, 32, 27 and 37 us as
-// 2 x 1, 2 x 2, 2 x 4 and 4 x 4; 333 x 1000 x 1016 11.5, 8.6, 8.0 and 11.1.
-int best_tile(const Gemm16Args& p, float& least) {
-  struct { int mb, nb; float time; } const tiles[] = {{2, 1, 0.9f}, {2, 2, 1.0f}, {2, 4, 1.3f}, {4, 2, 1.3f}, {4, 4, 1.75f}};
+// Tiles of 16 mb rows and 16 nb weight rows, and the us of a round of 256 workgroups:
+// about `fixed` for its start and join, `block` per 64 k.  128 rows, K 7168, N 4096
+// take 44, 32, 27 and 37 us as 2 x 1, 2 x 2, 2 x 4 and 4 x 4; 333 x 1000 x 1016 11.5,
+// 8.6, 8.0 and 11.1; 3468 rows, K 400, N 352 24, 14, 15 and 16.
+struct SlimTile {
+  int mb, nb;
+  double fixed, block;
+};
+constexpr SlimTile kSlimTiles[] = {{1, 2, 1.1, 0.085}, {2, 1, 1.1, 0.08}, {2, 2, 0.8, 0.115},
+                                   {2, 4, 1.8, 0.19},  {4, 2, 2.0, 0.2},  {4, 4, 2.3, 0.3}};
+
+// The tile by that time: up to 16 rows a group go to the first, whose weights pass
+// the caches.
+int best_tile(const Gemm16Args& p, double& least) {
+  const bool few = average_rows(p) <= 16;
   int best = 0;
-  least = INFINITY;
-  for (int i = 0; i < 5; ++i) {
-    const float cost = (float)((slim_tiles(p, tiles[i].mb, tiles[i].nb) + 255) / 256) * tiles[i].time;
-    if (cost < least) {
-      least = cost;
+  for (int i = few ? 0 : 1; i < (few ? 1 : 6); ++i) {
+    const SlimTile& t = kSlimTiles[i];
+    const double time = (double)((slim_tiles(p, t.mb, t.nb) + 255) / 256) * (t.fixed + p.K / 64.0 * t.block);
+    if (best == 0 || time < least) {
+      least = time;
       best = i;
     }
   }
@@ -212,35 +220,24 @@ int best_tile(const Gemm16Args& p, float& least) {
 template <class E>
 void launch_slim(const Gemm16Args& p, hipStream_t stream) {
   if (p.groups.rows <= 8) return run<E, 1, 1, 2, 8>(p, stream);   // no tile has more
-  if (average_rows(p) <= 16) return run<E, 1, 1, 2>(p, stream);
-  float cost;
-  const int best = best_tile(p, cost);
-  if (best == 0) run<E, 2, 1, 2>(p, stream);
-  else if (best == 1) run<E, 2, 2, 1>(p, stream);
-  else if (best == 2) run<E, 2, 4, 1>(p, stream);
-  else if (best == 3) run<E, 4, 2, 1>(p, stream);
-  else run<E, 4, 4, 1>(p, stream);
+  double time;
+  switch (best_tile(p, time)) {
+    case 0: return run<E, 1, 1, 2>(p, stream);
+    case 1: return run<E, 2, 1, 2>(p, stream);
+    case 2: return run<E, 2, 2, 1>(p, stream);
+    case 3: return run<E, 2, 4, 1>(p, stream);
+    case 4: return run<E, 4, 2, 1>(p, stream);
+    default: return run<E, 4, 4, 1>(p, stream);
+  }
 }
 
 }  // namespace
 
-// Up to two rounds of 4 x 4 tiles (512 rows, K 4096, N 4096: 39 us against 55 of
-// the tile kernel; 1024 rows, four rounds: 73 against 54), and few rows a group
-// at any size (128 rows in 64 groups, K 7168, N 4096: 425 against 540; 512 rows in
-// 33 groups, K 1024, N 2048: 53 against 30).
-bool gemm16_few_rows(const Gemm16Args& p) { return average_rows(p) <= (p.groups.n == 1 ? 16 : 6); }
-
-bool gemm16_slim(const Gemm16Args& p) {
-  if ((size_t)p.N * p.K * 2 > 0x7F000000u) return false;   // a group's matrix within one buffer's bounds
-  return gemm16_few_rows(p) || slim_tiles(p, 4, 4) <= 512;
-}
-
-// A round of 4 x 4 tiles takes 0.26 us per 64 k (512 rows, K and N 4096, two
-// rounds: 39 us with the launch).
 double gemm16_slim_time(const Gemm16Args& p) {
-  float cost;
-  best_tile(p, cost);
-  return p.K / 64.0 * 0.15 * cost;
+  if ((size_t)p.N * p.K * 2 > 0x7F000000u) return INFINITY;   // a group's matrix within one buffer's bounds
+  double time;
+  best_tile(p, time);
+  return time;
 }
 
 hipError_t launch_gemm16_slim(int type, const Gemm16Args& p, hipStream_t stream) {
