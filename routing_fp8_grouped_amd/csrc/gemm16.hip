@@ -621,7 +621,9 @@ struct RowTiles {
 // Parts of k for products whose tiles may be too few for the chip: the number
 // with the least time in us by what was measured: a block of 64 k takes 0.65 with
 // at most one 128 x 128 tile to a CU and 1.0 a round of two; joining takes 2.5 for
-// its launch and the parts' bytes, written and read, at 6 TB/s.  (2048 x 2048 from
+// its launch and the parts' bytes, written and read, at 6 TB/s, or 3 where they are
+// more than 64 MB (both gradients of 8192 rows in 32 groups, K 2048, N 7168: 881 to
+// 965 us over cards, 1020 with the rows' in two parts of 67 MB).  (2048 x 2048 from
 // a sum over 16384: one part 194 us, two 149, four 160; 256 x 256 over 8192: 70, 42,
 // 26, 19 and 18.5 with 1 to 16; 6867 x 128 over 4088: 45, 28, 23, 25 and 35.)
 int parts_of(long t128, int k, double elements, double* time = nullptr) {
@@ -631,7 +633,8 @@ int parts_of(long t128, int k, double elements, double* time = nullptr) {
     const long blocks = ((k + BK - 1) / BK + p - 1) / p, wgs = t128 * p;
     if (p > 1 && blocks < 2) break;
     const double rounds = wgs <= kCus ? 0.65 : (double)((wgs + 2 * kCus - 1) / (2 * kCus));
-    const double t = blocks * rounds + (p > 1 ? 2.5 + elements * 8 * p / 6e6 : 0.0);
+    const double bytes = elements * 4 * p;
+    const double t = blocks * rounds + (p > 1 ? 2.5 + 2 * bytes / (bytes > 64e6 ? 3e6 : 6e6) : 0.0);
     if (p == 1 || t < least) {
       least = t;
       best = p;
