@@ -113,6 +113,20 @@ def test_gemm_validation(lib):
         assert size(*bad) == 0
 
 
+def test_gemm_workspace_validation(lib):
+    """Few tiles over a long sum: parts of it, which need the workspace."""
+    D = P(0x20000000)
+    need = lib.grouped_gemm16_workspace_bytes(256, 1, 5120, 5120, 0)
+    assert need >= 2 * 4 * 256 * 5120
+
+    def call(ws=D, n=need, out=C, pre=None, res=None):
+        return lib.grouped_gemm16(BF16, A, None, 1, 256, 5120, 5120, B, None, 0, res, pre, out, ws, n, None)
+
+    refused(lib, call, [(dict(ws=None), 3, "workspace"), (dict(n=need - 1), 3, "workspace"),
+                        (dict(ws=MIS4), 3, "workspace"), (dict(ws=A), 1, "must not"), (dict(ws=C), 1, "must not"),
+                        (dict(pre=D), 1, "must not"), (dict(res=D), 1, "must not")])
+
+
 def test_gemm_backward_validation(lib):
     def dgrad(type=BF16, dz=A, off=None, G=1, rows=4, K=64, N=64, b=B, res=None, da=C, ws=None, n=0):
         return lib.grouped_gemm16_dgrad(type, dz, off, G, rows, K, N, b, res, da, ws, n, None)

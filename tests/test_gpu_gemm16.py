@@ -239,6 +239,45 @@ def test_operands_beyond_4_gib():
     assert torch.equal(a[at], before.clamp_min(0))
 
 
+def test_parts_forward_replayed():
+    """The forward in parts, captured, replayed with other rows and group sizes; NaN behind the last row and in one
+    group; the residual's own memory as out."""
+    rows, K, N, G = 1200, 4104, 1040, 4
+    p = Product(torch.bfloat16, rows, K, N, [700, 0, 1, 400], bias=True, residual=N)
+    ws = torch.empty(moe.grouped_gemm16_workspace_bytes(rows, G, K, N, "silu"), dtype=torch.uint8, device=DEV)
+    assert ws.numel() > 0
+    a0, res, out, pre = p.dev["a"].clone(), p.dev["res"].clone(), p.dev["res"].clone(), torch.zeros_like(p.dev["dz"])
+
+    def run(o, z, w):
+        moe.grouped_gemm16(p.dev["a"], p.dev["b"], o, w, offsets=p.dev["off"], bias=p.dev["bias"], act="silu",
+                           residual=o, pre=z)
+
+    run(out, pre, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(out, pre, ws)
+    for i, sizes in enumerate([[700, 0, 1, 400], [0, 0, 0, 1200], [0, 0, 0, 0], [300, 300, 300, 299], [1, 1, 0, 0]]):
+        off = offsets_of(sizes)
+        n = int(off[-1])
+        p.dev["off"].copy_(torch.from_numpy(off))
+        p.dev["a"].copy_(a0.roll(i, 0))
+        clean, cz = res.clone(), torch.full_like(pre, 7.0)
+        run(clean, cz, torch.empty_like(ws))
+        p.dev["a"][n:] = float("nan")
+        if sizes[0]:
+            p.dev["a"][0] = float("nan")
+        out.copy_(res)
+        pre.fill_(7.0)
+        ws.fill_(255)     # NaN, whichever parts are not written
+        graph.replay()
+        torch.cuda.synchronize()
+        lo = 1 if sizes[0] else 0
+        assert torch.equal(out[lo:], clean[lo:]) and torch.equal(pre[lo:], cz[lo:]), i
+        assert torch.equal(out[n:], res[n:]) and (pre[n:] == 7).all(), i
+        assert not lo or (out[0].isnan().all() and pre[0].isnan().all()), i
+
+
 @pytest.mark.parametrize("rows,sizes", [(3, [1, 1, 1]), (400, [130, 140, 130]), (40, [13, 14, 13])])
 def test_nan_and_infinities_stay_in_their_rows(rows, sizes):
     """Rows, groups and memory behind the last row that hold NaN and infinities reach no other row's results."""
