@@ -137,3 +137,51 @@ def test_step_replayed():
         assert torch.equal(s.out, e.out)
         for n, t in ge.items():
             assert torch.equal(getattr(s, n), t), (call, n)
+
+
+def test_gradients_are_differences():
+    """Small whole numbers, of which every sum is exact in every type: the gradients of the product and of the tokens'
+    ways equal the differences that a step of one makes in <gradient, output>."""
+    g = torch.Generator().manual_seed(0)
+    whole = lambda *s, dt=torch.bfloat16: torch.randint(-2, 3, s, generator=g).to(dt).to(DEV)
+    rows, K, N, T, k, E, d = 11, 24, 16, 5, 3, 4, 16
+    off = torch.tensor([0, 4, 4, 11], dtype=torch.int32, device=DEV)
+    a, b, dz = whole(rows, K), whole(3, N, K), whole(rows, N)
+
+    def product():
+        z = torch.empty_like(dz)
+        moe.grouped_gemm16(a, b, z, offsets=off)
+        return (z.double() * dz.double()).sum().item()
+
+    da, db = torch.empty_like(a), torch.empty(3, N, K, device=DEV)
+    moe.grouped_gemm16_dgrad(dz, b, da, offsets=off)
+    moe.grouped_gemm16_wgrad(dz, a, db, offsets=off)
+
+    idx = torch.tensor([[0, 3, 1], [3, -1, 3], [2, 2, 0], [1, 5, 3], [0, 1, 2]], dtype=torch.int32, device=DEV)
+    offsets = torch.empty(E + 1, dtype=torch.int32, device=DEV)
+    pos, slot = torch.empty_like(idx), torch.empty(T * k, dtype=torch.int32, device=DEV)
+    moe.moe_sort(idx, E, offsets, pos, slot)
+    x, y, w = whole(T, d), whole(T * k, d), whole(T, k, dt=torch.float32)
+    drows, dout = whole(T * k, d), whole(T, d)
+    drows[13:] = 0          # behind the last row of a slot
+
+    def dispatch():
+        out = torch.zeros_like(drows)
+        moe.moe_dispatch(x, pos, out, w=w)
+        return (out.double() * drows.double()).sum().item()
+
+    def collect():
+        out = torch.empty_like(dout)
+        moe.moe_collect(y, pos, out, w=w)
+        return (out.double() * dout.double()).sum().item()
+
+    dx, dw1, dy, dw2 = torch.empty_like(x), torch.empty_like(w), torch.zeros_like(y), torch.empty_like(w)
+    moe.moe_dispatch_backward(drows, pos, dx, w=w, x=x, dw=dw1)
+    moe.moe_collect_backward(dout, pos, dy, w=w, y=y, dw=dw2)
+    for f, t, grad in [(product, a, da), (product, b, db), (dispatch, x, dx), (dispatch, w, dw1), (collect, y, dy),
+                       (collect, w, dw2)]:
+        base, flat, want = f(), t.view(-1), grad.double().view(-1).tolist()
+        for i in range(0, flat.numel(), 5):
+            flat[i] += 1
+            assert f() - base == want[i], (f.__name__, i)
+            flat[i] -= 1
