@@ -62,7 +62,8 @@ size_t moe_rmsnorm_backward_workspace_bytes(int T, int d);
  *   dres     [T, d] BF16: the gradient that reaches sum past the norm (through
  *            the residual stream), or NULL
  *   dh       [T, d] BF16 out: the gradient with respect to sum, which is that
- *            of x and of residual.  May be dres's own memory.
+ *            of x and of residual.  May be dres's own memory, which may
+ *            then be dy's or h's too.
  *   dweight  [d] FP32 out (zeros for T = 0)
  *   workspace  at least moe_rmsnorm_backward_workspace_bytes(T, d) bytes,
  *            16-byte aligned; overwritten; calls that share it must not overlap

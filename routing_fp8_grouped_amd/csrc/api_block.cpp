@@ -38,7 +38,7 @@ moe_status rmsnorm_impl(const uint16_t* x, const uint16_t* residual, const uint1
   REQUIRE_ALIGNED4_OR_NULL(scale);
   REQUIRE_ALIGNED4_OR_NULL(rstd);
   const size_t n = (size_t)T * d, row = (size_t)T * 4;
-  s = check_apart({{{"sum", sum, 2 * n}, {x, residual}},
+  s = check_apart({{{"sum", sum, 2 * n}, {"x", "residual"}},
                    {{"y", y, 2 * n}, {}},
                    {{"q", q, n}, {}},
                    {{"scale", scale, n / 32}, {}},
@@ -90,7 +90,7 @@ moe_status layer_few_impl(const uint16_t* x, const uint16_t* wg, const float* bi
     return fail(MOE_ERR_WORKSPACE, "workspace %p of %zu bytes: %zu bytes, 16-byte aligned, needed", workspace,
                 workspace_bytes, need);
   const size_t n = (size_t)T * d * 2, sel = (size_t)T * p.topk * 4, E = p.n_experts, wn = (E + 1) * f * d;
-  s = check_apart({{{"out", out, n}, {x, residual}},
+  s = check_apart({{{"out", out, n}, {"x", "residual"}},
                    {{"idx", idx, sel}, {}},
                    {{"w", w, sel}, {}},
                    {{"workspace", workspace, need}, {}}},
@@ -197,7 +197,9 @@ moe_status moe_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const uin
       return fail(MOE_ERR_WORKSPACE, "workspace %p of %zu bytes: %zu bytes, 16-byte aligned, needed", workspace,
                   workspace_bytes, need);
     const size_t n = (size_t)T * d * 2;
-    s = check_apart({{{"dh", dh, n}, {dres}},
+    // a thread has its elements of dy and h before it stores dh: where these are dres as well, dh may still be its memory
+    const bool in_place = dh == dres;
+    s = check_apart({{{"dh", dh, n}, {"dres", in_place ? "dy" : nullptr, in_place ? "h" : nullptr}},
                      {{"dweight", dweight, (size_t)d * 4}, {}},
                      {{"workspace", workspace, need}, {}}},
                     {{"dy", dy, n}, {"h", h, n}, {"weight", weight, (size_t)d * 2}, {"rstd", rstd, (size_t)T * 4},

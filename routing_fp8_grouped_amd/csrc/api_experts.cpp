@@ -72,7 +72,7 @@ moe_status spread(moe_dtype type, const void* x, const int32_t* pos, const float
   REQUIRE_ALIGNED_OR_NULL(y);
   REQUIRE_ALIGNED4_OR_NULL(dw);
   const CopySizes n(type, T, k, d, rows);
-  s = check_apart({{{out_name, out, n.rows}, {y}}, {{"dw", dw, n.slots}, {}}},
+  s = check_apart({{{out_name, out, n.rows}, {"y"}}, {{"dw", dw, n.slots}, {}}},
                   {{x_name, x, n.tokens}, {"pos", pos, n.slots}, {"w", w, n.slots}, {"y", y, n.rows}});
   if (s != MOE_OK) return s;
   return hip_status(moe::launch_spread(type, x, pos, w, y, T, k, d, rows, out, dw, static_cast<hipStream_t>(stream)), what);
@@ -91,7 +91,7 @@ moe_status sum(moe_dtype type, const void* in, const int32_t* pos, const float* 
   REQUIRE_ALIGNED_OR_NULL(residual);
   REQUIRE_ALIGNED4_OR_NULL(dw);
   const CopySizes n(type, T, k, d, rows);
-  s = check_apart({{{out_name, out, n.tokens}, {residual}}, {{"dw", dw, n.slots}, {}}},
+  s = check_apart({{{out_name, out, n.tokens}, {"residual"}}, {{"dw", dw, n.slots}, {}}},
                   {{in_name, in, n.rows}, {"pos", pos, n.slots}, {"w", w, n.slots}, {"x", x, n.tokens},
                    {"residual", residual, n.tokens}});
   if (s != MOE_OK) return s;
@@ -214,7 +214,7 @@ moe_status grouped_gemm16(moe_dtype type, const void* a, const int32_t* offsets,
   s = check_workspace(workspace, workspace_bytes, need, 16);
   if (s != MOE_OK) return s;
   const size_t R = rows, G = n_groups, No = act == MOE_ACT_SWIGLU ? N / 2 : N;
-  s = check_apart({{{"out", out, 2 * R * No}, {residual}}, {{"pre", pre, 2 * R * N}, {}},
+  s = check_apart({{{"out", out, 2 * R * No}, {"residual"}}, {{"pre", pre, 2 * R * N}, {}},
                    {{"workspace", need ? workspace : nullptr, need}, {}}},
                   {{"a", a, 2 * R * K}, {"b", b, 2 * G * N * K}, {"bias", bias, 2 * G * N},
                    {"residual", residual, 2 * R * No}, {"offsets", offsets, offsets_bytes(n_groups)}});
@@ -252,7 +252,7 @@ moe_status grouped_act_backward(moe_dtype type, const void* dout, const void* pr
     if (s != MOE_OK) return s;
     const size_t R = rows, G = n_groups, No = act == MOE_ACT_SWIGLU ? N / 2 : N;
     const void* used = act == MOE_ACT_NONE ? nullptr : pre;
-    s = check_apart({{{"dz", dz, 2 * R * N}, {used, No == (size_t)N ? dout : nullptr}}, {{"dbias", dbias, 4 * G * N}, {}},
+    s = check_apart({{{"dz", dz, 2 * R * N}, {"pre", "dout"}}, {{"dbias", dbias, 4 * G * N}, {}},
                      {{"workspace", need ? workspace : nullptr, need}, {}}},
                     {{"dout", dout, 2 * R * No}, {"pre", used, 2 * R * N},
                      {"offsets", offsets, offsets_bytes(n_groups)}});
@@ -288,7 +288,7 @@ moe_status grouped_gemm16_dgrad(moe_dtype type, const void* dz, const int32_t* o
   s = check_workspace(workspace, workspace_bytes, need, 16);
   if (s != MOE_OK) return s;
   const size_t R = rows, G = n_groups;
-  s = check_apart({{{"da", da, 2 * R * K}, {residual}}, {{"workspace", need ? workspace : nullptr, need}, {}}},
+  s = check_apart({{{"da", da, 2 * R * K}, {"residual"}}, {{"workspace", need ? workspace : nullptr, need}, {}}},
                   {{"dz", dz, 2 * R * N}, {"b", b, 2 * G * N * K}, {"residual", residual, 2 * R * K},
                    {"offsets", offsets, offsets_bytes(n_groups)}});
   if (s != MOE_OK) return s;
@@ -333,7 +333,7 @@ static moe_status dropout(moe_dtype type, const void* x, const void* residual, i
   REQUIRE_PTR_A(rng, 8);
   REQUIRE(out != nullptr && aligned16(out), "%s is NULL or not 16-byte aligned", out_name);
   const size_t bytes = (size_t)n * bytes_of(type);
-  s = check_apart({{{out_name, out, bytes}, {x, residual}}},
+  s = check_apart({{{out_name, out, bytes}, {x_name, "residual"}}},
                   {{x_name, x, bytes}, {"residual", residual, bytes}, {"rng", rng, 16}});
   if (s != MOE_OK) return s;
   return hip_status(moe::launch_dropout(type, x, residual, n, p, rng, out, static_cast<hipStream_t>(stream)), what);

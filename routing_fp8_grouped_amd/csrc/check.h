@@ -9,6 +9,7 @@
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
+#include <cstring>
 #include <initializer_list>
 
 #include "moe.h"
@@ -74,17 +75,19 @@ inline bool overlap(const Span& a, const Span& b) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
   return x != 0 && y != 0 && x < y + b.bytes && y < x + a.bytes;
 }
-// No output shares memory with an input (but for `same`, whose operand it may
-// be as a whole) or with another output.
+// No output shares memory with an input (but for those named in `same`, which
+// it may be as a whole; NULL names none) or with another output.  An input that
+// is not named is refused at a named one's address, too.
 struct Out {
   Span span;
-  std::initializer_list<const void*> same;
+  std::initializer_list<const char*> same;
 };
 inline moe_status check_apart(std::initializer_list<Out> outs, std::initializer_list<Span> ins) {
   for (const Out* o = outs.begin(); o != outs.end(); ++o) {
     for (const Span& i : ins) {
       bool allowed = false;
-      for (const void* s : o->same) allowed = allowed || (s == i.p && s == o->span.p);
+      for (const char* s : o->same)
+        allowed = allowed || (s && i.p == o->span.p && i.bytes == o->span.bytes && std::strcmp(s, i.name) == 0);
       REQUIRE(allowed || !overlap(o->span, i), "%s must not share memory with %s", o->span.name, i.name);
     }
     for (const Out* b = outs.begin(); b != o; ++b)

@@ -233,3 +233,17 @@ def test_grad_norm_refuses_outputs_in_the_gradients(lib):
     # an outer tensor whose parts the outputs are
     whole = grads([0x1000000], [1 << 24], [0])
     assert norm(g=whole, ws=P(0x100), n=1 << 16) == 1 and "norm must not share memory with grads[0]" in last(lib)
+
+
+def test_in_place_is_the_named_operand_only(lib):
+    """sum, out and dh may be x, residual and dres, but no other operand at the same address."""
+    C = P(0x1100000)
+    assert lib.moe_rmsnorm_quant(A, None, A, 1, 256, 1e-6, A, B, None, None, None, None) == 1
+    assert "sum must not share memory with weight" in last(lib)
+    need = lib.moe_rmsnorm_backward_workspace_bytes(1, 256)
+    assert lib.moe_rmsnorm_backward(B, B, A, P(0x500), A, 1, 256, A, P(0x2000), C, need, None) == 1
+    assert "dh must not share memory with weight" in last(lib)
+    need = lib.moe_layer_few_workspace_bytes(4, 256, 128, 16, 4)
+    assert lib.moe_layer_few(A, A, None, 4, 256, 128, _lib.RouteParams(16, 4, 2, 4, 2.5), P(0x3000000), P(0x500),
+                             P(0x5000000), P(0x600), None, P(0x700), P(0x800), A, C, need, None) == 1
+    assert "out must not share memory with wg" in last(lib)

@@ -193,3 +193,43 @@ def test_binding_refuses_before_the_library():
         moe.grouped_gemm16_workspace_bytes(1, 1, 8, 8, "tanh")
     with pytest.raises(ValueError, match="GPU"):
         moe.moe_dropout(x, 0.1, torch.zeros(2, dtype=torch.int64), x)
+
+
+def test_in_place_is_the_named_operand_only(lib):
+    """An output that is the operand it may be, where another operand lies at the same address: refused, since that one
+    is still read (by other rows, columns or turns) when the output is stored."""
+    pos, dw = P(0x100), C
+
+    def gemm(a=A, b=B, bias=None, res=A, out=A, act=0, N=64):
+        return lib.grouped_gemm16(BF16, a, None, 1, 64, 64, N, b, bias, act, res, None, out, None, 0, None)
+
+    refused(lib, gemm, [(dict(), 1, "out must not share memory with a"), (dict(act=4, N=128), 1, "with a"),
+                        (dict(a=C, b=A), 1, "out must not share memory with b"), (dict(a=C, bias=A), 1, "with bias")])
+
+    def dgrad(dz=A, b=B, K=64, N=64):
+        return lib.grouped_gemm16_dgrad(BF16, dz, None, 1, 64, K, N, b, A, A, None, 0, None)
+
+    refused(lib, dgrad, [(dict(), 1, "da must not share memory with dz"), (dict(K=128), 1, "with dz"),
+                         (dict(dz=C, b=A), 1, "da must not share memory with b")])
+
+    def collect(y=A, w=None, T=8, k=1):
+        return lib.moe_collect(FP32, y, pos, w, A, T, k, 64, 8, A, None)
+
+    refused(lib, collect, [(dict(), 1, "out must not share memory with y"), (dict(y=B, w=A), 1, "with w")])
+
+    def dispatch_backward(drows=B, x=A, k=9):
+        return lib.moe_dispatch_backward(BF16, drows, pos, None, x, A, 8, k, 64, 8, A, dw, None)
+
+    refused(lib, dispatch_backward, [(dict(), 1, "dx must not share memory with x"), (dict(k=2), 1, "with x"),
+                                     (dict(drows=A, x=B), 1, "dx must not share memory with drows")])
+
+    def collect_backward(dout=A, w=None):
+        return lib.moe_collect_backward(BF16, dout, pos, w, A, 8, 1, 64, 8, A, dw, None)
+
+    refused(lib, collect_backward, [(dict(), 1, "dy must not share memory with dout"),
+                                    (dict(dout=B, w=A), 1, "dy must not share memory with w")])
+
+    def act_backward(dout=A, act=4, N=64):
+        return lib.grouped_act_backward(BF16, dout, A, None, 1, 64, N, act, A, None, None, 0, None)
+
+    refused(lib, act_backward, [(dict(), 1, "dz must not share memory with dout")])

@@ -190,6 +190,20 @@ def test_backward_in_place_and_repeatable():
     assert torch.equal(dh, dres) and torch.equal(dw, dw2)
 
 
+@pytest.mark.parametrize("d", [256, 2048, 7168])
+@pytest.mark.parametrize("which", ["dy", "h"])
+def test_backward_in_place_of_an_operand_that_is_dres(which, d):
+    """dh and dres one memory, which dy or h is as well: the same bits as apart."""
+    T = 37
+    t = {n: rows(i, T, d).to(DEV) for i, n in enumerate(("dy", "h"))}
+    w, rstd = weight(4, d).to(DEV), torch.rand(T, device=DEV) + 0.5
+    dh, dw, dw2 = torch.empty_like(t["dy"]), torch.empty(d, device=DEV), torch.empty(d, device=DEV)
+    ws = torch.empty(moe.moe_rmsnorm_backward_workspace_bytes(T, d), dtype=torch.uint8, device=DEV)
+    moe.moe_rmsnorm_backward(t["dy"], t["h"], w, rstd, dh, dw, ws, dres=t[which])
+    moe.moe_rmsnorm_backward(t["dy"], t["h"], w, rstd, t[which], dw2, ws, dres=t[which])
+    assert torch.equal(dh, t[which]) and torch.equal(dw, dw2)
+
+
 def test_no_rows():
     d = 256
     e = buffers(0, d)
