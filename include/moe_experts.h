@@ -122,7 +122,8 @@ size_t grouped_gemm16_workspace_bytes(int rows, int n_groups, int K, int N, moe_
  *             share it must not overlap
  * rows = 0 is a no-op.  MOE_ERR_INVALID_ARG: K or No not a positive multiple of
  * 8, n_groups < 1, offsets NULL with n_groups > 1, an unknown type or act.
- * MOE_ERR_UNSUPPORTED: n_groups > 1024, K or N > 2^20, MOE_FP32.
+ * MOE_ERR_UNSUPPORTED: n_groups > 1024, rows > 2^31 - 1024, K or N > 2^20,
+ * MOE_FP32.
  * MOE_ERR_WORKSPACE: workspace missing, misaligned or short. */
 moe_status grouped_gemm16(moe_dtype type, const void* a, const int32_t* offsets, int n_groups, int rows, int K, int N,
                           const void* b, const void* bias, moe_act act, const void* residual, void* pre, void* out,

@@ -111,6 +111,7 @@ moe_status check_product(int n_groups, int rows, int K, int N, bool glu) {
   REQUIRE(N >= unit && N % unit == 0, "N=%d must be a positive multiple of %d", N, unit);
   if (n_groups > moe::kMaxGroups)
     return fail(MOE_ERR_UNSUPPORTED, "n_groups=%d > %d is not implemented", n_groups, moe::kMaxGroups);
+  if (rows > moe::kMaxRows) return fail(MOE_ERR_UNSUPPORTED, "rows=%d > %d is not implemented", rows, moe::kMaxRows);
   if (K > (1 << 20) || N > (1 << 20)) return fail(MOE_ERR_UNSUPPORTED, "K=%d or N=%d is above 2^20", K, N);
   return MOE_OK;
 }

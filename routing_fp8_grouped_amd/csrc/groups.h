@@ -7,6 +7,9 @@
 namespace moe {
 
 constexpr int kMaxGroups = 1024;
+// Rows of a product: what kernels and host add to a row number or a number of
+// rows (a tile's rows less one, a chunk's, the groups) stays within an int.
+constexpr int kMaxRows = INT32_MAX - (kMaxGroups - 1);
 
 // First row of group g (g = n: the end of the last).  Ranges never leave [0, rows).
 struct Groups {

@@ -233,3 +233,24 @@ def test_in_place_is_the_named_operand_only(lib):
         return lib.grouped_act_backward(BF16, dout, A, None, 1, 64, N, act, A, None, None, 0, None)
 
     refused(lib, act_backward, [(dict(), 1, "dz must not share memory with dout")])
+
+
+def test_most_rows_of_a_product(lib):
+    """Rows whose rounding up to a tile would leave 31 bits are refused by every product; one fewer passes this check."""
+    most = (1 << 31) - 1024
+    off, ws = P(0x100), P(0x10)
+    calls = {
+        "a is NULL": lambda rows: lib.grouped_gemm16(BF16, None, off, 1024, rows, 8, 8, None, None, 0, None, None, None, None,
+                                                     0, None),
+        "dz is NULL": lambda rows: lib.grouped_gemm16_dgrad(BF16, None, off, 1024, rows, 8, 8, None, None, None, None, 0, None),
+        "a is NULL ": lambda rows: lib.grouped_gemm16_wgrad(BF16, A, None, off, 1024, rows, 8, 8, ws, ws, 0, None),
+        "dout is NULL": lambda rows: lib.grouped_act_backward(BF16, None, None, off, 1024, rows, 8, 0, A, None, None, 0, None)}
+    for msg, call in calls.items():
+        for rows in (most + 1, (1 << 31) - 1):
+            assert call(rows) == 2 and f"rows={rows}" in lib.moe_last_error().decode(), (msg, rows)
+        assert call(most) == 1 and msg.strip() in lib.moe_last_error().decode(), msg
+    for rows in (most + 1, (1 << 31) - 1):
+        assert lib.grouped_gemm16_workspace_bytes(rows, 1, 8, 8, 0) == 0
+        assert lib.grouped_gemm16_backward_workspace_bytes(rows, 1, 8, 8) == 0
+        assert lib.grouped_act_backward_workspace_bytes(rows, 1, 8) == 0
+    assert lib.grouped_gemm16_backward_workspace_bytes(most, 1, 8, 8) > 0

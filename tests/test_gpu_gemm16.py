@@ -440,3 +440,35 @@ def test_replays_and_another_stream(rows):
     s.synchronize()
     for n in names:
         assert torch.equal(o2[n], e[n]), n
+
+
+def test_most_rows():
+    """The largest number of rows, in groups of which one has almost all: nearly all rows are zeros, so are their results."""
+    rows, K, N = (1 << 31) - 1024, 8, 8
+    at = torch.tensor([0, 1, 5, rows // 2, rows - 300, rows - 2, rows - 1], device=DEV)
+    off = torch.tensor([0, 2, 2, rows], dtype=I32, device=DEV)
+    few = Product(torch.bfloat16, len(at), K, N, [2, 0, 5], seed=11)
+    a, out = (torch.zeros(rows, 8, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    a[at] = few.dev["a"]
+
+    def check(got, ref, err, name):
+        assert np.all(np.abs(np64(got[at]) - ref) <= rounded(torch.bfloat16, ref, err)), name
+        got[at] = 0
+        assert not got.view(torch.int64).any(), name
+
+    ws = lambda n: torch.empty(max(16, n), dtype=torch.uint8, device=DEV)
+    moe.grouped_gemm16(a, few.dev["b"], out, ws(moe.grouped_gemm16_workspace_bytes(rows, 3, K, N)), offsets=off)
+    ref, mag = ox.gemm(np64(few.a), np64(few.b), few.off, None)
+    check(out, ref, steps(K) * U * mag, "out")
+    w = ws(moe.grouped_gemm16_backward_workspace_bytes(rows, 3, K, N))
+    db = torch.full((3, N, K), 7.0, device=DEV)
+    out[at] = few.dev["dz"]
+    moe.grouped_gemm16_wgrad(out, a, db, w, offsets=off)
+    ref, mag = ox.wgrad(np64(few.dz), np64(few.a), few.off, 3)
+    # zeros add without rounding; the others are at most five terms and their joins
+    assert np.all(np.abs(np64(db) - ref) <= steps(5) * U * mag + U * np.abs(ref))
+    moe.grouped_gemm16_dgrad(out, few.dev["b"], a, w, offsets=off)
+    ref, mag = ox.dgrad(np64(few.dz), np64(few.b), few.off)
+    check(a, ref, steps(N) * U * mag, "da")
+    del a, out
+    torch.cuda.empty_cache()
