@@ -13,6 +13,15 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 constexpr int kWave = 64;
 constexpr float kE4M3Max = 448.0f;
 
+// Workgroups of up to 512 threads in any number, numbered over a grid's x and
+// y.  A dimension of a launch takes fewer than 2^32 threads; more are cut off
+// there without an error.
+constexpr int64_t kGridX = int64_t(1) << 22;
+inline dim3 grid_of(int64_t workgroups) {
+  return dim3((unsigned)(workgroups < kGridX ? workgroups : kGridX), (unsigned)((workgroups + kGridX - 1) / kGridX));
+}
+__device__ __forceinline__ int64_t workgroup() { return blockIdx.y * kGridX + blockIdx.x; }
+
 __device__ __forceinline__ float bf16_to_f32(uint16_t b) {
   return __uint_as_float(static_cast<uint32_t>(b) << 16);
 }

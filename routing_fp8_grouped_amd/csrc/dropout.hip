@@ -54,7 +54,7 @@ __global__ __launch_bounds__(kThreads) void dropout_kernel(const typename E::sto
   constexpr int V = E::kWidth, C = 8 / V;
   using Val = Values<E, true>;
   const Philox philox(rng);
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int64_t i = workgroup() * kThreads + threadIdx.x;
   if (i < n / 8) {
     u32x4 xr[C], rr[C];
 #pragma unroll
@@ -92,12 +92,12 @@ void run(const void* x, const void* residual, int64_t n, uint32_t kept, float sc
          hipStream_t stream) {
   using S = typename E::storage;
   const int64_t groups = n / 8 + 1;
-  const unsigned grid = (unsigned)((groups + kThreads - 1) / kThreads);   // n <= 2^40
+  const dim3 grid = grid_of((groups + kThreads - 1) / kThreads);
   if (residual)
-    hipLaunchKernelGGL((dropout_kernel<E, true>), dim3(grid), dim3(kThreads), 0, stream, static_cast<const S*>(x),
+    hipLaunchKernelGGL((dropout_kernel<E, true>), grid, dim3(kThreads), 0, stream, static_cast<const S*>(x),
                        static_cast<const S*>(residual), n, kept, scale, rng, static_cast<S*>(out));
   else
-    hipLaunchKernelGGL((dropout_kernel<E, false>), dim3(grid), dim3(kThreads), 0, stream, static_cast<const S*>(x),
+    hipLaunchKernelGGL((dropout_kernel<E, false>), grid, dim3(kThreads), 0, stream, static_cast<const S*>(x),
                        static_cast<const S*>(nullptr), n, kept, scale, rng, static_cast<S*>(out));
 }
 

@@ -120,3 +120,18 @@ def test_another_stream():
     moe.moe_dropout(x, 0.25, r, b, stream=s)
     s.synchronize()
     assert torch.equal(a, b)
+
+
+def test_more_threads_than_a_launch_dimension_takes():
+    """2^35 elements and some (2^32 threads of eight): windows of the front, of the middle and of the end."""
+    n = (1 << 35) + 19
+    x = torch.ones(n, dtype=torch.bfloat16, device=DEV)
+    moe.moe_dropout(x, 0.5, rng_of(11, 3), x)
+    for first, last in ((0, 64), ((1 << 33) - 9, (1 << 33) + 9), ((1 << 34) - 9, (1 << 34) + 9), ((1 << 35) - 9, n)):
+        keep, _ = ox.keep(last, 0.5, 11, 3, first=first)
+        assert np.array_equal(x[first:last].float().cpu().numpy(), np.where(keep, 2.0, 0.0)), first
+    # half of the elements are kept: within five deviations of a binomial count
+    kept = sum(int((part != 0).sum()) for part in x.split(1 << 32))
+    assert abs(kept - n / 2) < 5 * (n / 4) ** 0.5
+    del x
+    torch.cuda.empty_cache()
