@@ -234,8 +234,9 @@ __global__ __launch_bounds__(512) void copy_kernel(CopyArgs p, int team) {
   using S = typename E::storage;
   const int lane = BLOCK ? threadIdx.x : threadIdx.x & (team - 1);
   const int stride = BLOCK ? blockDim.x : team;
-  const int t = BLOCK ? blockIdx.x : (int)((blockIdx.x * (size_t)blockDim.x + threadIdx.x) / (unsigned)team);
-  if (!BLOCK && t >= p.T) return;   // whole teams
+  const int64_t token = BLOCK ? workgroup() : workgroup() * (256u / (unsigned)team) + threadIdx.x / (unsigned)team;
+  if (token >= p.T) return;   // whole teams
+  const int t = (int)token;
   const size_t d = p.d;
   const S* tok = static_cast<const S*>(p.tok) + (size_t)t * d;
   const S* add = static_cast<const S*>(p.add) + (size_t)t * d;
@@ -314,7 +315,7 @@ void run_copy(const CopyArgs& p, hipStream_t stream) {
   auto go = [&](auto block, auto stream_past) {
     constexpr bool BLOCK = decltype(block)::value;
     hipLaunchKernelGGL((copy_kernel<E, SUM, DOTS, BLOCK, decltype(stream_past)::value, MANY, KB>),
-                       dim3(BLOCK ? p.T : (p.T + 256 / team - 1) / (256 / team)), dim3(BLOCK ? team : 256), 0, stream, p,
+                       grid_of(BLOCK ? p.T : ((int64_t)p.T + 256 / team - 1) / (256 / team)), dim3(BLOCK ? team : 256), 0, stream, p,
                        team);
   };
   using Yes = std::true_type;

@@ -292,3 +292,33 @@ def test_replays_and_another_stream():
     s.synchronize()
     for n in ("offsets", "pos", "slot", "rows", "out", "dw"):
         assert torch.equal(o[n], e[n]), n
+
+
+@pytest.mark.parametrize("T,d", [((1 << 28) + 3, 8), (22369700, 1032)])
+def test_more_threads_than_a_launch_dimension_takes(T, d):
+    """Teams of 16 lanes and of 192 threads, 2^32 threads and some: the tokens in reverse order and back."""
+    x = torch.empty(T, d, dtype=torch.bfloat16, device=DEV)
+    x.view(torch.int16).random_(1 << 14)       # finite, positive
+    pos = torch.arange(T - 1, -1, -1, dtype=I32, device=DEV).view(T, 1)
+    rows = torch.full_like(x, 7.0)
+    moe.moe_dispatch(x, pos, rows)
+    step = 1 << 20
+    for lo in range(0, T, step):
+        hi = min(T, lo + step)
+        assert torch.equal(rows[T - hi:T - lo].flip(0), x[lo:hi]), lo
+    # back, the weights' gradient along: products of a row with itself where one token in many is not zero
+    at = torch.tensor([0, 1, T // 2, (1 << 22) * 16 % T, T - 1], device=DEV)
+    some = x[at].clone()
+    x.zero_()
+    x[at] = some
+    dx, dw = torch.full_like(x, 7.0), torch.full((T, 1), 7.0, device=DEV)
+    moe.moe_dispatch_backward(rows, pos, dx, x=x, dw=dw)
+    for lo in range(0, T, step):
+        hi = min(T, lo + step)
+        assert torch.equal(rows[T - hi:T - lo].flip(0), dx[lo:hi]), lo
+    ref = np64(some) ** 2
+    assert np.all(np.abs(np64(dw[at, 0]) - ref.sum(1)) <= (d + 16) * U * ref.sum(1))
+    dw[at] = 0
+    assert not dw.any()
+    del x, rows, dx
+    torch.cuda.empty_cache()
