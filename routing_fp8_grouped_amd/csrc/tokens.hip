@@ -245,7 +245,7 @@ __global__ __launch_bounds__(512) void copy_kernel(CopyArgs p, int team) {
   auto each = [&](auto fn) {
     const int full = p.d / E::kWidth;
     for (int c = lane; c < full; c += stride) fn(c * E::kWidth, std::true_type{});
-    for (int c = full * E::kWidth + lane; c < p.d; c += stride) fn(c, std::false_type{});
+    if (lane < p.d - full * E::kWidth) fn(full * E::kWidth + lane, std::false_type{});
   };
   if constexpr (SUM) {
     const Slots<KB> s(p, t, 0);
@@ -307,7 +307,7 @@ int team_of(int n) {
 
 template <class E, bool SUM, bool DOTS, bool MANY, int KB>
 void run_copy(const CopyArgs& p, hipStream_t stream) {
-  const int team = team_of((p.d + E::kWidth - 1) / E::kWidth);
+  const int team = team_of((p.d - 1) / E::kWidth + 1);
   // Wide rows that are more than the last-level cache holds go past it (V3 rows of
   // 16384 tokens there and back: 853 -> 809 us; of 4099 tokens of 2052: 67.6 -> 65.9).
   const size_t row = (size_t)p.d * sizeof(typename E::storage);

@@ -322,3 +322,25 @@ def test_more_threads_than_a_launch_dimension_takes(T, d):
     assert not dw.any()
     del x, rows, dx
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("ty", ["bf16", "fp32"])
+def test_widest_rows(ty):
+    """Two tokens of 2^31 - 1 elements, whose last chunk is cut off: there, back, and the weights' gradient."""
+    T, d, dt = 2, (1 << 31) - 1, TYPES[ty]
+    g = torch.Generator().manual_seed(3)
+    at = torch.tensor([0, 9, d // 2, d - 400, d - 9, d - 8, d - 2, d - 1], device=DEV)
+    v = torch.randn(T, len(at), generator=g).to(dt)
+    x, rows = torch.zeros(T, d, dtype=dt, device=DEV), torch.full((T + 1, d), 7.0, dtype=dt, device=DEV)
+    x[:, at] = v.to(DEV)
+    pos = torch.tensor([[2], [0]], dtype=I32, device=DEV)
+    moe.moe_dispatch(x, pos, rows)
+    assert torch.equal(rows[2], x[0]) and torch.equal(rows[0], x[1]) and (rows[1] == 7).all()
+    dx, dw = torch.full_like(x, 7.0), torch.full((T, 1), 7.0, device=DEV)
+    moe.moe_dispatch_backward(rows, pos, dx, x=x, dw=dw)
+    assert torch.equal(dx, x)
+    ref = (np64(v) ** 2).sum(1, keepdims=True)
+    # zeros add without rounding; eight terms, and the joins of lanes and waves
+    assert np.all(np.abs(np64(dw) - ref) <= (8 + 6 + 8) * U * ref)
+    del x, rows, dx
+    torch.cuda.empty_cache()
