@@ -22,10 +22,13 @@ namespace {
 constexpr int kThreads = 256, kWaves = kThreads / 64, kCols = 512;
 constexpr int U = 4;   // rows in flight a wave
 
-// Rows of a chunk: 64, fewer while the launch would not fill the chip.
-int chunk_rows(int rows, int N) {
+// Rows of a chunk: 64, fewer while the launch would not fill the chip, more
+// where its chunks would be 2^32 threads (a launch's dimension takes fewer and
+// cuts the others off without an error).
+int chunk_rows(int rows, int n_groups, int N) {
   int r = 64;
   while (r > 8 && (long)(rows / r + 1) * ((N + kCols - 1) / kCols) < 1024) r /= 2;
+  while (((int64_t)rows / r + n_groups) * kThreads >= int64_t(1) << 32) r *= 2;
   return r;
 }
 
@@ -149,13 +152,13 @@ void run(int act, const ActArgs& p, dim3 grid, hipStream_t stream) {
 }  // namespace
 
 size_t act_backward_workspace_bytes(int rows, int n_groups, int N) {
-  return rows == 0 ? 0 : ((size_t)rows / chunk_rows(rows, N) + n_groups) * N * sizeof(float);
+  return rows == 0 ? 0 : ((size_t)rows / chunk_rows(rows, n_groups, N) + n_groups) * N * sizeof(float);
 }
 
 hipError_t launch_act_backward(int type, const void* dout, const void* pre, const int32_t* offsets, int n_groups,
                                int rows, int N, int act, void* dz, float* dbias, float* partial, hipStream_t stream) {
   const Groups groups{offsets, n_groups, rows};
-  const int R = chunk_rows(rows, N);
+  const int R = chunk_rows(rows, n_groups, N);
   if (rows > 0) {
     const int width = act == kActSwiglu ? N / 2 : N;
     const ActArgs p{static_cast<const uint16_t*>(dout), static_cast<const uint16_t*>(pre), groups, N, R,

@@ -472,3 +472,28 @@ def test_most_rows():
     check(a, ref, steps(N) * U * mag, "da")
     del a, out
     torch.cuda.empty_cache()
+
+
+def test_most_rows_act_backward():
+    """The largest number of rows (more chunks than a launch takes, were they of 64 rows): almost all are zeros."""
+    rows, N = (1 << 31) - 1024, 8
+    at = torch.tensor([0, 1, 5, rows // 2, rows - 300, rows - 2, rows - 1], device=DEV)
+    off = torch.tensor([0, 2, 2, rows], dtype=I32, device=DEV)
+    dout, z = torch.randn(len(at), N).bfloat16(), torch.randn(len(at), N).bfloat16()
+    d, dz = (torch.zeros(rows, N, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    d[at], dz[at] = dout.to(DEV), z.to(DEV)
+    db = torch.full((3, N), 7.0, device=DEV)
+    ws = torch.empty(moe.grouped_act_backward_workspace_bytes(rows, 3, N), dtype=torch.uint8, device=DEV)
+    moe.grouped_act_backward(d, dz, "silu", dz, offsets=off, dbias=db, workspace=ws)
+    _, slopes = ox.act(np64(z), "silu")
+    ref = np64(dout) * slopes[0]
+    # a slope's error as in test_act_backward; zeros add without rounding
+    err = 16 * U * (1 + np.abs(np64(z))) * np.abs(np64(dout)) + 2.0 ** -126
+    assert np.all(np.abs(np64(dz[at]) - ref) <= rounded(torch.bfloat16, ref, err))
+    for g, part in enumerate((slice(0, 2), slice(0, 0), slice(2, 7))):
+        bound = err[part].sum(0) + 8 * U * (np.abs(ref[part]) + err[part]).sum(0)
+        assert np.all(np.abs(np64(db)[g] - ref[part].sum(0)) <= bound), g
+    dz[at] = 0
+    assert not dz.view(torch.int64).any()
+    del d, dz
+    torch.cuda.empty_cache()
