@@ -17,7 +17,7 @@ __global__ __launch_bounds__(256) void quant_1x128_kernel(const uint16_t* __rest
                                                           long n_tiles,
                                                           uint8_t* __restrict__ q,
                                                           float* __restrict__ scale) {
-  const long tile = (long)blockIdx.x * 16 + (threadIdx.x >> 4);
+  const long tile = workgroup() * 16 + (threadIdx.x >> 4);
   const int sub = threadIdx.x & 15;
   const bool valid = tile < n_tiles;
   uint4 raw = make_uint4(0, 0, 0, 0);
@@ -91,10 +91,10 @@ hipError_t launch_quant_1x128(const uint16_t* x, long rows, int cols, uint8_t* q
   const long n_tiles = rows * (long)(cols / 128);
   const long blocks = (n_tiles + 15) / 16;
   if (pow2)
-    hipLaunchKernelGGL(quant_1x128_kernel<true>, dim3((unsigned)blocks), dim3(256), 0, stream, x,
+    hipLaunchKernelGGL(quant_1x128_kernel<true>, grid_of(blocks), dim3(256), 0, stream, x,
                        n_tiles, q, scale);
   else
-    hipLaunchKernelGGL(quant_1x128_kernel<false>, dim3((unsigned)blocks), dim3(256), 0, stream, x,
+    hipLaunchKernelGGL(quant_1x128_kernel<false>, grid_of(blocks), dim3(256), 0, stream, x,
                        n_tiles, q, scale);
   return hipGetLastError();
 }
