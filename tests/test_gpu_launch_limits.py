@@ -31,3 +31,24 @@ def test_quant():
     assert not q.view(torch.int64).any() and (s == 1).all()
     del x, q, s
     torch.cuda.empty_cache()
+
+
+def test_permute():
+    """2^24 rows and some (2^32 threads of 256 a row): every row is its token's."""
+    T, k, E, d = 1900000, 8, 32, 128
+    idx = torch.rand(T, E, device=DEV).topk(k, dim=1).indices.int()
+    xq = torch.randint(0, 256, (T, d), dtype=torch.uint8, device=DEV)
+    xs = torch.rand(T, 1, device=DEV)
+    rows = T * (k + 1)
+    assert rows > 1 << 24
+    i32 = lambda *s: torch.full(s, 7, dtype=torch.int32, device=DEV)
+    offsets, pos, row_token = i32(E + 2), i32(T, k), i32(rows)
+    xp, sp = torch.zeros(rows, d, dtype=torch.uint8, device=DEV), torch.zeros(rows, 1, device=DEV)
+    ws = torch.empty(moe.moe_permute_workspace_bytes(T, k, E), dtype=torch.uint8, device=DEV)
+    moe.moe_permute(idx, E, offsets, pos, row_token, ws, xq, xs, xp, sp)
+    token = row_token.long()
+    assert torch.equal(token[pos.long().flatten()], torch.arange(T, device=DEV).repeat_interleave(k))
+    assert torch.equal(token[T * k:], torch.arange(T, device=DEV))
+    assert torch.equal(xp, xq[token]) and torch.equal(sp, xs[token])
+    del xp
+    torch.cuda.empty_cache()
