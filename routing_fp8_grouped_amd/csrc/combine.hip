@@ -46,13 +46,14 @@ __device__ __forceinline__ uint4 load_once(const uint16_t* p) {
 template <int KC>
 __global__ __launch_bounds__(256) void combine_kernel(const uint16_t* __restrict__ y,
                                                       const int32_t* __restrict__ pos,
-                                                      const float* __restrict__ w, int k, int d,
+                                                      const float* __restrict__ w, int T, int k, int d,
                                                       int rows, int shared_row0,
                                                       const uint16_t* __restrict__ residual,
                                                       uint16_t* __restrict__ out) {
   __shared__ int s_pos[16];
   __shared__ float s_w[16];
-  const int t = blockIdx.x;
+  if (workgroup() >= T) return;
+  const int t = (int)workgroup();
   const int kk = KC > 0 ? KC : k;
   const int tid = threadIdx.x;
   if (tid < kk) {
@@ -104,10 +105,10 @@ hipError_t launch_combine(const uint16_t* y, const int32_t* pos, const float* w,
   for (int q = (n8 + 255) / 256; n8 / q >= 128; ++q)
     if (n8 % q == 0) { nt = n8 / q; break; }
   if (k == 8)
-    hipLaunchKernelGGL(combine_kernel<8>, dim3(T), dim3(nt), 0, stream, y, pos, w, k, d, rlim, shared_row0,
+    hipLaunchKernelGGL(combine_kernel<8>, grid_of(T), dim3(nt), 0, stream, y, pos, w, T, k, d, rlim, shared_row0,
                        residual, out);
   else
-    hipLaunchKernelGGL(combine_kernel<0>, dim3(T), dim3(nt), 0, stream, y, pos, w, k, d, rlim, shared_row0,
+    hipLaunchKernelGGL(combine_kernel<0>, grid_of(T), dim3(nt), 0, stream, y, pos, w, T, k, d, rlim, shared_row0,
                        residual, out);
   return hipGetLastError();
 }

@@ -52,3 +52,23 @@ def test_permute():
     assert torch.equal(xp, xq[token]) and torch.equal(sp, xs[token])
     del xp
     torch.cuda.empty_cache()
+
+
+def test_combine():
+    """2^24 tokens and some (2^32 threads of 256 a token), forward and backward."""
+    T, d = (1 << 24) + 5, 128
+    y = torch.empty(T, d, dtype=torch.bfloat16, device=DEV)
+    y.view(torch.int16).random_(1 << 14)       # finite, positive
+    pos = torch.arange(T - 1, -1, -1, dtype=torch.int32, device=DEV).view(T, 1)
+    w = torch.full((T, 1), 0.5, device=DEV)
+    out = torch.full_like(y, 7.0)
+    moe.moe_combine(y, pos, w, -1, out)
+    assert torch.equal(out, y.flip(0) * 0.5)
+    dy, dw = torch.full_like(y, 7.0), torch.full((T, 1), 7.0, device=DEV)
+    moe.moe_combine_backward(out, y, pos, w, -1, dy, dw)
+    assert torch.equal(dy, out.flip(0) * 0.5)
+    # dw = <out, y of the row>: positive terms, 128 of them, so each sum is within 128 roundings
+    ref = torch.cat([(a.double() ** 2).sum(1) * 2 for a in out.split(1 << 20)])
+    assert ((dw[:, 0].double() - ref).abs() <= 128 * 2.0 ** -24 * ref + 128 * 2.0 ** -149).all()
+    del y, out, dy
+    torch.cuda.empty_cache()
