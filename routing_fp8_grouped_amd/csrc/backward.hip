@@ -20,6 +20,8 @@
 // column range [128 pb[e], 128 pb[e+1]) with pb[e] = sum over earlier experts of
 // ceil(rows / 128); padding columns are zero codes.  Their scales are
 // [Kp/128, C]: one per column and 128-row block.
+#include <algorithm>
+
 #include "common.h"
 #include "kernels.h"
 
@@ -123,11 +125,10 @@ __device__ __forceinline__ void quant_chunk_pow2(const uint32_t (&o)[4], uint8_t
 template <bool Q>
 __global__ __launch_bounds__(256) void combine_backward_kernel(
     const uint16_t* __restrict__ dout, const uint16_t* __restrict__ y, const int32_t* __restrict__ pos,
-    const float* __restrict__ w, int T, int k, int d, int rows, int shared_row0, uint16_t* __restrict__ dy,
+    const float* __restrict__ w, int k, int d, int rows, int shared_row0, uint16_t* __restrict__ dy,
     float* __restrict__ dw, uint8_t* __restrict__ dyq, float* __restrict__ dys) {
   __shared__ float red[4];
-  if (workgroup() >= T) return;
-  const int t = (int)workgroup(), tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const uint16_t* go = dout + (size_t)t * d;
   const int n8 = d / 8;
   for (int j = 0; j < k; ++j) {
@@ -451,12 +452,16 @@ hipError_t launch_combine_backward(const uint16_t* dout, const uint16_t* y, cons
                                    float* dw, uint8_t* dyq, float* dys, hipStream_t stream) {
   // rows of y / dy (the same bound as the forward combine's)
   const int rlim = shared_row0 >= 0 ? shared_row0 + T : T * k;
-  if (dyq)
-    hipLaunchKernelGGL(combine_backward_kernel<true>, grid_of(T), dim3(256), 0, stream, dout, y, pos, w, T, k, d,
-                       rlim, shared_row0, dy, dw, dyq, dys);
-  else
-    hipLaunchKernelGGL(combine_backward_kernel<false>, grid_of(T), dim3(256), 0, stream, dout, y, pos, w, T, k, d,
-                       rlim, shared_row0, dy, dw, nullptr, nullptr);
+  for (int64_t t0 = 0; t0 < T; t0 += kGridX) {
+    const dim3 grid((unsigned)std::min(T - t0, kGridX));
+    const int shared0 = shared_row0 >= 0 ? shared_row0 + (int)t0 : shared_row0;
+    if (dyq)
+      hipLaunchKernelGGL(combine_backward_kernel<true>, grid, dim3(256), 0, stream, dout + t0 * d, y, pos + t0 * k,
+                         w + t0 * k, k, d, rlim, shared0, dy, dw + t0 * k, dyq, dys);
+    else
+      hipLaunchKernelGGL(combine_backward_kernel<false>, grid, dim3(256), 0, stream, dout + t0 * d, y, pos + t0 * k,
+                         w + t0 * k, k, d, rlim, shared0, dy, dw + t0 * k, nullptr, nullptr);
+  }
   return hipGetLastError();
 }
 

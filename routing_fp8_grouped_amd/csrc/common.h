@@ -13,9 +13,10 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 constexpr int kWave = 64;
 constexpr float kE4M3Max = 448.0f;
 
-// Workgroups of up to 512 threads in any number, numbered over a grid's x and
-// y.  A dimension of a launch takes fewer than 2^32 threads; more are cut off
-// there without an error.
+// Workgroups of up to 512 threads in any number.  A dimension of a launch takes
+// fewer than 2^32 threads; more are cut off there without an error.  Kernels
+// that check their bounds anyway number their workgroups over a grid's x and y;
+// the others are launched once per kGridX workgroups, with moved pointers.
 constexpr int64_t kGridX = int64_t(1) << 22;
 inline dim3 grid_of(int64_t workgroups) {
   return dim3((unsigned)(workgroups < kGridX ? workgroups : kGridX), (unsigned)((workgroups + kGridX - 1) / kGridX));

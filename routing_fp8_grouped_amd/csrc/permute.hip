@@ -14,6 +14,7 @@
 // and an optional gather that copies each token's FP8 row and scales to its
 // k + 1 rows (the dispatch proper; the grouped GEMM can instead read the
 // token rows through row_token).
+#include <algorithm>
 #include <mutex>
 
 #include "common.h"
@@ -123,13 +124,12 @@ __global__ __launch_bounds__(PB) void permute_scatter_kernel(const int32_t* __re
 
 // One destination row per workgroup: 16-byte chunks of the FP8 row, then the
 // row's FP32 scales.
-__global__ __launch_bounds__(256) void permute_gather_kernel(size_t rows, const int32_t* __restrict__ row_token,
+__global__ __launch_bounds__(256) void permute_gather_kernel(const int32_t* __restrict__ row_token,
                                                              const uint8_t* __restrict__ xq,
                                                              const float* __restrict__ xs, int T,
                                                              int d, uint8_t* __restrict__ xq_perm,
                                                              float* __restrict__ xs_perm) {
-  const size_t r = workgroup();
-  if (r >= rows) return;
+  const size_t r = blockIdx.x;
   // Rows left unassigned by out-of-range expert ids hold no token: clamp the
   // source so every read stays inside xq.
   const int src = min(max(row_token[r], 0), T - 1);
@@ -154,9 +154,10 @@ hipError_t launch_permute(const int32_t* idx, int T, int k, int E, const uint8_t
   hipLaunchKernelGGL(permute_scatter_kernel, dim3(nb), dim3(PB), 0, stream, idx, T, k, E,
                      block_counts, offsets, pos, row_token);
   if (xq_perm != nullptr) {
-    const size_t rows = (size_t)T * k + T;
-    hipLaunchKernelGGL(permute_gather_kernel, grid_of(rows), dim3(256), 0, stream, rows,
-                       row_token, xq, xs, T, d, xq_perm, xs_perm);
+    const int64_t rows = (int64_t)T * k + T;
+    for (int64_t r0 = 0; r0 < rows; r0 += kGridX)
+      hipLaunchKernelGGL(permute_gather_kernel, dim3((unsigned)std::min(rows - r0, kGridX)), dim3(256), 0, stream,
+                         row_token + r0, xq, xs, T, d, xq_perm + r0 * d, xs_perm + r0 * (d / 128));
   }
   return hipGetLastError();
 }

@@ -3,6 +3,8 @@
 // (a) fine-grained quantization and (d) online scaling; the book's chapter 16,
 // "V3's grouping" and "Online scales").  Both kernels are HBM-bound streams:
 // read BF16 once, write E4M3 once plus one FP32 per tile.
+#include <algorithm>
+
 #include "common.h"
 #include "kernels.h"
 
@@ -17,7 +19,7 @@ __global__ __launch_bounds__(256) void quant_1x128_kernel(const uint16_t* __rest
                                                           long n_tiles,
                                                           uint8_t* __restrict__ q,
                                                           float* __restrict__ scale) {
-  const long tile = workgroup() * 16 + (threadIdx.x >> 4);
+  const long tile = (long)blockIdx.x * 16 + (threadIdx.x >> 4);
   const int sub = threadIdx.x & 15;
   const bool valid = tile < n_tiles;
   uint4 raw = make_uint4(0, 0, 0, 0);
@@ -89,13 +91,16 @@ __global__ __launch_bounds__(256) void quant_128x128_kernel(const uint16_t* __re
 hipError_t launch_quant_1x128(const uint16_t* x, long rows, int cols, uint8_t* q, float* scale,
                               bool pow2, hipStream_t stream) {
   const long n_tiles = rows * (long)(cols / 128);
-  const long blocks = (n_tiles + 15) / 16;
-  if (pow2)
-    hipLaunchKernelGGL(quant_1x128_kernel<true>, grid_of(blocks), dim3(256), 0, stream, x,
-                       n_tiles, q, scale);
-  else
-    hipLaunchKernelGGL(quant_1x128_kernel<false>, grid_of(blocks), dim3(256), 0, stream, x,
-                       n_tiles, q, scale);
+  for (long t0 = 0; t0 < n_tiles; t0 += kGridX * 16) {
+    const long n = std::min<long>(n_tiles - t0, kGridX * 16);
+    const dim3 grid((unsigned)((n + 15) / 16));
+    if (pow2)
+      hipLaunchKernelGGL(quant_1x128_kernel<true>, grid, dim3(256), 0, stream, x + t0 * 128, n, q + t0 * 128,
+                         scale + t0);
+    else
+      hipLaunchKernelGGL(quant_1x128_kernel<false>, grid, dim3(256), 0, stream, x + t0 * 128, n, q + t0 * 128,
+                         scale + t0);
+  }
   return hipGetLastError();
 }
 

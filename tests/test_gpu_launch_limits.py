@@ -72,3 +72,29 @@ def test_combine():
     assert ((dw[:, 0].double() - ref).abs() <= 128 * 2.0 ** -24 * ref + 128 * 2.0 ** -149).all()
     del y, out, dy
     torch.cuda.empty_cache()
+
+
+def test_combine_over_two_launches():
+    """2^22 tokens and some, with shared rows, the residual and the backward's FP8 copy: the same as in two calls."""
+    T, d = (1 << 22) + 5, 128
+    y = torch.randn(2 * T, d, dtype=torch.bfloat16, device=DEV)
+    res = torch.randn(T, d, dtype=torch.bfloat16, device=DEV)
+    pos = torch.randperm(T, device=DEV).int().view(T, 1)
+    w = torch.rand(T, 1, device=DEV)
+    out = torch.full_like(res, 7.0)
+    moe.moe_combine(y, pos, w, T, out, residual=res)
+    grads = lambda: (torch.full_like(y, 7.0), torch.full((T, 1), 7.0, device=DEV),
+                     torch.full((2 * T, d), 7, dtype=torch.uint8, device=DEV), torch.full((2 * T, 1), 7.0, device=DEV))
+    dy, dw, dyq, dys = grads()
+    moe.moe_combine_backward(out, y, pos, w, T, dy, dw, dyq=dyq, dys=dys)
+    # two halves, the second's shared rows moved with its tokens
+    half = T // 2
+    out2, (dy2, dw2, dyq2, dys2) = torch.full_like(res, 7.0), grads()
+    for lo, hi in ((0, half), (half, T)):
+        cut = slice(lo, hi)
+        moe.moe_combine(y, pos[cut], w[cut], T + lo, out2[cut], residual=res[cut])
+        moe.moe_combine_backward(out[cut], y, pos[cut], w[cut], T + lo, dy2, dw2[cut], dyq=dyq2, dys=dys2)
+    assert torch.equal(out, out2)
+    for a, b in ((dy, dy2), (dw, dw2), (dyq, dyq2), (dys, dys2)):
+        assert torch.equal(a, b)
+    assert torch.equal(dy[T:], out) and not (dw == 7).any()
