@@ -101,7 +101,7 @@ moe_status moe_collect_backward(moe_dtype type, const void* dout, const int32_t*
 typedef enum {
   MOE_ACT_NONE = 0,
   MOE_ACT_RELU = 1,
-  MOE_ACT_SILU = 2,     /* z / (1 + e^-z) */
+  MOE_ACT_SILU = 2,     /* z / (1 + e^-z); 0 below z = -87.3, where it is at most 2^-119 */
   MOE_ACT_GELU = 3,     /* z / 2 (1 + erf(z / sqrt 2)) */
   MOE_ACT_SWIGLU = 4    /* N = 2f: silu(z[:, 0:f]) * z[:, f:2f], f columns out */
 } moe_act;

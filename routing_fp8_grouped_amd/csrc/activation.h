@@ -11,12 +11,13 @@ enum Act { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActSwiglu = 
 __device__ __forceinline__ float exp_f32(float z) { return __builtin_amdgcn_exp2f(1.44269504088896341f * z); }
 
 // By the hardware's 2^x and reciprocal (an ulp each): within (4 + |z|) 2^-23 of
-// the exact value, where what it goes into is rounded to 16 bits.
+// the exact value, where what it goes into is rounded to 16 bits; 0 where it is
+// below 2^-126, from z = -87.3 on, where z times it is at most 2^-119.
 __device__ __forceinline__ float sigmoid_f32(float z) { return __builtin_amdgcn_rcpf(1.0f + exp_f32(-z)); }
 
 // Phi(z), the normal distribution's: for t = |z|, Phi(-t) = e^(-t^2/2) g(t) with
 // g(t) = e^(t^2/2) erfc(t / sqrt 2) / 2 smooth and falling, so a polynomial of
-// degree 8 in u = 1 / (1 + 0.23 t) is within 4.8e-8 of it (relative, t <= 14; a
+// degree 8 in u = 1 / (1 + 0.23 t) is within 5.8e-8 of it (relative, t <= 14; a
 // minimax fit made for this file; beyond, e^(-t^2/2) is 0).  No cancellation on
 // the side that vanishes; in FP32 the exponent's rounding leaves 1.3e-6 of Phi
 // for |z| < 6 and 4e-6 at 12.  15 operations where the library's erfc takes some

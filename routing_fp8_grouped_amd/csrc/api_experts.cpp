@@ -101,8 +101,7 @@ moe_status sum(moe_dtype type, const void* in, const int32_t* pos, const float* 
 
 // ---- products ----
 
-// Sizes that every product shares; `width`: the columns that have to be whole
-// 16-byte chunks besides N's own.
+// Sizes that every product shares; glu: N's halves have to be whole 16-byte chunks.
 moe_status check_product(int n_groups, int rows, int K, int N, bool glu) {
   REQUIRE(rows >= 0, "rows=%d is negative", rows);
   REQUIRE(n_groups >= 1, "n_groups=%d must be positive", n_groups);

@@ -400,8 +400,8 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void gemm16_kernel(Gemm16Args p) {
       // are out of the buffer's bounds, which drops them), so that the wait for the
       // next tile's first block can leave them in flight.  Rows of 512 bytes a
       // store, past the caches: 1.9 GB of gradients (8192 rows in 32 groups, 7168 x
-      // 2048) take 665 us against 745 with 128-byte rows from registers and 770
-      // through the caches.
+      // 2048) take 535 to 620 us over cards; on one where this took 665 it was 745
+      // with 128-byte rows from registers and 770 through the caches.
       const size_t row0 = WGRAD ? ((size_t)done.part * p.groups.n + done.g) * p.M : (size_t)done.part * p.groups.rows;
       const uint64_t base = reinterpret_cast<uint64_t>(static_cast<float*>(p.out) + (row0 + done.m0) * p.N);
       const __amdgpu_buffer_rsrc_t buffer = __builtin_amdgcn_make_buffer_rsrc(
@@ -621,11 +621,16 @@ struct RowTiles {
 // Parts of k for products whose tiles may be too few for the chip: the number
 // with the least time in us by what was measured: a block of 64 k takes 0.65 with
 // at most one 128 x 128 tile to a CU and 1.0 a round of two; joining takes 2.5 for
-// its launch and the parts' bytes, written and read, at 6 TB/s, or 3 where they are
-// more than 64 MB (both gradients of 8192 rows in 32 groups, K 2048, N 7168: 881 to
-// 965 us over cards, 1020 with the rows' in two parts of 67 MB).  (2048 x 2048 from
-// a sum over 16384: one part 194 us, two 149, four 160; 256 x 256 over 8192: 70, 42,
-// 26, 19 and 18.5 with 1 to 16; 6867 x 128 over 4088: 45, 28, 23, 25 and 35.)
+// its launch and the parts' bytes, written and read, at 6 TB/s (so measured from 17
+// to 400 MB of them).  Above 64 MB they are counted at 3: not the bytes are slower
+// there, but whole rounds overstate a partly filled last one, which one part has and
+// two have not.  640 tiles over a sum of 4096 are modelled as 128 us in one part and
+// 126 in two of 84 MB; they take 95 and 103.  Both gradients of 8192 rows in 32
+// groups, K 2048, N 7168, take 881 to 965 us over cards, 1020 with the rows' in two
+// parts of 134 MB together.  Between 64 MB and 84 the border is not measured.  (2048 x
+// 2048 from a sum over 16384: one part 194 us, two 149, four 160; 256 x 256 over
+// 8192: 70, 42, 26, 19 and 18.5 with 1 to 16; 6867 x 128 over 4088: 45, 28, 23, 25
+// and 35.)
 int parts_of(long t128, int k, double elements, double* time = nullptr) {
   int best = 1;
   double least = 0;
@@ -645,9 +650,10 @@ int parts_of(long t128, int k, double elements, double* time = nullptr) {
 }
 // The forward's: 0 where slim tiles take less time, 16 rows and fewer among them.
 // Both read the groups' weights, the slim tiles faster (128 rows in 64 groups, K
-// 7168, N 4096: 418 against 540 us).  Of 120 random products 114 take at most 8%
-// longer than the fastest of slim tiles and 1 to 16 parts (at sums of at most 30
-// GFLOP), the others 25%.
+// 7168, N 4096: 418 against 540 us); both are counted as reading them once, though
+// slim tiles read those of a group with several row tiles again.  Of 120 random
+// products of at most 30 GFLOP 114 take at most 8% longer than the fastest of slim
+// tiles and 1 to 16 parts, the others up to 25%; larger ones were not in that set.
 int forward_parts(const Gemm16Args& p) {
   double slim = gemm16_slim_time(p), tile;
   const long t128 = tiles_of(p.groups.rows, p.groups.n, p.N, 128, 128);

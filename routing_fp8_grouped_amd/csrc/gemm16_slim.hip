@@ -190,10 +190,12 @@ long slim_tiles(const Gemm16Args& p, int mb, int nb) {
 
 long average_rows(const Gemm16Args& p) { return (p.groups.rows + p.groups.n - 1) / p.groups.n; }
 
-// Tiles of 16 mb rows and 16 nb weight rows, and the us of a round of 256 workgroups:
-// about `fixed` for its start and join, `block` per 64 k.  128 rows, K 7168, N 4096
-// take 44, 32, 27 and 37 us as 2 x 1, 2 x 2, 2 x 4 and 4 x 4; 333 x 1000 x 1016 11.5,
-// 8.6, 8.0 and 11.1; 3468 rows, K 400, N 352 24, 14, 15 and 16.
+// Tiles of 16 mb rows and 16 nb weight rows, and the us of a round of 256 of them:
+// about `fixed` for its start and join, `block` per 64 k.  The first stands for two
+// workgroups of 1 x 1, which is what is launched (three of these fit a CU at a
+// time).  128 rows, K 7168, N 4096 take 44, 32, 27 and 37 us as 2 x 1, 2 x 2, 2 x 4
+// and 4 x 4; 333 x 1000 x 1016 11.5, 8.6, 8.0 and 11.1; 3468 rows, K 400, N 352 24,
+// 14, 15 and 16.
 struct SlimTile {
   int mb, nb;
   double fixed, block;
@@ -201,8 +203,11 @@ struct SlimTile {
 constexpr SlimTile kSlimTiles[] = {{1, 2, 1.1, 0.085}, {2, 1, 1.1, 0.08}, {2, 2, 0.8, 0.115},
                                    {2, 4, 1.8, 0.19},  {4, 2, 2.0, 0.2},  {4, 4, 2.3, 0.3}};
 
-// The tile by that time: up to 16 rows a group go to the first, whose weights pass
-// the caches.
+// The tile by that time, but up to 16 rows a group on average go to the first, whose
+// weights pass the caches, whatever the others would take: right where no group has
+// many more (128 rows in 64 groups of K 7168, N 4096: 418 us, all weights read once),
+// and slow where some do, since these read their weights again for every 16 rows (336
+// rows in 64 groups, K 3512, N 2272: 239 us; the weights' read alone is 145).
 int best_tile(const Gemm16Args& p, double& least) {
   const bool few = average_rows(p) <= 16;
   int best = 0;

@@ -1,6 +1,5 @@
 // Element types of the operators whose operands are not quantised (BF16, FP16,
-// FP32): 16-byte chunks of them, conversions, and the launch dispatch over
-// moe_dtype.
+// FP32): 16-byte chunks of them, and conversions.
 #pragma once
 
 #include <type_traits>
